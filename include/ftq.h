@@ -354,6 +354,142 @@ int ftq_moe_gguf_q8_1_partials(const void* w, int wtype, const void* a, const in
                                hipStream_t stream);
 
 /*
+ * ---- Routing to experts, and experts in 8-bit floating point -----------------
+ *
+ * The step before the expert matmul (the router's choice) and the same matmul
+ * for experts stored in 8-bit floating point with one fp32 scale per block of
+ * 128: OCP e4m3 codes (finite up to 448, NaN 0x7f/0xff), weights in 128 x 128
+ * blocks, activations in 1 x 128 blocks.  One expert FFN, every step a call:
+ *
+ *   ftq_moe_topk -> ftq_quantize_fp8 -> ftq_moe_fp8 (gate and up, act) ->
+ *   ftq_quantize_fp8 -> ftq_moe_fp8 (down, act_per_pair) -> ftq_moe_combine_topk
+ */
+
+/* Element types of the calls below. */
+typedef enum {
+    FTQ_F32 = 0,
+    FTQ_F16 = 1,
+    FTQ_BF16 = 2
+} ftq_dtype;
+
+typedef enum {
+    FTQ_SCORE_SOFTMAX = 0,    /* s = exp(l) / sum over the experts of exp(l) */
+    FTQ_SCORE_SIGMOID = 1     /* s = 1 / (1 + exp(-l)), each expert by itself */
+} ftq_score;
+
+#define FTQ_FP8_BLOCK 128
+
+/*
+ * Router: every token's top_k experts and their gate weights, in the layout
+ * the matmuls (topk_ids) and ftq_moe_combine_topk (gates) take.
+ *   logits   dtype [T][E], row t at element t*ld (ld >= E), aligned to its
+ *            element size.
+ *   bias     fp32 [E] or NULL: added to the scores for the choice alone (a
+ *            balance correction); finite.
+ *   topk_ids int32 [T][top_k], gates fp32 [T][top_k], 4-byte aligned, written.
+ * For one token, with s the scores of its logits:
+ *   c_e = s_e + bias_e; without bias the order of c is that of the logits.  An
+ *     expert whose logit (or bias) is -inf is not available.
+ *   n_group > 1: the experts form n_group runs of E/n_group; a run's score is
+ *     the sum of its group_top (1 or 2) largest c, unavailable ones counting as
+ *     -inf; only experts of the topk_group runs of largest score are chosen.
+ *   topk_ids = the top_k available experts of largest c, largest first.  Equal
+ *     values go to the lower expert or run.  If fewer are available, the rest of
+ *     the row is -1 (a masked pair for the matmuls) with gate 0.
+ *   gates_j = scale * s[topk_ids_j], with renorm divided by the sum of the
+ *     chosen s (0 if that sum is 0).
+ * The choice is the one 64-bit arithmetic makes; gates are computed in fp32 and
+ * are within a few units in the last place.  A row that holds a NaN (for
+ * softmax also +inf) has no scores: its ids are -1 and its gates NaN.  Rows are
+ * independent: a row's results depend on no other row.
+ * Limits: 1 <= E <= 1024, 1 <= top_k <= 64 (FTQ_ERR_UNSUPPORTED above), n_group
+ * >= 1 divides E, n_group <= 64 (FTQ_ERR_UNSUPPORTED above), 1 <= topk_group <=
+ * n_group, 1 <= group_top <= min(2, E/n_group), top_k <= topk_group*E/n_group, T >= 0
+ * (T == 0: no-op).  Other values: FTQ_ERR_INVALID_ARG.
+ */
+int ftq_moe_topk(const void* logits, int dtype, int64_t ld, const float* bias, int32_t* topk_ids, float* gates,
+                 int64_t T, int64_t E, int64_t top_k, int score, int64_t n_group, int64_t topk_group, int group_top,
+                 int renorm, float scale, hipStream_t stream);
+
+/*
+ * Quantise activations to e4m3 with one fp32 scale per row and 128 columns.
+ *   x       dtype [T][K], row t at element t*ld; x and ld*sizeof(element) are
+ *           multiples of 16 bytes.  K % 16 == 0, ld >= K, T >= 0.
+ *   y       [T][K] codes, 16-byte aligned, written.
+ *   scales  fp32 [T][ceil(K/128)], 4-byte aligned, written.
+ * Per block (the last one of a row may be shorter): scale = max|x| / 448 (fp32,
+ * IEEE division), code = e4m3(x / scale) (fp32 IEEE division, then round to
+ * nearest even, saturated at 448); codes 0 when scale is 0.  A block that holds
+ * a NaN has a NaN scale and NaN codes; one that holds an infinity has an infinite
+ * scale, NaN codes at the infinities and zeros elsewhere: either way every
+ * product with the block is NaN.  Bit-exact and deterministic.
+ */
+int ftq_quantize_fp8(const void* x, int dtype, int64_t ld, int64_t T, int64_t K, void* y, float* scales,
+                     hipStream_t stream);
+
+/*
+ * Quantise expert weights to e4m3 with one fp32 scale per 128 x 128 block (weight
+ * preparation; checkpoints that hold such codes and scales need no call).
+ *   w       dtype [E][N][K], 16-byte aligned.  K % 16 == 0.
+ *   y       [E][N][K] codes, 16-byte aligned, written.
+ *   scales  fp32 [E][ceil(N/128)][ceil(K/128)], 4-byte aligned, written.
+ * The blocks of an expert start at its row 0; blocks at the ends of N and K may
+ * be smaller.  Scale and codes as in ftq_quantize_fp8, over the block.
+ */
+int ftq_quantize_fp8_weight(const void* w, int dtype, int64_t E, int64_t N, int64_t K, void* y, float* scales,
+                            hipStream_t stream);
+
+/*
+ * The expert matmul on such weights and activations.  For pair p = t*top_k + j,
+ * e = topk_ids[t][j], activation row r = t (act_per_pair == 0) or p:
+ *
+ *   y[p][n] = sum over blocks b of  P[p][n][b] * (a_scale[r][b] * w_scale[e][n/128][b])
+ *   P[p][n][b] = sum over i in block b of  w[e][n][i] * a[r][i]
+ *
+ * The sum over blocks is held in fp32.  P is an fp32 sum of exact products, with
+ * one exception: for 16-bit out the grouped path leaves P to the matrix units'
+ * 8-bit instructions, which drop bits below 2^-13 of the largest of every eight
+ * products (about 1.5e-5 of a result's norm on normal values, a hundredth of what
+ * rounding to bf16 costs).  act == 0: out[p][n] = y[p][n],
+ * N columns; act FTQ_ACT_*: out[p][c] = act(y[p][c]) * y[p][N/2 + c], N/2 columns
+ * (gate rows, then up rows, as ftq_moe_q4_0_q8_1_act).
+ *   w        [E][N][K] e4m3 codes, 16-byte aligned; w_scale fp32
+ *            [E][ceil(N/128)][ceil(K/128)], 4-byte aligned.
+ *   a        [T or T*top_k][K] e4m3 codes, 16-byte aligned; a_scale fp32
+ *            [T or T*top_k][ceil(K/128)], 4-byte aligned.
+ *   topk_ids int32 [T][top_k]; ids outside [0, E) give zero rows.
+ *   out      out_dtype [T*top_k][N or N/2], aligned to its element size; the fp32
+ *            sum is rounded once to out_dtype.
+ *   workspace, path: as ftq_moe_q4_0_q8_1, with ftq_moe_fp8_workspace_bytes
+ *            and ftq_moe_fp8_select_path in place of that call's.
+ * A row's bits depend neither on the other rows nor on the batch size while the
+ * path is the same.  A NaN code or scale reaches only the results it is a term of.
+ * Limits: K % 16 == 0; with act, N % 32 == 0 (FTQ_ERR_UNSUPPORTED otherwise;
+ * odd N: FTQ_ERR_INVALID_ARG); FTQ_PATH_GEMV takes at most 4096 pairs
+ * (FTQ_ERR_UNSUPPORTED above); E, N, T, top_k as ftq_moe_q4_0_q8_1.
+ *
+ * ftq_moe_fp8_route and ftq_moe_fp8_routed are the two halves of the call, as
+ * ftq_moe_route and ftq_moe_q4_0_q8_1_routed are (the tables differ, so that
+ * each matmul wants its own route call): one routing serves every ftq_moe_fp8
+ * matmul over the same topk_ids, E, T, top_k, path and workspace.
+ */
+int ftq_moe_fp8_select_path(int64_t E, int64_t N, int64_t K, int64_t T, int64_t top_k);
+
+int64_t ftq_moe_fp8_workspace_bytes(int64_t E, int64_t N, int64_t K, int64_t T, int64_t top_k, int path);
+
+int ftq_moe_fp8(const void* w, const float* w_scale, const void* a, const float* a_scale, const int32_t* topk_ids,
+                void* out, int out_dtype, int64_t E, int64_t N, int64_t K, int64_t T, int64_t top_k,
+                int act_per_pair, int act, void* workspace, size_t workspace_bytes, int path, hipStream_t stream);
+
+int ftq_moe_fp8_route(const int32_t* topk_ids, int64_t E, int64_t T, int64_t top_k, void* workspace,
+                      size_t workspace_bytes, int path, hipStream_t stream);
+
+int ftq_moe_fp8_routed(const void* w, const float* w_scale, const void* a, const float* a_scale,
+                       const int32_t* topk_ids, void* out, int out_dtype, int64_t E, int64_t N, int64_t K, int64_t T,
+                       int64_t top_k, int act_per_pair, int act, void* workspace, size_t workspace_bytes, int path,
+                       hipStream_t stream);
+
+/*
  * Message for the last failing call on this thread ("" if none): for a
  * rejected launch it names the kernel, grid, block and LDS bytes and the HIP
  * error (FreeToken PR #185, Fix: report the geometry of a failed launch).  The

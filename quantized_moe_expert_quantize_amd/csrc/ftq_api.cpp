@@ -222,6 +222,86 @@ int64_t workspace_bytes(int64_t E, int64_t N, int64_t K, int64_t T, int64_t top_
     return plan.bytes;
 }
 
+int64_t dtype_bytes(int dtype) { return dtype == FTQ_F32 ? 4 : (dtype == FTQ_F16 || dtype == FTQ_BF16) ? 2 : 0; }
+
+// A [rows][K] array of `dtype` for the 8-bit floating-point quantisers: whole
+// 16-byte runs of codes per row, offsets that fit int64.
+int check_quantize_fp8(int dtype, int64_t rows, int64_t K, int64_t ld)
+{
+    if (!dtype_bytes(dtype)) { set_error("unknown element type %d", dtype); return FTQ_ERR_INVALID_ARG; }
+    if (K <= 0 || K % 16 != 0) { set_error("K must be a positive multiple of 16 (got %lld)", (long long)K); return FTQ_ERR_INVALID_ARG; }
+    if (rows < 0 || ld < K || ld > INT64_MAX / 16 || (ld * dtype_bytes(dtype)) % 16 != 0) {
+        set_error("need rows >= 0 and a row stride of at least K elements and whole 16-byte units (got %lld rows, stride %lld)",
+                  (long long)rows, (long long)ld);
+        return FTQ_ERR_INVALID_ARG;
+    }
+    if (rows > INT64_MAX / 8 / ld) { set_error("tensor sizes overflow 64-bit byte offsets"); return FTQ_ERR_UNSUPPORTED; }
+    return FTQ_OK;
+}
+
+// K of the 8-bit floating-point matmul is a multiple of 16, not of 32: the
+// shared size rules are applied to K rounded up.
+int check_sizes_fp8(int64_t E, int64_t N, int64_t K, int64_t T, int64_t top_k)
+{
+    if (K <= 0 || K % 16 != 0) { set_error("K must be a positive multiple of 16 (got %lld)", (long long)K); return FTQ_ERR_INVALID_ARG; }
+    if (K > INT64_MAX / 64) { set_error("tensor sizes overflow 64-bit byte offsets"); return FTQ_ERR_UNSUPPORTED; }
+    const int st = check_sizes(E, N, (K + 31) / 32 * 32, T, top_k);
+    if (st != FTQ_OK) return st;
+    if (T > 0 && K > INT64_MAX / 64 / (T * top_k)) { set_error("tensor sizes overflow 64-bit byte offsets"); return FTQ_ERR_UNSUPPORTED; }
+    return FTQ_OK;
+}
+
+int resolve_path_fp8(int path, int64_t E, int64_t T, int64_t top_k)
+{
+    if (path == FTQ_PATH_AUTO) return fp8_select_path(E, T, top_k);
+    if (path == FTQ_PATH_GEMV || path == FTQ_PATH_GROUPED) return path;
+    return -1;
+}
+
+int fp8_common(const Fp8Args& m, bool per_pair, void* ws, size_t ws_bytes, int path, hipStream_t stream, int phases)
+{
+    clear_error();
+    int st = check_sizes_fp8(m.E, m.N, m.K, m.T, m.top_k);
+    if (st != FTQ_OK) return st;
+    if (phases & kMatmul) {
+        if (!dtype_bytes(m.out_dtype)) { set_error("unknown element type %d", m.out_dtype); return FTQ_ERR_INVALID_ARG; }
+        if (m.act != 0) {
+            if (m.act != FTQ_ACT_SILU && m.act != FTQ_ACT_GELU_TANH) { set_error("unknown activation %d", m.act); return FTQ_ERR_INVALID_ARG; }
+            if (m.N % 2 != 0) { set_error("a gated activation needs an even N (gate and up halves), got %lld", (long long)m.N); return FTQ_ERR_INVALID_ARG; }
+            if (m.N % 32 != 0) { set_error("a gated activation needs N %% 32 == 0 here, got %lld", (long long)m.N); return FTQ_ERR_UNSUPPORTED; }
+        }
+    }
+    const int rp = resolve_path_fp8(path, m.E, m.T, m.top_k);
+    if (rp < 0) { set_error("unknown path %d", path); return FTQ_ERR_INVALID_ARG; }
+    const int64_t pairs = m.T * m.top_k;
+    if (rp == FTQ_PATH_GEMV && pairs > kFp8GemvMaxPairs) {
+        set_error("the GEMV path takes at most %lld pairs (got %lld)", (long long)kFp8GemvMaxPairs, (long long)pairs);
+        return FTQ_ERR_UNSUPPORTED;
+    }
+    if (m.T == 0) return FTQ_OK;
+    if (!m.ids || ((phases & kMatmul) && (!m.w || !m.w_scale || !m.a || !m.a_scale || !m.out))) {
+        set_error("null pointer argument (w, w_scale, a, a_scale, topk_ids or out)");
+        return FTQ_ERR_INVALID_ARG;
+    }
+    if (!aligned(m.ids, 4) || ((phases & kMatmul) &&
+        (!aligned(m.w, 16) || !aligned(m.w_scale, 4) || !aligned(m.a, 16) || !aligned(m.a_scale, 4) ||
+         !aligned(m.out, dtype_bytes(m.out_dtype))))) {
+        set_error("misaligned pointer (w and a need 16-byte, scales and topk_ids 4-byte, out its element's alignment)");
+        return FTQ_ERR_INVALID_ARG;
+    }
+    Fp8Args args = m;
+    args.act_div = per_pair ? 1 : m.top_k;
+    if (rp == FTQ_PATH_GEMV) return (phases & kMatmul) ? run_fp8_gemv(args, stream) : FTQ_OK;
+    const BucketPlan plan = make_bucket_plan(pairs, m.E, fp8_tile_m(m.E, m.T, m.top_k));
+    st = check_workspace(plan.bytes, ws, ws_bytes);
+    if (st != FTQ_OK) return st;
+    if (phases & kRoute) {
+        st = run_bucket(m.ids, m.E, plan, ws, stream);
+        if (st != FTQ_OK) return st;
+    }
+    return (phases & kMatmul) ? run_fp8_grouped(args, plan, ws, stream) : FTQ_OK;
+}
+
 }  // namespace
 
 int moe_q4_0_q8_1_call(const void* w, const void* a, const int32_t* ids, float* out, int64_t E, int64_t N, int64_t K,
@@ -400,6 +480,113 @@ int ftq_moe_gguf_q8_1_partials(const void* w, int wtype, const void* a, const in
 {
     return moe_common(w, a, topk_ids, nullptr, partials, E, N, K, T, top_k, workspace, workspace_bytes, path, stream,
                       kRoute | kMatmul, act_per_pair != 0, 0, wtype);
+}
+
+int ftq_moe_topk(const void* logits, int dtype, int64_t ld, const float* bias, int32_t* topk_ids, float* gates,
+                 int64_t T, int64_t E, int64_t top_k, int score, int64_t n_group, int64_t topk_group, int group_top,
+                 int renorm, float scale, hipStream_t stream)
+{
+    clear_error();
+    const int64_t esz = dtype_bytes(dtype);
+    if (!esz) { set_error("unknown element type %d", dtype); return FTQ_ERR_INVALID_ARG; }
+    if (score != FTQ_SCORE_SOFTMAX && score != FTQ_SCORE_SIGMOID) { set_error("unknown score function %d", score); return FTQ_ERR_INVALID_ARG; }
+    if (T < 0 || E < 1 || top_k < 1 || ld < E) {
+        set_error("need T >= 0, E >= 1, top_k >= 1, ld >= E (got T=%lld E=%lld top_k=%lld ld=%lld)", (long long)T,
+                  (long long)E, (long long)top_k, (long long)ld);
+        return FTQ_ERR_INVALID_ARG;
+    }
+    if (n_group < 1 || E % n_group != 0 || topk_group < 1 || topk_group > n_group || group_top < 1 ||
+        group_top > 2 || group_top > E / n_group || top_k > topk_group * (E / n_group)) {
+        set_error("n_group=%lld topk_group=%lld group_top=%d top_k=%lld do not fit %lld experts", (long long)n_group,
+                  (long long)topk_group, group_top, (long long)top_k, (long long)E);
+        return FTQ_ERR_INVALID_ARG;
+    }
+    if (E > kTopkMaxExperts || top_k > kTopkMaxK || n_group > kTopkMaxGroups) {
+        set_error("the router takes at most %lld experts, %lld choices and %lld groups (got %lld, %lld, %lld)",
+                  (long long)kTopkMaxExperts, (long long)kTopkMaxK, (long long)kTopkMaxGroups, (long long)E,
+                  (long long)top_k, (long long)n_group);
+        return FTQ_ERR_UNSUPPORTED;
+    }
+    if (ld > INT64_MAX / 16 || T > INT64_MAX / 16 / ld) { set_error("T*ld overflows 64-bit byte offsets"); return FTQ_ERR_UNSUPPORTED; }
+    if (T == 0) return FTQ_OK;
+    if (!logits || !topk_ids || !gates) { set_error("null pointer argument (logits, topk_ids or gates)"); return FTQ_ERR_INVALID_ARG; }
+    if (!aligned(logits, esz) || !aligned(topk_ids, 4) || !aligned(gates, 4) || (bias && !aligned(bias, 4))) {
+        set_error("misaligned pointer (logits need their element's alignment, bias, topk_ids and gates 4-byte alignment)");
+        return FTQ_ERR_INVALID_ARG;
+    }
+    const TopkArgs m{logits, bias, topk_ids, gates, T, ld, dtype, (int32_t)E, (int32_t)top_k, score, (int32_t)n_group,
+                     (int32_t)topk_group, group_top, renorm != 0, scale};
+    return run_topk(m, stream);
+}
+
+int ftq_quantize_fp8(const void* x, int dtype, int64_t ld, int64_t T, int64_t K, void* y, float* scales,
+                     hipStream_t stream)
+{
+    clear_error();
+    int st = check_quantize_fp8(dtype, T, K, ld);
+    if (st != FTQ_OK) return st;
+    if (T == 0) return FTQ_OK;
+    if (!x || !y || !scales) { set_error("null pointer argument (x, y or scales)"); return FTQ_ERR_INVALID_ARG; }
+    if (!aligned(x, 16) || !aligned(y, 16) || !aligned(scales, 4)) { set_error("misaligned pointer (x and y need 16-byte, scales 4-byte alignment)"); return FTQ_ERR_INVALID_ARG; }
+    return run_quantize_fp8(x, dtype, ld, T, K, y, scales, stream);
+}
+
+int ftq_quantize_fp8_weight(const void* w, int dtype, int64_t E, int64_t N, int64_t K, void* y, float* scales,
+                            hipStream_t stream)
+{
+    clear_error();
+    if (E < 0 || N < 0 || (N > 0 && E > INT64_MAX / N)) { set_error("need E >= 0 and N >= 0 (got E=%lld N=%lld)", (long long)E, (long long)N); return FTQ_ERR_INVALID_ARG; }
+    int st = check_quantize_fp8(dtype, E * N, K, K);
+    if (st != FTQ_OK) return st;
+    if (E * N == 0) return FTQ_OK;
+    if (!w || !y || !scales) { set_error("null pointer argument (w, y or scales)"); return FTQ_ERR_INVALID_ARG; }
+    if (!aligned(w, 16) || !aligned(y, 16) || !aligned(scales, 4)) { set_error("misaligned pointer (w and y need 16-byte, scales 4-byte alignment)"); return FTQ_ERR_INVALID_ARG; }
+    return run_quantize_fp8_weight(w, dtype, E, N, K, y, scales, stream);
+}
+
+int ftq_moe_fp8_select_path(int64_t E, int64_t N, int64_t K, int64_t T, int64_t top_k)
+{
+    clear_error();
+    int st = check_sizes_fp8(E, N, K, T, top_k);
+    if (st != FTQ_OK) return -st;
+    return fp8_select_path(E, T, top_k);
+}
+
+int64_t ftq_moe_fp8_workspace_bytes(int64_t E, int64_t N, int64_t K, int64_t T, int64_t top_k, int path)
+{
+    clear_error();
+    if (check_sizes_fp8(E, N, K, T, top_k) != FTQ_OK) return -1;
+    const int rp = resolve_path_fp8(path, E, T, top_k);
+    if (rp < 0) { set_error("unknown path %d", path); return -1; }
+    if (T == 0 || rp == FTQ_PATH_GEMV) return 0;
+    return make_bucket_plan(T * top_k, E, fp8_tile_m(E, T, top_k)).bytes;
+}
+
+int ftq_moe_fp8(const void* w, const float* w_scale, const void* a, const float* a_scale, const int32_t* topk_ids,
+                void* out, int out_dtype, int64_t E, int64_t N, int64_t K, int64_t T, int64_t top_k,
+                int act_per_pair, int act, void* workspace, size_t workspace_bytes, int path, hipStream_t stream)
+{
+    const Fp8Args m{static_cast<const uint8_t*>(w), w_scale, static_cast<const uint8_t*>(a), a_scale, topk_ids, out,
+                    E, N, K, T, top_k, 0, act, out_dtype};
+    return fp8_common(m, act_per_pair != 0, workspace, workspace_bytes, path, stream, kRoute | kMatmul);
+}
+
+int ftq_moe_fp8_route(const int32_t* topk_ids, int64_t E, int64_t T, int64_t top_k, void* workspace,
+                      size_t workspace_bytes, int path, hipStream_t stream)
+{
+    // N and K do not enter the routing; any valid values pass the size checks
+    const Fp8Args m{nullptr, nullptr, nullptr, nullptr, topk_ids, nullptr, E, 1, kFp8Block, T, top_k, 0, 0, FTQ_F32};
+    return fp8_common(m, false, workspace, workspace_bytes, path, stream, kRoute);
+}
+
+int ftq_moe_fp8_routed(const void* w, const float* w_scale, const void* a, const float* a_scale,
+                       const int32_t* topk_ids, void* out, int out_dtype, int64_t E, int64_t N, int64_t K, int64_t T,
+                       int64_t top_k, int act_per_pair, int act, void* workspace, size_t workspace_bytes, int path,
+                       hipStream_t stream)
+{
+    const Fp8Args m{static_cast<const uint8_t*>(w), w_scale, static_cast<const uint8_t*>(a), a_scale, topk_ids, out,
+                    E, N, K, T, top_k, 0, act, out_dtype};
+    return fp8_common(m, act_per_pair != 0, workspace, workspace_bytes, path, stream, kMatmul);
 }
 
 const char* ftq_last_error(void) { return g_error.c_str(); }

@@ -165,4 +165,51 @@ int64_t moe_workspace_need(int64_t E, int64_t N, int64_t K, int64_t T, int64_t t
 int run_combine_topk(const float* y, const float* gates, float* out, int64_t T, int64_t top_k, int64_t N,
                      hipStream_t s);
 
+// Router (topk.hip).
+struct TopkArgs {
+    const void* logits;
+    const float* bias;
+    int32_t* ids;
+    float* gates;
+    int64_t T, ld;
+    int dtype;
+    int32_t E, top_k, score, n_group, topk_group, group_top, renorm;
+    float scale;
+};
+constexpr int64_t kTopkMaxExperts = 1024;
+constexpr int64_t kTopkMaxK = 64;          // one lane of a wave per chosen expert
+constexpr int64_t kTopkMaxGroups = 64;     // one lane per group
+int run_topk(const TopkArgs& m, hipStream_t s);
+
+// 8-bit floating-point quantisers (fp8_quantize.hip).
+constexpr int kFp8Block = 128;
+int run_quantize_fp8(const void* x, int dtype, int64_t ld, int64_t T, int64_t K, void* y, float* scales, hipStream_t s);
+int run_quantize_fp8_weight(const void* w, int dtype, int64_t E, int64_t N, int64_t K, void* y, float* scales,
+                            hipStream_t s);
+
+// 8-bit floating-point expert matmul (moe_fp8.hip).
+struct Fp8Args {
+    const uint8_t* w;
+    const float* w_scale;
+    const uint8_t* a;
+    const float* a_scale;
+    const int32_t* ids;
+    void* out;
+    int64_t E, N, K, T, top_k;
+    int64_t act_div;       // activation row of pair p: p / act_div (top_k: per token; 1: per pair)
+    int act;               // 0: N columns; FTQ_ACT_*: N/2
+    int out_dtype;
+};
+constexpr int64_t kFp8GemvMaxPairs = 4096;   // the GEMV path finds an expert's pairs by scanning the ids
+int fp8_select_path(int64_t E, int64_t T, int64_t top_k);
+int64_t fp8_tile_m(int64_t E, int64_t T, int64_t top_k);
+int run_fp8_gemv(const Fp8Args& m, hipStream_t s);
+int run_fp8_grouped(const Fp8Args& m, const BucketPlan& plan, const void* ws, hipStream_t s);
+
+// Element conversions of the FTQ_F32 / FTQ_F16 / FTQ_BF16 types (bits of a 16-bit value; round to nearest even).
+__device__ __forceinline__ float f32_of_f16(uint16_t h) { return (float)__builtin_bit_cast(_Float16, h); }
+__device__ __forceinline__ float f32_of_bf16(uint16_t h) { return __builtin_bit_cast(float, (uint32_t)h << 16); }
+__device__ __forceinline__ uint16_t f16_of_f32(float f) { return __builtin_bit_cast(uint16_t, (_Float16)f); }
+__device__ __forceinline__ uint16_t bf16_of_f32(float f) { return __builtin_bit_cast(uint16_t, (__bf16)f); }
+
 }  // namespace ftq

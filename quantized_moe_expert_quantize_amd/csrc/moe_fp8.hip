@@ -1,0 +1,412 @@
+// The expert matmul on 8-bit floating-point (e4m3) weights and activations with
+// one fp32 scale per 128 x 128 block of the weights and per 128 values of an
+// activation row.  For pair p of expert e with activation row r:
+//
+//   y[p][n] = sum_b P_b * (a_scale[r][b] * w_scale[e][n/128][b]),
+//   P_b     = sum over the 128 values of block b of w[e][n][.] * a[r][.]
+//
+// P_b of 16 weight rows x 16 activation rows is made on the matrix units from a
+// zero accumulator, and one fp32 FMA per element and block adds it, scaled, to
+// the sum.  The weights are the instructions' left operand, so that a lane holds
+// four weight rows of ONE activation row: its scale is one value a lane, and its
+// results four consecutive outputs.  Operand layout: lane l holds row l%16 of
+// its side, and as k the 16-byte runs l/16 and l/16 + 4 of the block.  (The
+// instructions' own order of k within the block does not matter while both sides
+// use the same.)
+//
+// Two forms of P_b:
+//   exact  the codes are converted to fp16, which holds every e4m3 value, and
+//          multiplied by four v_mfma_f32_16x16x32_f16: exact products, fp32 sums
+//          (measured 1e-8 relative to the result's norm on normal values).
+//   fast   one v_mfma_f32_16x16x128_f8f6f4, twice the rate and no conversion.
+//          It aligns each run of eight products to the largest one's exponent and
+//          drops bits below 2^-13 of it (measured: 1.5e-5 relative to the result's
+//          norm, 1.1e-5 of the sum of the terms' magnitudes at most).
+// fp32 results take the exact form.  fp16 and bf16 results of the grouped path
+// take the fast one: what it drops is a hundredth of their own rounding (2^-9,
+// 2^-12).  The GEMV, which waits for memory, takes the exact form always.
+//
+// Two kernels: the GEMV splits K over the waves of a workgroup and reads each
+// weight once for up to a few dozen pairs of its expert; the grouped one walks
+// expert-sorted tiles (bucket.hip) with the activations staged in LDS.
+#include "ftq_internal.h"
+
+namespace ftq {
+namespace {
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+
+// One lane's 32 codes of a block, as the matrix instructions of a form take them.
+template <bool EXACT> struct Operand;
+template <> struct Operand<false> {
+    i32x8 v;
+    __device__ __forceinline__ explicit Operand(i32x8 codes) : v(codes) {}
+    __device__ __forceinline__ Operand() {}
+};
+template <> struct Operand<true> {
+    f16x8 v[4];
+    __device__ __forceinline__ Operand() {}
+    __device__ __forceinline__ explicit Operand(i32x8 codes)
+    {
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+#pragma unroll
+            for (int d = 0; d < 2; ++d) {
+                const int c = codes[2 * h + d];
+                const f16x2 lo = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c, 1.0f, false);
+                const f16x2 hi = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c, 1.0f, true);
+                v[h][4 * d] = lo[0];
+                v[h][4 * d + 1] = lo[1];
+                v[h][4 * d + 2] = hi[0];
+                v[h][4 * d + 3] = hi[1];
+            }
+        }
+    }
+};
+
+// P_b of NW weight tiles with one activation tile.
+template <int NW>
+__device__ __forceinline__ void block_products(const Operand<false> (&w)[NW], const Operand<false>& a, f32x4 (&p)[NW])
+{
+    const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < NW; ++i) p[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w[i].v, a.v, zero, 0, 0, 0, 0, 0, 0);
+}
+template <int NW>
+__device__ __forceinline__ void block_products(const Operand<true> (&w)[NW], const Operand<true>& a, f32x4 (&p)[NW])
+{
+    const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+#pragma unroll
+        for (int i = 0; i < NW; ++i) p[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w[i].v[h], a.v[h], h == 0 ? zero : p[i], 0, 0, 0);
+    }
+}
+
+__device__ __forceinline__ i32x8 join(i32x4 lo, i32x4 hi) { return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7); }
+
+// This lane's two 16-byte runs of block kb of a row of K codes, zeros past K.
+__device__ __forceinline__ i32x8 load_block(const uint8_t* row, int64_t kb, int64_t K, int run)
+{
+    const int64_t k0 = kb * kFp8Block + run * 16, k1 = k0 + 64;
+    i32x4 lo = {0, 0, 0, 0}, hi = {0, 0, 0, 0};
+    if (k0 < K) lo = *reinterpret_cast<const i32x4*>(row + k0);
+    if (k1 < K) hi = *reinterpret_cast<const i32x4*>(row + k1);
+    return join(lo, hi);
+}
+
+template <int OUT>
+__device__ __forceinline__ void store1(void* out, int64_t i, float v)
+{
+    if constexpr (OUT == FTQ_F32) static_cast<float*>(out)[i] = v;
+    else static_cast<uint16_t*>(out)[i] = OUT == FTQ_F16 ? f16_of_f32(v) : bf16_of_f32(v);
+}
+
+__device__ __forceinline__ bool expert_ok(int32_t id, int64_t E) { return id >= 0 && id < E; }
+
+// ---- GEMV ---------------------------------------------------------------------
+
+constexpr int kGemvWaves = 8;
+constexpr int kGemvThreads = 64 * kGemvWaves;
+
+// A workgroup takes 16 output columns of one expert: one 16-row weight tile, or
+// with ACT the gate and the up tile of the columns.  by_pair: workgroups are laid
+// out over the pairs, and the one of an expert's first pair serves all its
+// pairs (few pairs: no workgroup for an expert that none takes); else over the
+// experts and, last, the masked pairs.
+template <int OUT, bool ACT>
+__global__ __launch_bounds__(kGemvThreads) void moe_fp8_gemv_kernel(Fp8Args m, int64_t nb, int64_t nr, int64_t ntiles,
+                                                                    int by_pair)
+{
+    constexpr int RT = ACT ? 2 : 1;
+    __shared__ uint16_t list[kFp8GemvMaxPairs];
+    __shared__ int count_lds;
+    __shared__ f32x4 part[kGemvWaves][RT][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t slot = blockIdx.x / ntiles, n0 = (blockIdx.x - slot * ntiles) * 16;
+    const int pairs = (int)(m.T * m.top_k);
+    const int64_t cols = ACT ? m.N / 2 : m.N;
+    const int32_t e = by_pair ? m.ids[slot] : slot < m.E ? (int32_t)slot : -1;
+    const bool live = expert_ok(e, m.E);
+    // the pairs of this expert (or the masked ones), ascending
+    if (wave == 0) {
+        int count = 0;
+        for (int p0 = 0; p0 < pairs; p0 += 64) {
+            const int p = p0 + lane;
+            const int32_t id = p < pairs ? m.ids[p] : 0;
+            const bool mine = p < pairs && (live ? id == e : by_pair ? p == (int)slot : !expert_ok(id, m.E));
+            const uint64_t vote = __ballot(mine);
+            if (mine) list[count + __popcll(vote & ((1ull << lane) - 1))] = (uint16_t)p;
+            count += __popcll(vote);
+        }
+        if (lane == 0) count_lds = count;
+    }
+    __syncthreads();
+    const int count = count_lds;
+    if (count == 0 || (by_pair && list[0] != slot)) return;
+    if (!live) {
+        for (int i = threadIdx.x; i < count * 16; i += kGemvThreads) {
+            if (n0 + i % 16 < cols) store1<OUT>(m.out, list[i / 16] * cols + n0 + i % 16, 0.0f);
+        }
+        return;
+    }
+    const int r = lane & 15, run = lane >> 4;
+    const uint8_t* wrow[RT];
+    const float* wscale[RT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+        const int64_t n = min(n0 + r, cols - 1) + i * cols;
+        wrow[i] = m.w + ((int64_t)e * m.N + n) * m.K;
+        // this lane's results are rows 4*run .. 4*run+3: one scale, since tiles of 16 start at multiples of 16
+        wscale[i] = m.w_scale + ((int64_t)e * nr + (min(n0, cols - 1) + i * cols) / kFp8Block) * nb;
+    }
+    for (int t0 = 0; t0 < count; t0 += 16) {
+        const bool have = t0 + r < count;
+        const int64_t arow = have ? list[t0 + r] / m.act_div : 0;
+        f32x4 acc[RT] = {};
+        for (int64_t kb = wave; kb < nb; kb += kGemvWaves) {
+            i32x8 a = {};
+            float sa = 0.0f;
+            if (have) {
+                a = load_block(m.a + arow * m.K, kb, m.K, run);
+                sa = m.a_scale[arow * nb + kb];
+            }
+            Operand<true> w[RT];
+            f32x4 p[RT];
+#pragma unroll
+            for (int i = 0; i < RT; ++i) w[i] = Operand<true>(load_block(wrow[i], kb, m.K, run));
+            block_products(w, Operand<true>(a), p);
+#pragma unroll
+            for (int i = 0; i < RT; ++i) {
+                const float s = sa * wscale[i][kb];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) acc[i][q] = __builtin_fmaf(p[i][q], s, acc[i][q]);
+            }
+        }
+        __syncthreads();   // the last pass has read part[]
+#pragma unroll
+        for (int i = 0; i < RT; ++i) part[wave][i][lane] = acc[i];
+        __syncthreads();
+        if (threadIdx.x < 256) {
+            // thread h: column h%16 of activation row h/16 of this pass, its parts in wave order
+            const int c = threadIdx.x % 16, t = threadIdx.x / 16;
+            float y[RT];
+#pragma unroll
+            for (int i = 0; i < RT; ++i) {
+                y[i] = 0.0f;
+#pragma unroll
+                for (int v = 0; v < kGemvWaves; ++v) y[i] += part[v][i][(c / 4) * 16 + t][c % 4];
+            }
+            if (t0 + t < count && n0 + c < cols) {
+                float v = y[0];
+                if constexpr (ACT) v = gated_act(m.act, y[0]) * y[RT - 1];
+                store1<OUT>(m.out, list[t0 + t] * cols + n0 + c, v);
+            }
+        }
+    }
+}
+
+// ---- grouped ------------------------------------------------------------------
+
+constexpr int kWaves = 4;
+constexpr int kThreads = 64 * kWaves;
+constexpr int kRowsPerWave = 64;                       // weight rows: four 16-row tiles
+
+struct GroupedTables {
+    const int32_t* tiles;     // [E + 2] first tile of each bucket; the last entry is their number
+    const int32_t* sorted;    // pair ids by expert
+    const int4* tdesc;        // per tile {bucket, first slot, rows, 0}
+    int64_t nb, nr, ntn;      // K blocks, weight row blocks per expert, column tiles
+};
+
+// A workgroup makes 16*TT pairs x 256 weight rows; wave v has 64 rows of them and
+// all the pairs, so each weight is read by one wave only, straight into
+// registers, and the activations, which every wave needs, go through LDS.
+// Within a wave, row r of weight tile i is row 16*(r/4) + 4*i + r%4 of its 64,
+// so that a lane's results over the four tiles are 16 consecutive columns.  With
+// ACT the wave has 32 columns, tiles 0 and 1 their gate and 2 and 3 their up
+// rows, and a lane 8 consecutive columns.
+template <int TT, int OUT, bool ACT>
+__global__ __launch_bounds__(kThreads) void moe_fp8_grouped_kernel(Fp8Args m, GroupedTables g)
+{
+    constexpr bool kExact = OUT == FTQ_F32;
+    constexpr int BM = 16 * TT;
+    constexpr int kRuns = BM * 8 / kThreads;           // 16-byte runs of an activation tile per thread
+    constexpr int kCols = ACT ? 32 : 64;               // output columns per wave
+    constexpr int kLaneCols = kCols / 4;               // consecutive columns per lane
+    constexpr int kScales = ACT ? 2 : 1;               // weight scales per lane and block
+    __shared__ i32x4 act[2][BM][8];                    // run c of row x sits at c ^ (x % 8)
+    __shared__ float act_scale[2][BM];
+    __shared__ int32_t pair_of[BM];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int r = lane & 15, run = lane >> 4;
+    const int64_t cols = ACT ? m.N / 2 : m.N;
+    const int64_t total = (int64_t)g.tiles[m.E + 1] * g.ntn;
+    for (int64_t item = blockIdx.x; item < total; item += gridDim.x) {
+        const int64_t mt = item / g.ntn, c0 = (item - mt * g.ntn) * (kWaves * kCols) + wave * kCols;
+        const int4 desc = g.tdesc[mt];
+        const int rows = desc.z;
+        __syncthreads();                               // the last item's LDS has been read
+        if (threadIdx.x < BM) pair_of[threadIdx.x] = g.sorted[desc.y + min((int)threadIdx.x, rows - 1)];
+        __syncthreads();
+        if (desc.x >= m.E) {                           // masked pairs: zero rows
+            const int64_t first = c0 - wave * kCols, n = min((int64_t)(kWaves * kCols), cols - first);
+            for (int64_t i = threadIdx.x; i < rows * n; i += kThreads) store1<OUT>(m.out, pair_of[i / n] * cols + first + i % n, 0.0f);
+            continue;
+        }
+        const uint8_t* wrow[4];
+        const float* wscale[kScales];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t c = ACT ? c0 + 8 * (r / 4) + 4 * (i & 1) + r % 4 : c0 + 16 * (r / 4) + 4 * i + r % 4;
+            const int64_t n = min(c, cols - 1) + (ACT && i >= 2 ? cols : 0);
+            wrow[i] = m.w + ((int64_t)desc.x * m.N + n) * m.K;
+        }
+#pragma unroll
+        for (int i = 0; i < kScales; ++i) {
+            const int64_t n = min(c0 + run * kLaneCols, cols - 1) + i * cols;
+            wscale[i] = m.w_scale + ((int64_t)desc.x * g.nr + n / kFp8Block) * g.nb;
+        }
+        const uint8_t* arow[kRuns];
+#pragma unroll
+        for (int i = 0; i < kRuns; ++i) {
+            const int x = threadIdx.x / 8 + i * (kThreads / 8);
+            arow[i] = m.a + (pair_of[x] / m.act_div) * m.K;
+        }
+        const float* ascale = m.a_scale + (pair_of[threadIdx.x % BM] / m.act_div) * g.nb;
+        const auto stage = [&](int64_t kb) {
+            const int c = threadIdx.x % 8;
+            const int64_t k = kb * kFp8Block + c * 16;
+#pragma unroll
+            for (int i = 0; i < kRuns; ++i) {
+                const int x = threadIdx.x / 8 + i * (kThreads / 8);
+                i32x4 v = {0, 0, 0, 0};
+                if (k < m.K) v = *reinterpret_cast<const i32x4*>(arow[i] + k);
+                act[kb & 1][x][c ^ (x % 8)] = v;
+            }
+            if (threadIdx.x < BM) act_scale[kb & 1][threadIdx.x] = ascale[kb];
+        };
+        f32x4 acc[4][TT] = {};
+        stage(0);
+        for (int64_t kb = 0; kb < g.nb; ++kb) {
+            __syncthreads();                           // block kb is staged; block kb - 1 has been read
+            if (kb + 1 < g.nb) stage(kb + 1);
+            Operand<kExact> w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = Operand<kExact>(load_block(wrow[i], kb, m.K, run));
+            float sw[kScales];
+#pragma unroll
+            for (int i = 0; i < kScales; ++i) sw[i] = wscale[i][kb];
+#pragma unroll
+            for (int j = 0; j < TT; ++j) {
+                const int x = j * 16 + r;
+                const Operand<kExact> b(join(act[kb & 1][x][run ^ (x % 8)], act[kb & 1][x][(run + 4) ^ (x % 8)]));
+                const float sa = act_scale[kb & 1][x];
+                f32x4 p[4];
+                block_products(w, b, p);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float s = sa * sw[ACT ? i / 2 : 0];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) acc[i][j][q] = __builtin_fmaf(p[i][q], s, acc[i][j][q]);
+                }
+            }
+        }
+        const int64_t first = c0 + run * kLaneCols;    // this lane's columns
+#pragma unroll
+        for (int j = 0; j < TT; ++j) {
+            const int x = j * 16 + r;
+            if (x >= rows) continue;
+            const int64_t o = pair_of[x] * cols + first;
+#pragma unroll
+            for (int c = 0; c < kLaneCols; ++c) {
+                float v = acc[c / 4][j][c % 4];
+                if constexpr (ACT) v = gated_act(m.act, v) * acc[c / 4 + 2][j][c % 4];
+                if (first + c < cols) store1<OUT>(m.out, o + c, v);
+            }
+        }
+    }
+}
+
+constexpr int64_t kMaxGrid = int64_t(1) << 22;         // workgroups; more tiles than that are walked with a stride
+
+template <int OUT, bool ACT>
+int launch_gemv(const Fp8Args& m, hipStream_t s)
+{
+    const int64_t cols = ACT ? m.N / 2 : m.N;
+    const int64_t pairs = m.T * m.top_k, ntiles = (cols + 15) / 16;
+    const int by_pair = pairs <= m.E + 1;
+    const int64_t nb = (m.K + kFp8Block - 1) / kFp8Block, nr = (m.N + kFp8Block - 1) / kFp8Block;
+    return launch("moe_fp8_gemv_kernel", moe_fp8_gemv_kernel<OUT, ACT>, (by_pair ? pairs : m.E + 1) * ntiles,
+                  kGemvThreads, 0, s, m, nb, nr, ntiles, by_pair);
+}
+
+template <int OUT, bool ACT>
+int launch_grouped(const Fp8Args& m, const GroupedTables& g, int64_t tile_m, int64_t max_tiles, hipStream_t s)
+{
+    const int64_t grid = std::min(max_tiles * g.ntn, kMaxGrid);
+    if (tile_m == 128) return launch("moe_fp8_grouped_kernel<8>", moe_fp8_grouped_kernel<8, OUT, ACT>, grid, kThreads, 0, s, m, g);
+    if (tile_m == 64) return launch("moe_fp8_grouped_kernel<4>", moe_fp8_grouped_kernel<4, OUT, ACT>, grid, kThreads, 0, s, m, g);
+    return launch("moe_fp8_grouped_kernel<2>", moe_fp8_grouped_kernel<2, OUT, ACT>, grid, kThreads, 0, s, m, g);
+}
+
+// Calls f<OUT, ACT>() for the output type and activation of m.
+template <typename F>
+int dispatch(const Fp8Args& m, F f)
+{
+    if (m.act != 0) {
+        if (m.out_dtype == FTQ_F32) return f.template operator()<FTQ_F32, true>();
+        if (m.out_dtype == FTQ_F16) return f.template operator()<FTQ_F16, true>();
+        return f.template operator()<FTQ_BF16, true>();
+    }
+    if (m.out_dtype == FTQ_F32) return f.template operator()<FTQ_F32, false>();
+    if (m.out_dtype == FTQ_F16) return f.template operator()<FTQ_F16, false>();
+    return f.template operator()<FTQ_BF16, false>();
+}
+
+struct GemvCall {
+    const Fp8Args& m;
+    hipStream_t s;
+    template <int OUT, bool ACT> int operator()() const { return launch_gemv<OUT, ACT>(m, s); }
+};
+struct GroupedCall {
+    const Fp8Args& m;
+    const GroupedTables& g;
+    int64_t tile_m, max_tiles;
+    hipStream_t s;
+    template <int OUT, bool ACT> int operator()() const { return launch_grouped<OUT, ACT>(m, g, tile_m, max_tiles, s); }
+};
+
+}  // namespace
+
+int fp8_select_path(int64_t E, int64_t T, int64_t top_k)
+{
+    const int64_t pairs = T * top_k;
+    return pairs <= kFp8GemvMaxPairs && pairs <= 8 * E ? FTQ_PATH_GEMV : FTQ_PATH_GROUPED;
+}
+
+int64_t fp8_tile_m(int64_t E, int64_t T, int64_t top_k)
+{
+    const int64_t per_expert = T * top_k / E;
+    return per_expert >= 96 ? 128 : per_expert >= 40 ? 64 : 32;
+}
+
+int run_fp8_gemv(const Fp8Args& m, hipStream_t s) { return dispatch(m, GemvCall{m, s}); }
+
+int run_fp8_grouped(const Fp8Args& m, const BucketPlan& plan, const void* ws, hipStream_t s)
+{
+    const uint8_t* base = static_cast<const uint8_t*>(ws);
+    const int64_t cols = m.act ? m.N / 2 : m.N, tile = kWaves * (m.act ? 32 : 64);
+    const GroupedTables g{reinterpret_cast<const int32_t*>(base + plan.off_tiles),
+                          reinterpret_cast<const int32_t*>(base + plan.off_sorted),
+                          reinterpret_cast<const int4*>(base + plan.off_tdesc),
+                          (m.K + kFp8Block - 1) / kFp8Block, (m.N + kFp8Block - 1) / kFp8Block, (cols + tile - 1) / tile};
+    return dispatch(m, GroupedCall{m, g, plan.tile_m, plan.max_tiles, s});
+}
+
+}  // namespace ftq

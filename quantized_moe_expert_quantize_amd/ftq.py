@@ -26,6 +26,11 @@ W_Q4_0, W_Q4_1, W_Q5_0, W_Q5_1, W_Q8_0 = 2, 3, 6, 7, 8
 W_BLOCK_BYTES = {W_Q4_0: 18, W_Q4_1: 20, W_Q5_0: 22, W_Q5_1: 24, W_Q8_0: 34}
 GEMV_ONLY = (W_Q5_0, W_Q5_1)   # the other types also run on the grouped path
 QK, Q4_0_BYTES, Q8_1_BYTES = 32, 18, 36
+# element types of the router and the 8-bit floating-point calls
+F32, F16, BF16 = 0, 1, 2
+_DTYPE = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+FP8, FP8_BLOCK = torch.float8_e4m3fn, 128
 
 EXPORTS = (
     "ftq_quantize_q8_1", "ftq_quantize_q4_0", "ftq_moe_select_path", "ftq_moe_workspace_bytes",
@@ -36,6 +41,8 @@ EXPORTS = (
     "ftq_moe_gguf_q8_1", "ftq_moe_gguf_q8_1_partials",
     "ftq_last_error", "ftq_version",
     "ftq_debug_force_block_threads", "ftq_debug_grouped_kernel", "ftq_debug_route_kernels", "ftq_debug_gemv_plan", "ftq_moe_q4_0_q8_1_noalloc",
+    "ftq_moe_topk", "ftq_quantize_fp8", "ftq_quantize_fp8_weight",
+    "ftq_moe_fp8_select_path", "ftq_moe_fp8_workspace_bytes", "ftq_moe_fp8", "ftq_moe_fp8_route", "ftq_moe_fp8_routed",
 )
 
 
@@ -100,6 +107,23 @@ def lib() -> ctypes.CDLL:
     L.ftq_debug_gemv_plan.restype = I32
     L.ftq_moe_q4_0_q8_1_noalloc.argtypes = [P, P, P, P, I64, I64, I64, I64, I64, I32, P]
     L.ftq_moe_q4_0_q8_1_noalloc.restype = I32
+    F = ctypes.c_float
+    L.ftq_moe_topk.argtypes = [P, I32, I64, P, P, P, I64, I64, I64, I32, I64, I64, I32, I32, F, P]
+    L.ftq_moe_topk.restype = I32
+    L.ftq_quantize_fp8.argtypes = [P, I32, I64, I64, I64, P, P, P]
+    L.ftq_quantize_fp8.restype = I32
+    L.ftq_quantize_fp8_weight.argtypes = [P, I32, I64, I64, I64, P, P, P]
+    L.ftq_quantize_fp8_weight.restype = I32
+    L.ftq_moe_fp8_select_path.argtypes = [I64, I64, I64, I64, I64]
+    L.ftq_moe_fp8_select_path.restype = I32
+    L.ftq_moe_fp8_workspace_bytes.argtypes = [I64, I64, I64, I64, I64, I32]
+    L.ftq_moe_fp8_workspace_bytes.restype = I64
+    for name in ("ftq_moe_fp8", "ftq_moe_fp8_routed"):
+        f = getattr(L, name)
+        f.argtypes = [P, P, P, P, P, P, I32, I64, I64, I64, I64, I64, I32, I32, P, SZ, I32, P]
+        f.restype = I32
+    L.ftq_moe_fp8_route.argtypes = [P, I64, I64, I64, P, SZ, I32, P]
+    L.ftq_moe_fp8_route.restype = I32
     _lib = L
     return L
 
@@ -420,3 +444,161 @@ def combine_topk(y: torch.Tensor, gates: torch.Tensor, out: torch.Tensor | None 
     _check(lib().ftq_moe_combine_topk(_dev(y, "y", torch.float32), _dev(gates, "gates", torch.float32),
                                       _out(out, T * N, "out", torch.float32), T, top_k, N, _stream(stream)))
     return out
+
+
+# ---- router, and experts in 8-bit floating point -----------------------------
+
+def _here(t: torch.Tensor, name: str, dtype, shape=None):
+    """Address of a contiguous tensor on the current device."""
+    p = _dev(t, name, dtype)
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have the shape {shape}, got {tuple(t.shape)}")
+    return p
+
+
+def _rows(t: torch.Tensor, name: str):
+    """(address, dtype, row stride) of a [rows, columns] tensor with contiguous columns."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    if t.dtype not in _DTYPE:
+        raise ValueError(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+        raise ValueError(f"{name} must be [rows, columns] with contiguous columns and rows that do not overlap")
+    return t.data_ptr(), _DTYPE[t.dtype], t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _stream_here(stream) -> int:
+    if stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    if stream.device.index != torch.cuda.current_device():
+        raise ValueError(f"the stream is on {stream.device}, the current device is cuda:{torch.cuda.current_device()}")
+    return stream.cuda_stream
+
+
+def _keep(stream, *tensors):
+    """Memory allocated here for work on `stream` is not reused before that work is done."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
+def moe_topk(logits: torch.Tensor, top_k: int, score: int = SCORE_SOFTMAX, bias: torch.Tensor | None = None,
+             n_group: int = 1, topk_group: int = 1, group_top: int = 1, renorm: bool = True, scale: float = 1.0,
+             ids: torch.Tensor | None = None, gates: torch.Tensor | None = None, stream=None):
+    """Router: logits [T, E] (rows may be strided) -> (int32 ids, fp32 gates), each [T, top_k] (see ftq_moe_topk)."""
+    p, dt, ld = _rows(logits, "logits")
+    T, E = logits.shape
+    shape = (T, max(top_k, 0))
+    if ids is None:
+        ids = torch.empty(shape, dtype=torch.int32, device=logits.device)
+        _keep(stream, ids)
+    if gates is None:
+        gates = torch.empty(shape, dtype=torch.float32, device=logits.device)
+        _keep(stream, gates)
+    _check(lib().ftq_moe_topk(p, dt, ld, _here(bias, "bias", torch.float32, (E,)) if bias is not None else None,
+                              _here(ids, "ids", torch.int32, shape), _here(gates, "gates", torch.float32, shape),
+                              T, E, top_k, score, n_group, topk_group, group_top, int(renorm), scale, _stream_here(stream)))
+    return ids, gates
+
+
+def quantize_fp8(x: torch.Tensor, out: torch.Tensor | None = None, scales: torch.Tensor | None = None, stream=None):
+    """x [T, K] (rows may be strided) -> (e4m3 codes [T, K], fp32 scales [T, ceil(K/128)])."""
+    p, dt, ld = _rows(x, "x")
+    T, K = x.shape
+    shape = (T, -(-K // FP8_BLOCK))
+    if out is None:
+        out = torch.empty((T, K), dtype=FP8, device=x.device)
+        _keep(stream, out)
+    if scales is None:
+        scales = torch.empty(shape, dtype=torch.float32, device=x.device)
+        _keep(stream, scales)
+    _check(lib().ftq_quantize_fp8(p, dt, ld, T, K, _here(out, "out", FP8, (T, K)),
+                                  _here(scales, "scales", torch.float32, shape), _stream_here(stream)))
+    return out, scales
+
+
+def quantize_fp8_weight(w: torch.Tensor, out: torch.Tensor | None = None, scales: torch.Tensor | None = None, stream=None):
+    """w [E, N, K] -> (e4m3 codes [E, N, K], fp32 scales [E, ceil(N/128), ceil(K/128)])."""
+    if w.dim() != 3 or w.dtype not in _DTYPE:
+        raise ValueError("w must be [E, N, K] in float32, float16 or bfloat16")
+    E, N, K = w.shape
+    shape = (E, -(-N // FP8_BLOCK), -(-K // FP8_BLOCK))
+    if out is None:
+        out = torch.empty((E, N, K), dtype=FP8, device=w.device)
+        _keep(stream, out)
+    if scales is None:
+        scales = torch.empty(shape, dtype=torch.float32, device=w.device)
+        _keep(stream, scales)
+    _check(lib().ftq_quantize_fp8_weight(_here(w, "w", w.dtype), _DTYPE[w.dtype], E, N, K, _here(out, "out", FP8, (E, N, K)),
+                                         _here(scales, "scales", torch.float32, shape), _stream_here(stream)))
+    return out, scales
+
+
+def fp8_select_path(E: int, N: int, K: int, T: int, top_k: int) -> int:
+    r = lib().ftq_moe_fp8_select_path(E, N, K, T, top_k)
+    if r < 0:
+        raise FtqError(-r, last_error())
+    return r
+
+
+def fp8_workspace_bytes(E: int, N: int, K: int, T: int, top_k: int, path: int = PATH_AUTO) -> int:
+    r = lib().ftq_moe_fp8_workspace_bytes(E, N, K, T, top_k, path)
+    if r < 0:
+        raise FtqError(ERR_INVALID_ARG, last_error())
+    return r
+
+
+def _fp8_call(entry, w, w_scale, a, a_scale, topk_ids, E, N, K, per_pair, act, out, workspace, path, stream):
+    T, top_k = topk_ids.shape
+    rows, nb = T * top_k if per_pair else T, -(-K // FP8_BLOCK)
+    if out.dtype not in _DTYPE:
+        raise ValueError(f"out must be float32, float16 or bfloat16, got {out.dtype}")
+    ws_n = workspace.numel() if workspace is not None else 0
+    _check(entry(
+        _here(w, "w", FP8, (E, N, K)), _here(w_scale, "w_scale", torch.float32, (E, -(-N // FP8_BLOCK), nb)),
+        _here(a, "a", FP8, (rows, K)), _here(a_scale, "a_scale", torch.float32, (rows, nb)),
+        _here(topk_ids, "topk_ids", torch.int32), _here(out, "out", out.dtype, (T * top_k, N // 2 if act else N)),
+        _DTYPE[out.dtype], E, N, K, T, top_k, int(per_pair), act,
+        _here(workspace, "workspace", torch.uint8) if workspace is not None else None, ws_n, path, _stream_here(stream)))
+    return out
+
+
+def moe_fp8(w: torch.Tensor, w_scale: torch.Tensor, a: torch.Tensor, a_scale: torch.Tensor, topk_ids: torch.Tensor,
+            E: int, N: int, K: int, per_pair: bool = False, act: int = 0, path: int = PATH_AUTO,
+            out: torch.Tensor | None = None, out_dtype: torch.dtype = torch.float32,
+            workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Expert matmul on e4m3 weights [E, N, K] and activations [T or T*top_k, K] with their block scales:
+    out [T*top_k, N], or with act (ACT_*) act(gate) * up [T*top_k, N/2]."""
+    T, top_k = topk_ids.shape
+    if out is None:
+        out = torch.empty((T * top_k, N // 2 if act else N), dtype=out_dtype, device=a.device)
+        _keep(stream, out)
+    if workspace is None:
+        need = fp8_workspace_bytes(E, N, K, T, top_k, path)
+        workspace = torch.empty(need, dtype=torch.uint8, device=a.device) if need else None
+        _keep(stream, workspace)
+    return _fp8_call(lib().ftq_moe_fp8, w, w_scale, a, a_scale, topk_ids, E, N, K, per_pair, act, out, workspace, path,
+                     stream)
+
+
+def moe_fp8_route(topk_ids: torch.Tensor, E: int, workspace: torch.Tensor | None, path: int = PATH_AUTO,
+                  stream=None) -> None:
+    """Group the pairs by expert into `workspace` for moe_fp8_routed (see ftq_moe_fp8_route)."""
+    T, top_k = topk_ids.shape
+    ws_n = workspace.numel() if workspace is not None else 0
+    _check(lib().ftq_moe_fp8_route(_here(topk_ids, "topk_ids", torch.int32), E, T, top_k,
+                                   _here(workspace, "workspace", torch.uint8) if workspace is not None else None, ws_n,
+                                   path, _stream_here(stream)))
+
+
+def moe_fp8_routed(w: torch.Tensor, w_scale: torch.Tensor, a: torch.Tensor, a_scale: torch.Tensor,
+                   topk_ids: torch.Tensor, E: int, N: int, K: int, out: torch.Tensor, workspace: torch.Tensor | None,
+                   per_pair: bool = False, act: int = 0, path: int = PATH_AUTO, stream=None) -> torch.Tensor:
+    """moe_fp8 on pairs already routed into `workspace` by moe_fp8_route."""
+    return _fp8_call(lib().ftq_moe_fp8_routed, w, w_scale, a, a_scale, topk_ids, E, N, K, per_pair, act, out, workspace,
+                     path, stream)

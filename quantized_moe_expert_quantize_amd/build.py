@@ -40,8 +40,10 @@ FLAGS = ["-std=c++17", "-O3", "-fPIC", "-ffp-contract=off", "-fno-strict-aliasin
 # Per-file flags.  grouped.hip: machine-level sinking would move the
 # scale-accumulates of the warp-specialised kernel out of the slots between its
 # matrix products (into the block after a stage's counter update), which
-# serialises them and multiplies the live registers.
-FILE_FLAGS = {"grouped.hip": ["-mllvm", "-disable-machine-sink"]}
+# serialises them and multiplies the live registers.  moe_fp8.hip: likewise, it
+# would move the grouped kernel's scale-accumulates below the matrix products of
+# the whole K block, whose results then all stay live (it spills).
+FILE_FLAGS = {"grouped.hip": ["-mllvm", "-disable-machine-sink"], "moe_fp8.hip": ["-mllvm", "-disable-machine-sink"]}
 
 
 def sources():

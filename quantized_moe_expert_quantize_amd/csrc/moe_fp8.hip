@@ -107,6 +107,22 @@ __device__ __forceinline__ void store1(void* out, int64_t i, float v)
     else static_cast<uint16_t*>(out)[i] = OUT == FTQ_F16 ? f16_of_f32(v) : bf16_of_f32(v);
 }
 
+// Four consecutive results at any element address (the hardware takes unaligned accesses).
+struct F32x4 { float v[4]; } __attribute__((packed, aligned(4)));
+struct U16x4 { uint16_t v[4]; } __attribute__((packed, aligned(2)));
+template <int OUT>
+__device__ __forceinline__ void store4(void* out, int64_t i, const float (&v)[4])
+{
+    if constexpr (OUT == FTQ_F32) {
+        *reinterpret_cast<F32x4*>(static_cast<float*>(out) + i) = F32x4{{v[0], v[1], v[2], v[3]}};
+    } else {
+        U16x4 h;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) h.v[q] = OUT == FTQ_F16 ? f16_of_f32(v[q]) : bf16_of_f32(v[q]);
+        *reinterpret_cast<U16x4*>(static_cast<uint16_t*>(out) + i) = h;
+    }
+}
+
 __device__ __forceinline__ bool expert_ok(int32_t id, int64_t E) { return id >= 0 && id < E; }
 
 // ---- GEMV ---------------------------------------------------------------------
@@ -217,6 +233,16 @@ constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
 constexpr int kRowsPerWave = 64;                       // weight rows: four 16-row tiles
 
+// Barrier of the workgroup for LDS alone: global loads stay in flight across it.
+__device__ __forceinline__ void block_barrier()
+{
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+constexpr int kXcds = 8;
+
 struct GroupedTables {
     const int32_t* tiles;     // [E + 2] first tile of each bucket; the last entry is their number
     const int32_t* sorted;    // pair ids by expert
@@ -231,8 +257,9 @@ struct GroupedTables {
 // so that a lane's results over the four tiles are 16 consecutive columns.  With
 // ACT the wave has 32 columns, tiles 0 and 1 their gate and 2 and 3 their up
 // rows, and a lane 8 consecutive columns.
+// A table tile of more than 16*TT pairs is made by `subs` items.
 template <int TT, int OUT, bool ACT>
-__global__ __launch_bounds__(kThreads) void moe_fp8_grouped_kernel(Fp8Args m, GroupedTables g)
+__global__ __launch_bounds__(kThreads, 2) void moe_fp8_grouped_kernel(Fp8Args m, GroupedTables g, int subs)
 {
     constexpr bool kExact = OUT == FTQ_F32;
     constexpr int BM = 16 * TT;
@@ -243,14 +270,19 @@ __global__ __launch_bounds__(kThreads) void moe_fp8_grouped_kernel(Fp8Args m, Gr
     __shared__ i32x4 act[2][BM][8];                    // run c of row x sits at c ^ (x % 8)
     __shared__ float act_scale[2][BM];
     __shared__ int32_t pair_of[BM];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = uniform((int32_t)(threadIdx.x >> 6));
     const int r = lane & 15, run = lane >> 4;
     const int64_t cols = ACT ? m.N / 2 : m.N;
-    const int64_t total = (int64_t)g.tiles[m.E + 1] * g.ntn;
-    for (int64_t item = blockIdx.x; item < total; item += gridDim.x) {
+    const int64_t total = (int64_t)g.tiles[m.E + 1] * subs * g.ntn, full = m.K / kFp8Block;
+    // each XCD takes a contiguous eighth of the items, so that what its workgroups share meets in its L2
+    const int64_t per = (total + kXcds - 1) / kXcds, end = min(total, (int64_t)(blockIdx.x % kXcds + 1) * per);
+    for (int64_t item = blockIdx.x % kXcds * per + blockIdx.x / kXcds; item < end; item += gridDim.x / kXcds) {
         const int64_t mt = item / g.ntn, c0 = (item - mt * g.ntn) * (kWaves * kCols) + wave * kCols;
-        const int4 desc = g.tdesc[mt];
-        const int rows = desc.z;
+        const int sub = (int)(mt % subs) * BM;
+        const int4 td = g.tdesc[mt / subs];
+        const int4 desc{uniform(td.x), uniform(td.y) + sub, 0, 0};
+        const int rows = min(uniform(td.z) - sub, BM);
+        if (rows <= 0) continue;
         __syncthreads();                               // the last item's LDS has been read
         if (threadIdx.x < BM) pair_of[threadIdx.x] = g.sorted[desc.y + min((int)threadIdx.x, rows - 1)];
         __syncthreads();
@@ -259,63 +291,119 @@ __global__ __launch_bounds__(kThreads) void moe_fp8_grouped_kernel(Fp8Args m, Gr
             for (int64_t i = threadIdx.x; i < rows * n; i += kThreads) store1<OUT>(m.out, pair_of[i / n] * cols + first + i % n, 0.0f);
             continue;
         }
-        const uint8_t* wrow[4];
+        // weights: uniform bases, 32-bit lane offsets
+        const int64_t cb = min(c0, cols - 1);
+        const uint8_t* wbase[kScales];
         const float* wscale[kScales];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t c = ACT ? c0 + 8 * (r / 4) + 4 * (i & 1) + r % 4 : c0 + 16 * (r / 4) + 4 * i + r % 4;
-            const int64_t n = min(c, cols - 1) + (ACT && i >= 2 ? cols : 0);
-            wrow[i] = m.w + ((int64_t)desc.x * m.N + n) * m.K;
-        }
+        uint32_t woff[4];
 #pragma unroll
         for (int i = 0; i < kScales; ++i) {
+            wbase[i] = m.w + ((int64_t)desc.x * m.N + cb + i * cols) * m.K;
             const int64_t n = min(c0 + run * kLaneCols, cols - 1) + i * cols;
             wscale[i] = m.w_scale + ((int64_t)desc.x * g.nr + n / kFp8Block) * g.nb;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int c = ACT ? 8 * (r / 4) + 4 * (i & 1) + r % 4 : 16 * (r / 4) + 4 * i + r % 4;
+            woff[i] = (uint32_t)min((int64_t)c, cols - 1 - cb) * (uint32_t)m.K + run * 16;
         }
         const uint8_t* arow[kRuns];
 #pragma unroll
         for (int i = 0; i < kRuns; ++i) {
             const int x = threadIdx.x / 8 + i * (kThreads / 8);
-            arow[i] = m.a + (pair_of[x] / m.act_div) * m.K;
+            arow[i] = m.a + (pair_of[x] / (int)m.act_div) * m.K + threadIdx.x % 8 * 16;
         }
-        const float* ascale = m.a_scale + (pair_of[threadIdx.x % BM] / m.act_div) * g.nb;
-        const auto stage = [&](int64_t kb) {
-            const int c = threadIdx.x % 8;
-            const int64_t k = kb * kFp8Block + c * 16;
+        const float* ascale = m.a_scale + (pair_of[threadIdx.x % BM] / (int)m.act_div) * g.nb;
+        i32x4 av[kRuns];
+        float asv;
+        const auto put = [&](int buf) {
 #pragma unroll
             for (int i = 0; i < kRuns; ++i) {
                 const int x = threadIdx.x / 8 + i * (kThreads / 8);
-                i32x4 v = {0, 0, 0, 0};
-                if (k < m.K) v = *reinterpret_cast<const i32x4*>(arow[i] + k);
-                act[kb & 1][x][c ^ (x % 8)] = v;
+                act[buf][x][(threadIdx.x % 8) ^ (x % 8)] = av[i];
             }
-            if (threadIdx.x < BM) act_scale[kb & 1][threadIdx.x] = ascale[kb];
+            if (threadIdx.x < BM) act_scale[buf][threadIdx.x] = asv;
         };
-        f32x4 acc[4][TT] = {};
-        stage(0);
-        for (int64_t kb = 0; kb < g.nb; ++kb) {
-            __syncthreads();                           // block kb is staged; block kb - 1 has been read
-            if (kb + 1 < g.nb) stage(kb + 1);
-            Operand<kExact> w[4];
+        const auto fetch = [&](int64_t kb) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = Operand<kExact>(load_block(wrow[i], kb, m.K, run));
-            float sw[kScales];
+            for (int i = 0; i < kRuns; ++i) av[i] = *reinterpret_cast<const i32x4*>(arow[i] + kb * kFp8Block);
+            asv = ascale[kb];
+        };
+        i32x8 wv[4];
+        float sw[kScales];
+        const auto weights = [&](int64_t kb) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint8_t* p = wbase[ACT ? i / 2 : 0] + kb * kFp8Block;
+                wv[i] = join(*reinterpret_cast<const i32x4*>(p + woff[i]), *reinterpret_cast<const i32x4*>(p + woff[i] + 64));
+            }
 #pragma unroll
             for (int i = 0; i < kScales; ++i) sw[i] = wscale[i][kb];
+        };
+        f32x4 acc[4][TT] = {};
+        const auto multiply = [&](int buf) {
+            Operand<kExact> w[4];
 #pragma unroll
-            for (int j = 0; j < TT; ++j) {
-                const int x = j * 16 + r;
-                const Operand<kExact> b(join(act[kb & 1][x][run ^ (x % 8)], act[kb & 1][x][(run + 4) ^ (x % 8)]));
-                const float sa = act_scale[kb & 1][x];
-                f32x4 p[4];
-                block_products(w, b, p);
+            for (int i = 0; i < 4; ++i) w[i] = Operand<kExact>(wv[i]);
+            // tile j's products are made while tile j - 1's are added up
+            f32x4 p[2][4];
+            float sa = 0.0f;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float s = sa * sw[ACT ? i / 2 : 0];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) acc[i][j][q] = __builtin_fmaf(p[i][q], s, acc[i][j][q]);
+            for (int j = 0; j <= TT; ++j) {
+                float next = 0.0f;
+                if (j < TT) {
+                    const int x = j * 16 + r;
+                    const Operand<kExact> b(join(act[buf][x][run ^ (r % 8)], act[buf][x][(run + 4) ^ (r % 8)]));
+                    next = act_scale[buf][x];
+                    block_products(w, b, p[j & 1]);
                 }
+                if (j > 0) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float s = sa * sw[ACT ? i / 2 : 0];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) acc[i][j - 1][q] = __builtin_fmaf(p[(j - 1) & 1][i][q], s, acc[i][j - 1][q]);
+                    }
+                }
+                sa = next;
+                __builtin_amdgcn_sched_barrier(0);
             }
+        };
+        if (full > 0) {
+            fetch(0);
+            weights(0);
+            put(0);
+            fetch(min((int64_t)1, full - 1));
+            for (int64_t kb = 0; kb < full; ++kb) {
+                block_barrier();                       // block kb is staged; block kb - 1 has been read
+                multiply(kb & 1);
+                weights(min(kb + 1, full - 1));        // (past the end: the last block again, unused)
+                put((kb + 1) & 1);
+                fetch(min(kb + 2, full - 1));
+            }
+        }
+        if (full < g.nb) {                             // the last block is cut short: zeros past K on both sides
+            const int64_t k0 = full * kFp8Block;
+            const bool in = k0 + threadIdx.x % 8 * 16 < m.K;
+#pragma unroll
+            for (int i = 0; i < kRuns; ++i) {
+                av[i] = i32x4{0, 0, 0, 0};
+                if (in) av[i] = *reinterpret_cast<const i32x4*>(arow[i] + k0);
+            }
+            asv = ascale[full];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint8_t* p = wbase[ACT ? i / 2 : 0] + k0 + woff[i];
+                i32x4 lo = {0, 0, 0, 0}, hi = {0, 0, 0, 0};
+                if (k0 + run * 16 < m.K) lo = *reinterpret_cast<const i32x4*>(p);
+                if (k0 + run * 16 + 64 < m.K) hi = *reinterpret_cast<const i32x4*>(p + 64);
+                wv[i] = join(lo, hi);
+            }
+#pragma unroll
+            for (int i = 0; i < kScales; ++i) sw[i] = wscale[i][full];
+            put(full & 1);
+            block_barrier();
+            multiply(full & 1);
         }
         const int64_t first = c0 + run * kLaneCols;    // this lane's columns
 #pragma unroll
@@ -324,10 +412,21 @@ __global__ __launch_bounds__(kThreads) void moe_fp8_grouped_kernel(Fp8Args m, Gr
             if (x >= rows) continue;
             const int64_t o = pair_of[x] * cols + first;
 #pragma unroll
-            for (int c = 0; c < kLaneCols; ++c) {
-                float v = acc[c / 4][j][c % 4];
-                if constexpr (ACT) v = gated_act(m.act, v) * acc[c / 4 + 2][j][c % 4];
-                if (first + c < cols) store1<OUT>(m.out, o + c, v);
+            for (int c = 0; c < kLaneCols; c += 4) {
+                float v[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    v[q] = acc[c / 4][j][q];
+                    if constexpr (ACT) v[q] = gated_act(m.act, v[q]) * acc[c / 4 + 2][j][q];
+                }
+                if (first + c + 4 <= cols) {
+                    store4<OUT>(m.out, o + c, v);
+                } else {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        if (first + c + q < cols) store1<OUT>(m.out, o + c + q, v[q]);
+                    }
+                }
             }
         }
     }
@@ -349,10 +448,15 @@ int launch_gemv(const Fp8Args& m, hipStream_t s)
 template <int OUT, bool ACT>
 int launch_grouped(const Fp8Args& m, const GroupedTables& g, int64_t tile_m, int64_t max_tiles, hipStream_t s)
 {
-    const int64_t grid = std::min(max_tiles * g.ntn, kMaxGrid);
-    if (tile_m == 128) return launch("moe_fp8_grouped_kernel<8>", moe_fp8_grouped_kernel<8, OUT, ACT>, grid, kThreads, 0, s, m, g);
-    if (tile_m == 64) return launch("moe_fp8_grouped_kernel<4>", moe_fp8_grouped_kernel<4, OUT, ACT>, grid, kThreads, 0, s, m, g);
-    return launch("moe_fp8_grouped_kernel<2>", moe_fp8_grouped_kernel<2, OUT, ACT>, grid, kThreads, 0, s, m, g);
+    // the exact form's fp16 operands take twice the registers: at most 64 pairs at a time
+    constexpr int kMost = OUT == FTQ_F32 ? 64 : 128;
+    const int subs = (int)((tile_m + kMost - 1) / kMost);
+    const int64_t grid = std::min((max_tiles * subs * g.ntn + kXcds - 1) / kXcds * kXcds, kMaxGrid);
+    if (tile_m / subs == 128) {
+        if constexpr (kMost == 128) return launch("moe_fp8_grouped_kernel<8>", moe_fp8_grouped_kernel<8, OUT, ACT>, grid, kThreads, 0, s, m, g, subs);
+    }
+    if (tile_m / subs == 64) return launch("moe_fp8_grouped_kernel<4>", moe_fp8_grouped_kernel<4, OUT, ACT>, grid, kThreads, 0, s, m, g, subs);
+    return launch("moe_fp8_grouped_kernel<2>", moe_fp8_grouped_kernel<2, OUT, ACT>, grid, kThreads, 0, s, m, g, subs);
 }
 
 // Calls f<OUT, ACT>() for the output type and activation of m.

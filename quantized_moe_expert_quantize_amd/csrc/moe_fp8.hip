@@ -107,19 +107,21 @@ __device__ __forceinline__ void store1(void* out, int64_t i, float v)
     else static_cast<uint16_t*>(out)[i] = OUT == FTQ_F16 ? f16_of_f32(v) : bf16_of_f32(v);
 }
 
-// Four consecutive results at any element address (the hardware takes unaligned accesses).
+// 16 bytes of consecutive results at any element address (the hardware takes unaligned accesses).
 struct F32x4 { float v[4]; } __attribute__((packed, aligned(4)));
-struct U16x4 { uint16_t v[4]; } __attribute__((packed, aligned(2)));
-template <int OUT>
-__device__ __forceinline__ void store4(void* out, int64_t i, const float (&v)[4])
+struct U16x8 { uint16_t v[8]; } __attribute__((packed, aligned(2)));
+template <int OUT, int N>
+__device__ __forceinline__ void store_run(void* out, int64_t i, const float (&v)[N])
 {
     if constexpr (OUT == FTQ_F32) {
+        static_assert(N == 4);
         *reinterpret_cast<F32x4*>(static_cast<float*>(out) + i) = F32x4{{v[0], v[1], v[2], v[3]}};
     } else {
-        U16x4 h;
+        static_assert(N == 8);
+        U16x8 h;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) h.v[q] = OUT == FTQ_F16 ? f16_of_f32(v[q]) : bf16_of_f32(v[q]);
-        *reinterpret_cast<U16x4*>(static_cast<uint16_t*>(out) + i) = h;
+        for (int q = 0; q < 8; ++q) h.v[q] = OUT == FTQ_F16 ? f16_of_f32(v[q]) : bf16_of_f32(v[q]);
+        *reinterpret_cast<U16x8*>(static_cast<uint16_t*>(out) + i) = h;
     }
 }
 
@@ -253,10 +255,13 @@ struct GroupedTables {
 // A workgroup makes 16*TT pairs x 256 weight rows; wave v has 64 rows of them and
 // all the pairs, so each weight is read by one wave only, straight into
 // registers, and the activations, which every wave needs, go through LDS.
-// Within a wave, row r of weight tile i is row 16*(r/4) + 4*i + r%4 of its 64,
-// so that a lane's results over the four tiles are 16 consecutive columns.  With
-// ACT the wave has 32 columns, tiles 0 and 1 their gate and 2 and 3 their up
-// rows, and a lane 8 consecutive columns.
+// With ACT the wave has 32 columns, tiles 0 and 1 their gate and 2 and 3 their up
+// rows.  Which row of a tile is which column is free; it is chosen so that a
+// lane's results make whole 16-byte stores and the four lanes of a row 64 bytes
+// side by side (8-byte stores at a stride, the first form, took 290 us for the
+// 369 MB of a second layer's bf16 results that take 90 us so): fp32, row r of
+// tile i is column 16*i + r, four columns a lane and tile; 16 bits, column
+// 32*(i/2) + 8*(r/4) + 4*(i%2) + r%4, eight a lane and pair of tiles.
 // A table tile of more than 16*TT pairs is made by `subs` items.
 template <int TT, int OUT, bool ACT>
 __global__ __launch_bounds__(kThreads, 2) void moe_fp8_grouped_kernel(Fp8Args m, GroupedTables g, int subs)
@@ -265,8 +270,12 @@ __global__ __launch_bounds__(kThreads, 2) void moe_fp8_grouped_kernel(Fp8Args m,
     constexpr int BM = 16 * TT;
     constexpr int kRuns = BM * 8 / kThreads;           // 16-byte runs of an activation tile per thread
     constexpr int kCols = ACT ? 32 : 64;               // output columns per wave
-    constexpr int kLaneCols = kCols / 4;               // consecutive columns per lane
-    constexpr int kScales = ACT ? 2 : 1;               // weight scales per lane and block
+    constexpr bool kWide = OUT == FTQ_F32;
+    constexpr int kRun = kWide ? 4 : 8;                // consecutive columns of a lane's store
+    // weight scales per lane and block: 64 rows from a multiple of 64 on share one, 32 gate rows another, and
+    // 32 up rows, which start at a multiple of 16, have at most one for each 16
+    constexpr int kScales = ACT ? (kWide ? 3 : 2) : 1;
+    constexpr int kScaleOf[4] = {0, 0, ACT ? 1 : 0, kScales - 1};
     __shared__ i32x4 act[2][BM][8];                    // run c of row x sits at c ^ (x % 8)
     __shared__ float act_scale[2][BM];
     __shared__ int32_t pair_of[BM];
@@ -293,18 +302,21 @@ __global__ __launch_bounds__(kThreads, 2) void moe_fp8_grouped_kernel(Fp8Args m,
         }
         // weights: uniform bases, 32-bit lane offsets
         const int64_t cb = min(c0, cols - 1);
-        const uint8_t* wbase[kScales];
+        const uint8_t* wbase[ACT ? 2 : 1];
         const float* wscale[kScales];
         uint32_t woff[4];
 #pragma unroll
+        for (int i = 0; i < (ACT ? 2 : 1); ++i) wbase[i] = m.w + ((int64_t)desc.x * m.N + cb + i * cols) * m.K;
+#pragma unroll
         for (int i = 0; i < kScales; ++i) {
-            wbase[i] = m.w + ((int64_t)desc.x * m.N + cb + i * cols) * m.K;
-            const int64_t n = min(c0 + run * kLaneCols, cols - 1) + i * cols;
+            const int64_t c = i == 0 ? c0 : kWide ? c0 + (i - 1) * 16 : c0 + run * 8;
+            const int64_t n = min(c, cols - 1) + (i > 0 ? cols : 0);
             wscale[i] = m.w_scale + ((int64_t)desc.x * g.nr + n / kFp8Block) * g.nb;
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int c = ACT ? 8 * (r / 4) + 4 * (i & 1) + r % 4 : 16 * (r / 4) + 4 * i + r % 4;
+            const int t = ACT ? i & 1 : i;             // tile among those of its columns
+            const int c = kWide ? 16 * t + r : 32 * (t / 2) + 8 * (r / 4) + 4 * (t & 1) + r % 4;
             woff[i] = (uint32_t)min((int64_t)c, cols - 1 - cb) * (uint32_t)m.K + run * 16;
         }
         const uint8_t* arow[kRuns];
@@ -360,7 +372,7 @@ __global__ __launch_bounds__(kThreads, 2) void moe_fp8_grouped_kernel(Fp8Args m,
                 if (j > 0) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float s = sa * sw[ACT ? i / 2 : 0];
+                        const float s = sa * sw[kScaleOf[i]];
 #pragma unroll
                         for (int q = 0; q < 4; ++q) acc[i][j - 1][q] = __builtin_fmaf(p[(j - 1) & 1][i][q], s, acc[i][j - 1][q]);
                     }
@@ -405,26 +417,26 @@ __global__ __launch_bounds__(kThreads, 2) void moe_fp8_grouped_kernel(Fp8Args m,
             block_barrier();
             multiply(full & 1);
         }
-        const int64_t first = c0 + run * kLaneCols;    // this lane's columns
 #pragma unroll
         for (int j = 0; j < TT; ++j) {
             const int x = j * 16 + r;
             if (x >= rows) continue;
-            const int64_t o = pair_of[x] * cols + first;
+            const int64_t o = pair_of[x] * cols;
 #pragma unroll
-            for (int c = 0; c < kLaneCols; c += 4) {
-                float v[4];
+            for (int t = 0; t < kCols / 16; t += kRun / 4) {
+                const int64_t c = c0 + 16 * t + kRun * run;
+                float v[kRun];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    v[q] = acc[c / 4][j][q];
-                    if constexpr (ACT) v[q] = gated_act(m.act, v[q]) * acc[c / 4 + 2][j][q];
+                for (int q = 0; q < kRun; ++q) {
+                    v[q] = acc[t + q / 4][j][q % 4];
+                    if constexpr (ACT) v[q] = gated_act(m.act, v[q]) * acc[t + q / 4 + 2][j][q % 4];
                 }
-                if (first + c + 4 <= cols) {
-                    store4<OUT>(m.out, o + c, v);
+                if (c + kRun <= cols) {
+                    store_run<OUT>(m.out, o + c, v);
                 } else {
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        if (first + c + q < cols) store1<OUT>(m.out, o + c + q, v[q]);
+                    for (int q = 0; q < kRun; ++q) {
+                        if (c + q < cols) store1<OUT>(m.out, o + c + q, v[q]);
                     }
                 }
             }

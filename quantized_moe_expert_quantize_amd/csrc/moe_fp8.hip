@@ -235,6 +235,30 @@ constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
 constexpr int kRowsPerWave = 64;                       // weight rows: four 16-row tiles
 
+// Asynchronous copies from global memory into LDS, 16 or 4 bytes a lane, to
+// consecutive LDS addresses from `lds` (uniform).  Written as asm because the
+// compiler, which cannot tell the buffers of successive K blocks apart, would wait
+// for a copy in flight before every LDS read; the copies have no result
+// registers, and wait_copies() is the only thing that orders them.
+__device__ __forceinline__ uint32_t lds_address(const void* p)
+{
+    return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const uint8_t*)(const uint8_t*)p;
+}
+__device__ __forceinline__ void copy16(uint32_t lds, const uint8_t* base, uint32_t off)
+{
+    __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory", "m0");
+}
+__device__ __forceinline__ void copy16(uint32_t lds, const uint8_t* p)
+{
+    __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(p) : "memory", "m0");
+}
+__device__ __forceinline__ void copy4(uint32_t lds, const float* p)
+{
+    __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(lds), "v"(p) : "memory", "m0");
+}
+__device__ __forceinline__ void wait_copies() { __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+__device__ __forceinline__ void wait_lds() { __asm__ volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
 // Barrier of the workgroup for LDS alone: global loads stay in flight across it.
 __device__ __forceinline__ void block_barrier()
 {
@@ -277,7 +301,8 @@ __global__ __launch_bounds__(kThreads, 2) void moe_fp8_grouped_kernel(Fp8Args m,
     constexpr int kScales = ACT ? (kWide ? 3 : 2) : 1;
     constexpr int kScaleOf[4] = {0, 0, ACT ? 1 : 0, kScales - 1};
     __shared__ i32x4 act[2][BM][8];                    // run c of row x sits at c ^ (x % 8)
-    __shared__ float act_scale[2][BM];
+    __shared__ i32x4 weight[kWaves][64][8];            // each wave's rows of block kb, swizzled likewise
+    __shared__ float act_scale[2][BM < 64 ? 64 : BM];
     __shared__ int32_t pair_of[BM];
     const int lane = threadIdx.x & 63, wave = uniform((int32_t)(threadIdx.x >> 6));
     const int r = lane & 15, run = lane >> 4;
@@ -304,7 +329,6 @@ __global__ __launch_bounds__(kThreads, 2) void moe_fp8_grouped_kernel(Fp8Args m,
         const int64_t cb = min(c0, cols - 1);
         const uint8_t* wbase[ACT ? 2 : 1];
         const float* wscale[kScales];
-        uint32_t woff[4];
 #pragma unroll
         for (int i = 0; i < (ACT ? 2 : 1); ++i) wbase[i] = m.w + ((int64_t)desc.x * m.N + cb + i * cols) * m.K;
 #pragma unroll
@@ -313,44 +337,43 @@ __global__ __launch_bounds__(kThreads, 2) void moe_fp8_grouped_kernel(Fp8Args m,
             const int64_t n = min(c, cols - 1) + (i > 0 ? cols : 0);
             wscale[i] = m.w_scale + ((int64_t)desc.x * g.nr + n / kFp8Block) * g.nb;
         }
+        // copies: instruction d of a wave brings LDS rows 8*d .. 8*d + 7, eight lanes a row, so that a row's 128
+        // bytes are one request (lanes in operand order, one row each, read 16 bytes a cycle); lane l takes the
+        // 16-byte run (l%8) ^ (l/8) of its row
+        const int cr = lane / 8, cp = (lane % 8) ^ cr;
+        uint32_t woff[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int d = 0; d < 8; ++d) {
+            const int i = d / 2, y = d % 2 * 8 + cr;   // tile and row of it
             const int t = ACT ? i & 1 : i;             // tile among those of its columns
-            const int c = kWide ? 16 * t + r : 32 * (t / 2) + 8 * (r / 4) + 4 * (t & 1) + r % 4;
-            woff[i] = (uint32_t)min((int64_t)c, cols - 1 - cb) * (uint32_t)m.K + run * 16;
+            const int c = kWide ? 16 * t + y : 32 * (t / 2) + 8 * (y / 4) + 4 * (t & 1) + y % 4;
+            woff[d] = (uint32_t)min((int64_t)c, cols - 1 - cb) * (uint32_t)m.K + cp * 16;
         }
-        const uint8_t* arow[kRuns];
+        const uint8_t* arow[kRuns];                    // rows (i*4 + wave)*8 + l/8
 #pragma unroll
         for (int i = 0; i < kRuns; ++i) {
-            const int x = threadIdx.x / 8 + i * (kThreads / 8);
-            arow[i] = m.a + (pair_of[x] / (int)m.act_div) * m.K + threadIdx.x % 8 * 16;
+            const int x = (i * kWaves + wave) * 8 + cr;
+            arow[i] = m.a + (pair_of[x] / (int)m.act_div) * m.K + cp * 16;
         }
         const float* ascale = m.a_scale + (pair_of[threadIdx.x % BM] / (int)m.act_div) * g.nb;
-        i32x4 av[kRuns];
-        float asv;
-        const auto put = [&](int buf) {
+        constexpr int kScaleWaves = BM < 64 ? 1 : BM / 64;
+        float next[kScales];                           // weight scales of the block in flight
+        const auto copy_block = [&](int64_t kb, int buf) {
 #pragma unroll
-            for (int i = 0; i < kRuns; ++i) {
-                const int x = threadIdx.x / 8 + i * (kThreads / 8);
-                act[buf][x][(threadIdx.x % 8) ^ (x % 8)] = av[i];
-            }
-            if (threadIdx.x < BM) act_scale[buf][threadIdx.x] = asv;
-        };
-        const auto fetch = [&](int64_t kb) {
+            for (int i = 0; i < kScales; ++i) next[i] = wscale[i][kb];
 #pragma unroll
-            for (int i = 0; i < kRuns; ++i) av[i] = *reinterpret_cast<const i32x4*>(arow[i] + kb * kFp8Block);
-            asv = ascale[kb];
+            for (int d = 0; d < 8; ++d) copy16(lds_address(&weight[wave][8 * d][0]), wbase[ACT ? d / 4 : 0] + kb * kFp8Block, woff[d]);
+#pragma unroll
+            for (int i = 0; i < kRuns; ++i) copy16(lds_address(&act[buf][(i * kWaves + wave) * 8][0]), arow[i] + kb * kFp8Block);
+            if (wave < kScaleWaves) copy4(lds_address(&act_scale[buf][wave * 64]), ascale + kb);
         };
         i32x8 wv[4];
         float sw[kScales];
-        const auto weights = [&](int64_t kb) {
+        const auto read_weights = [&]() {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint8_t* p = wbase[ACT ? i / 2 : 0] + kb * kFp8Block;
-                wv[i] = join(*reinterpret_cast<const i32x4*>(p + woff[i]), *reinterpret_cast<const i32x4*>(p + woff[i] + 64));
-            }
+            for (int i = 0; i < 4; ++i) wv[i] = join(weight[wave][16 * i + r][run ^ (r % 8)], weight[wave][16 * i + r][(run + 4) ^ (r % 8)]);
 #pragma unroll
-            for (int i = 0; i < kScales; ++i) sw[i] = wscale[i][kb];
+            for (int i = 0; i < kScales; ++i) sw[i] = next[i];
         };
         f32x4 acc[4][TT] = {};
         const auto multiply = [&](int buf) {
@@ -362,11 +385,11 @@ __global__ __launch_bounds__(kThreads, 2) void moe_fp8_grouped_kernel(Fp8Args m,
             float sa = 0.0f;
 #pragma unroll
             for (int j = 0; j <= TT; ++j) {
-                float next = 0.0f;
+                float nsa = 0.0f;
                 if (j < TT) {
                     const int x = j * 16 + r;
                     const Operand<kExact> b(join(act[buf][x][run ^ (r % 8)], act[buf][x][(run + 4) ^ (r % 8)]));
-                    next = act_scale[buf][x];
+                    nsa = act_scale[buf][x];
                     block_products(w, b, p[j & 1]);
                 }
                 if (j > 0) {
@@ -377,45 +400,41 @@ __global__ __launch_bounds__(kThreads, 2) void moe_fp8_grouped_kernel(Fp8Args m,
                         for (int q = 0; q < 4; ++q) acc[i][j - 1][q] = __builtin_fmaf(p[(j - 1) & 1][i][q], s, acc[i][j - 1][q]);
                     }
                 }
-                sa = next;
+                sa = nsa;
                 __builtin_amdgcn_sched_barrier(0);
             }
         };
-        if (full > 0) {
-            fetch(0);
-            weights(0);
-            put(0);
-            fetch(min((int64_t)1, full - 1));
-            for (int64_t kb = 0; kb < full; ++kb) {
-                block_barrier();                       // block kb is staged; block kb - 1 has been read
-                multiply(kb & 1);
-                weights(min(kb + 1, full - 1));        // (past the end: the last block again, unused)
-                put((kb + 1) & 1);
-                fetch(min(kb + 2, full - 1));
-            }
+        if (full > 0) copy_block(0, 0);
+        for (int64_t kb = 0; kb < full; ++kb) {
+            wait_copies();
+            block_barrier();                           // every wave's copies of block kb are there, block kb - 1 has been read
+            read_weights();
+            wait_lds();                                // a wave's weights have one buffer: read before the next copy
+            if (kb + 1 < full) copy_block(kb + 1, (kb + 1) & 1);
+            multiply(kb & 1);
         }
         if (full < g.nb) {                             // the last block is cut short: zeros past K on both sides
+            const int buf = full & 1;
             const int64_t k0 = full * kFp8Block;
-            const bool in = k0 + threadIdx.x % 8 * 16 < m.K;
+            const bool in = k0 + cp * 16 < m.K;
+#pragma unroll
+            for (int d = 0; d < 8; ++d) {
+                i32x4 v = {0, 0, 0, 0};
+                if (in) v = *reinterpret_cast<const i32x4*>(wbase[ACT ? d / 4 : 0] + k0 + woff[d]);
+                weight[wave][8 * d + cr][lane % 8] = v;
+            }
 #pragma unroll
             for (int i = 0; i < kRuns; ++i) {
-                av[i] = i32x4{0, 0, 0, 0};
-                if (in) av[i] = *reinterpret_cast<const i32x4*>(arow[i] + k0);
+                i32x4 v = {0, 0, 0, 0};
+                if (in) v = *reinterpret_cast<const i32x4*>(arow[i] + k0);
+                act[buf][(i * kWaves + wave) * 8 + cr][lane % 8] = v;
             }
-            asv = ascale[full];
+            if (threadIdx.x < BM) act_scale[buf][threadIdx.x] = ascale[full];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint8_t* p = wbase[ACT ? i / 2 : 0] + k0 + woff[i];
-                i32x4 lo = {0, 0, 0, 0}, hi = {0, 0, 0, 0};
-                if (k0 + run * 16 < m.K) lo = *reinterpret_cast<const i32x4*>(p);
-                if (k0 + run * 16 + 64 < m.K) hi = *reinterpret_cast<const i32x4*>(p + 64);
-                wv[i] = join(lo, hi);
-            }
-#pragma unroll
-            for (int i = 0; i < kScales; ++i) sw[i] = wscale[i][full];
-            put(full & 1);
+            for (int i = 0; i < kScales; ++i) next[i] = wscale[i][full];
             block_barrier();
-            multiply(full & 1);
+            read_weights();
+            multiply(buf);
         }
 #pragma unroll
         for (int j = 0; j < TT; ++j) {

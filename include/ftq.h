@@ -464,7 +464,7 @@ int ftq_quantize_fp8_weight(const void* w, int dtype, int64_t E, int64_t N, int6
  *            and ftq_moe_fp8_select_path in place of that call's.
  * A row's bits depend neither on the other rows nor on the batch size while the
  * path is the same.  A NaN code or scale reaches only the results it is a term of.
- * Limits: K % 16 == 0; with act, N % 32 == 0 (FTQ_ERR_UNSUPPORTED otherwise;
+ * Limits: K % 16 == 0, K <= 2^25; with act, N % 32 == 0 (FTQ_ERR_UNSUPPORTED otherwise;
  * odd N: FTQ_ERR_INVALID_ARG); FTQ_PATH_GEMV takes at most 4096 pairs
  * (FTQ_ERR_UNSUPPORTED above); E, N, T, top_k as ftq_moe_q4_0_q8_1.
  *

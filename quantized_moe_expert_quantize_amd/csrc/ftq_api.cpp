@@ -244,7 +244,7 @@ int check_quantize_fp8(int dtype, int64_t rows, int64_t K, int64_t ld)
 int check_sizes_fp8(int64_t E, int64_t N, int64_t K, int64_t T, int64_t top_k)
 {
     if (K <= 0 || K % 16 != 0) { set_error("K must be a positive multiple of 16 (got %lld)", (long long)K); return FTQ_ERR_INVALID_ARG; }
-    if (K > INT64_MAX / 64) { set_error("tensor sizes overflow 64-bit byte offsets"); return FTQ_ERR_UNSUPPORTED; }
+    if (K > kFp8MaxK) { set_error("K = %lld exceeds the supported %lld", (long long)K, (long long)kFp8MaxK); return FTQ_ERR_UNSUPPORTED; }
     const int st = check_sizes(E, N, (K + 31) / 32 * 32, T, top_k);
     if (st != FTQ_OK) return st;
     if (T > 0 && K > INT64_MAX / 64 / (T * top_k)) { set_error("tensor sizes overflow 64-bit byte offsets"); return FTQ_ERR_UNSUPPORTED; }

@@ -69,22 +69,22 @@ template <> struct Operand<true> {
     }
 };
 
-// P_b of NW weight tiles with one activation tile.
-template <int NW>
-__device__ __forceinline__ void block_products(const Operand<false> (&w)[NW], const Operand<false>& a, f32x4 (&p)[NW])
+// P_b of the NP weight tiles from i0 on with one activation tile.
+template <int NW, int NP>
+__device__ __forceinline__ void block_products(const Operand<false> (&w)[NW], int i0, const Operand<false>& a, f32x4 (&p)[NP])
 {
     const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int i = 0; i < NW; ++i) p[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w[i].v, a.v, zero, 0, 0, 0, 0, 0, 0);
+    for (int i = 0; i < NP; ++i) p[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w[i0 + i].v, a.v, zero, 0, 0, 0, 0, 0, 0);
 }
-template <int NW>
-__device__ __forceinline__ void block_products(const Operand<true> (&w)[NW], const Operand<true>& a, f32x4 (&p)[NW])
+template <int NW, int NP>
+__device__ __forceinline__ void block_products(const Operand<true> (&w)[NW], int i0, const Operand<true>& a, f32x4 (&p)[NP])
 {
     const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int h = 0; h < 4; ++h) {
 #pragma unroll
-        for (int i = 0; i < NW; ++i) p[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w[i].v[h], a.v[h], h == 0 ? zero : p[i], 0, 0, 0);
+        for (int i = 0; i < NP; ++i) p[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w[i0 + i].v[h], a.v[h], h == 0 ? zero : p[i], 0, 0, 0);
     }
 }
 
@@ -198,7 +198,7 @@ __global__ __launch_bounds__(kGemvThreads) void moe_fp8_gemv_kernel(Fp8Args m, i
             f32x4 p[RT];
 #pragma unroll
             for (int i = 0; i < RT; ++i) w[i] = Operand<true>(load_block(wrow[i], kb, m.K, run));
-            block_products(w, Operand<true>(a), p);
+            block_products(w, 0, Operand<true>(a), p);
 #pragma unroll
             for (int i = 0; i < RT; ++i) {
                 const float s = sa * wscale[i][kb];
@@ -380,27 +380,41 @@ __global__ __launch_bounds__(kThreads, 2) void moe_fp8_grouped_kernel(Fp8Args m,
             Operand<kExact> w[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) w[i] = Operand<kExact>(wv[i]);
-            // tile j's products are made while tile j - 1's are added up
-            f32x4 p[2][4];
-            float sa = 0.0f;
+            // Two weight tiles at a time: their products are made while the last two's are added up, and the next
+            // activation tile is read meanwhile.  (The scheduling barriers keep the compiler from making all products
+            // first, which takes registers that are not there.)
+            const auto tile = [&](int j) {
+                const int x = j * 16 + r;
+                return join(act[buf][x][run ^ (r % 8)], act[buf][x][(run + 4) ^ (r % 8)]);
+            };
+            f32x4 p[2][2];
+            i32x8 codes = tile(0), ahead = codes;
+            float sa = act_scale[buf][r], last = 0.0f, sa_ahead = 0.0f;
 #pragma unroll
-            for (int j = 0; j <= TT; ++j) {
-                float nsa = 0.0f;
-                if (j < TT) {
-                    const int x = j * 16 + r;
-                    const Operand<kExact> b(join(act[buf][x][run ^ (r % 8)], act[buf][x][(run + 4) ^ (r % 8)]));
-                    nsa = act_scale[buf][x];
-                    block_products(w, b, p[j & 1]);
+            for (int h = 0; h <= 2 * TT; ++h) {
+                const int j = h / 2, i0 = h % 2 * 2;
+                if (i0 == 0 && j + 1 < TT) {
+                    ahead = tile(j + 1);
+                    sa_ahead = act_scale[buf][(j + 1) * 16 + r];
                 }
-                if (j > 0) {
+                if (h < 2 * TT) {
+                    const Operand<kExact> b(codes);
+                    block_products(w, i0, b, p[h & 1]);
+                }
+                if (h > 0) {
+                    const int l0 = 2 - i0, lj = (h - 1) / 2;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float s = sa * sw[kScaleOf[i]];
+                    for (int i = 0; i < 2; ++i) {
+                        const float s = (i0 == 0 ? last : sa) * sw[kScaleOf[l0 + i]];
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) acc[i][j - 1][q] = __builtin_fmaf(p[(j - 1) & 1][i][q], s, acc[i][j - 1][q]);
+                        for (int q = 0; q < 4; ++q) acc[l0 + i][lj][q] = __builtin_fmaf(p[(h - 1) & 1][i][q], s, acc[l0 + i][lj][q]);
                     }
                 }
-                sa = nsa;
+                if (i0 == 2) {
+                    last = sa;
+                    sa = sa_ahead;
+                    codes = ahead;
+                }
                 __builtin_amdgcn_sched_barrier(0);
             }
         };

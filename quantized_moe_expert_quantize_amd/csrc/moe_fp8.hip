@@ -231,9 +231,7 @@ __global__ __launch_bounds__(kGemvThreads) void moe_fp8_gemv_kernel(Fp8Args m, i
 
 // ---- grouped ------------------------------------------------------------------
 
-constexpr int kWaves = 4;
-constexpr int kThreads = 64 * kWaves;
-constexpr int kRowsPerWave = 64;                       // weight rows: four 16-row tiles
+constexpr int kGroups = 4;                             // groups of 64 weight rows (four 16-row tiles) per workgroup
 
 // Asynchronous copies from global memory into LDS, 16 or 4 bytes a lane, to
 // consecutive LDS addresses from `lds` (uniform).  Written as asm because the
@@ -287,11 +285,14 @@ struct GroupedTables {
 // tile i is column 16*i + r, four columns a lane and tile; 16 bits, column
 // 32*(i/2) + 8*(r/4) + 4*(i%2) + r%4, eight a lane and pair of tiles.
 // A table tile of more than 16*TT pairs is made by `subs` items.
-template <int TT, int OUT, bool ACT>
-__global__ __launch_bounds__(kThreads, 2) void moe_fp8_grouped_kernel(Fp8Args m, GroupedTables g, int subs)
+template <int TT, int WT, int NB, int OUT, bool ACT>
+__global__ __launch_bounds__(64 * kGroups * WT, 2) void moe_fp8_grouped_kernel(Fp8Args m, GroupedTables g, int subs)
 {
+    static_assert(NB == 2 || WT == 1);
     constexpr bool kExact = OUT == FTQ_F32;
-    constexpr int BM = 16 * TT;
+    constexpr int kWaves = kGroups * WT, kThreads = 64 * kWaves;
+    constexpr int BM = 16 * TT * WT;                   // pairs per workgroup
+    constexpr int kShare = 8 / WT;                     // copies of its group's weight rows that a wave makes
     constexpr int kRuns = BM * 8 / kThreads;           // 16-byte runs of an activation tile per thread
     constexpr int kCols = ACT ? 32 : 64;               // output columns per wave
     constexpr bool kWide = OUT == FTQ_F32;
@@ -301,17 +302,18 @@ __global__ __launch_bounds__(kThreads, 2) void moe_fp8_grouped_kernel(Fp8Args m,
     constexpr int kScales = ACT ? (kWide ? 3 : 2) : 1;
     constexpr int kScaleOf[4] = {0, 0, ACT ? 1 : 0, kScales - 1};
     __shared__ i32x4 act[2][BM][8];                    // run c of row x sits at c ^ (x % 8)
-    __shared__ i32x4 weight[kWaves][64][8];            // each wave's rows of block kb, swizzled likewise
+    __shared__ i32x4 weight[NB][kGroups][64][8];       // each group's rows, swizzled likewise
     __shared__ float act_scale[2][BM < 64 ? 64 : BM];
     __shared__ int32_t pair_of[BM];
     const int lane = threadIdx.x & 63, wave = uniform((int32_t)(threadIdx.x >> 6));
+    const int group = wave % kGroups, half = wave / kGroups;   // weight rows, pairs
     const int r = lane & 15, run = lane >> 4;
     const int64_t cols = ACT ? m.N / 2 : m.N;
     const int64_t total = (int64_t)g.tiles[m.E + 1] * subs * g.ntn, full = m.K / kFp8Block;
     // each XCD takes a contiguous eighth of the items, so that what its workgroups share meets in its L2
     const int64_t per = (total + kXcds - 1) / kXcds, end = min(total, (int64_t)(blockIdx.x % kXcds + 1) * per);
     for (int64_t item = blockIdx.x % kXcds * per + blockIdx.x / kXcds; item < end; item += gridDim.x / kXcds) {
-        const int64_t mt = item / g.ntn, c0 = (item - mt * g.ntn) * (kWaves * kCols) + wave * kCols;
+        const int64_t mt = item / g.ntn, c0 = (item - mt * g.ntn) * (kGroups * kCols) + group * kCols;
         const int sub = (int)(mt % subs) * BM;
         const int4 td = g.tdesc[mt / subs];
         const int4 desc{uniform(td.x), uniform(td.y) + sub, 0, 0};
@@ -321,7 +323,7 @@ __global__ __launch_bounds__(kThreads, 2) void moe_fp8_grouped_kernel(Fp8Args m,
         if (threadIdx.x < BM) pair_of[threadIdx.x] = g.sorted[desc.y + min((int)threadIdx.x, rows - 1)];
         __syncthreads();
         if (desc.x >= m.E) {                           // masked pairs: zero rows
-            const int64_t first = c0 - wave * kCols, n = min((int64_t)(kWaves * kCols), cols - first);
+            const int64_t first = c0 - group * kCols, n = min((int64_t)(kGroups * kCols), cols - first);
             for (int64_t i = threadIdx.x; i < rows * n; i += kThreads) store1<OUT>(m.out, pair_of[i / n] * cols + first + i % n, 0.0f);
             continue;
         }
@@ -341,13 +343,14 @@ __global__ __launch_bounds__(kThreads, 2) void moe_fp8_grouped_kernel(Fp8Args m,
         // bytes are one request (lanes in operand order, one row each, read 16 bytes a cycle); lane l takes the
         // 16-byte run (l%8) ^ (l/8) of its row
         const int cr = lane / 8, cp = (lane % 8) ^ cr;
-        uint32_t woff[8];
+        uint32_t woff[kShare];
+        static_assert(!ACT || kShare == 8 || kShare == 4);
 #pragma unroll
-        for (int d = 0; d < 8; ++d) {
-            const int i = d / 2, y = d % 2 * 8 + cr;   // tile and row of it
+        for (int e = 0; e < kShare; ++e) {
+            const int d = half * kShare + e, i = d / 2, y = d % 2 * 8 + cr;   // tile and row of it
             const int t = ACT ? i & 1 : i;             // tile among those of its columns
             const int c = kWide ? 16 * t + y : 32 * (t / 2) + 8 * (y / 4) + 4 * (t & 1) + y % 4;
-            woff[d] = (uint32_t)min((int64_t)c, cols - 1 - cb) * (uint32_t)m.K + cp * 16;
+            woff[e] = (uint32_t)min((int64_t)c, cols - 1 - cb) * (uint32_t)m.K + cp * 16;
         }
         const uint8_t* arow[kRuns];                    // rows (i*4 + wave)*8 + l/8
 #pragma unroll
@@ -362,18 +365,19 @@ __global__ __launch_bounds__(kThreads, 2) void moe_fp8_grouped_kernel(Fp8Args m,
 #pragma unroll
             for (int i = 0; i < kScales; ++i) next[i] = wscale[i][kb];
 #pragma unroll
-            for (int d = 0; d < 8; ++d) copy16(lds_address(&weight[wave][8 * d][0]), wbase[ACT ? d / 4 : 0] + kb * kFp8Block, woff[d]);
+            for (int e = 0; e < kShare; ++e) {
+                const uint8_t* base = ACT ? (kShare == 8 ? wbase[e / 4] : half ? wbase[ACT ? 1 : 0] : wbase[0]) : wbase[0];
+                copy16(lds_address(&weight[NB == 2 ? buf : 0][group][8 * (half * kShare + e)][0]), base + kb * kFp8Block, woff[e]);
+            }
 #pragma unroll
             for (int i = 0; i < kRuns; ++i) copy16(lds_address(&act[buf][(i * kWaves + wave) * 8][0]), arow[i] + kb * kFp8Block);
             if (wave < kScaleWaves) copy4(lds_address(&act_scale[buf][wave * 64]), ascale + kb);
         };
         i32x8 wv[4];
         float sw[kScales];
-        const auto read_weights = [&]() {
+        const auto read_weights = [&](int buf) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) wv[i] = join(weight[wave][16 * i + r][run ^ (r % 8)], weight[wave][16 * i + r][(run + 4) ^ (r % 8)]);
-#pragma unroll
-            for (int i = 0; i < kScales; ++i) sw[i] = next[i];
+            for (int i = 0; i < 4; ++i) wv[i] = join(weight[buf][group][16 * i + r][run ^ (r % 8)], weight[buf][group][16 * i + r][(run + 4) ^ (r % 8)]);
         };
         f32x4 acc[4][TT] = {};
         const auto multiply = [&](int buf) {
@@ -384,18 +388,18 @@ __global__ __launch_bounds__(kThreads, 2) void moe_fp8_grouped_kernel(Fp8Args m,
             // activation tile is read meanwhile.  (The scheduling barriers keep the compiler from making all products
             // first, which takes registers that are not there.)
             const auto tile = [&](int j) {
-                const int x = j * 16 + r;
+                const int x = half * 16 * TT + j * 16 + r;
                 return join(act[buf][x][run ^ (r % 8)], act[buf][x][(run + 4) ^ (r % 8)]);
             };
             f32x4 p[2][2];
             i32x8 codes = tile(0), ahead = codes;
-            float sa = act_scale[buf][r], last = 0.0f, sa_ahead = 0.0f;
+            float sa = act_scale[buf][half * 16 * TT + r], last = 0.0f, sa_ahead = 0.0f;
 #pragma unroll
             for (int h = 0; h <= 2 * TT; ++h) {
                 const int j = h / 2, i0 = h % 2 * 2;
                 if (i0 == 0 && j + 1 < TT) {
                     ahead = tile(j + 1);
-                    sa_ahead = act_scale[buf][(j + 1) * 16 + r];
+                    sa_ahead = act_scale[buf][half * 16 * TT + (j + 1) * 16 + r];
                 }
                 if (h < 2 * TT) {
                     const Operand<kExact> b(codes);
@@ -415,27 +419,45 @@ __global__ __launch_bounds__(kThreads, 2) void moe_fp8_grouped_kernel(Fp8Args m,
                     sa = sa_ahead;
                     codes = ahead;
                 }
+                if constexpr (!kExact) {               // a product, then the four sums of one made two products ago
+                    __builtin_amdgcn_sched_group_barrier(0x100, 3, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x002, 5, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x002, 5, 0);
+                }
                 __builtin_amdgcn_sched_barrier(0);
             }
         };
         if (full > 0) copy_block(0, 0);
         for (int64_t kb = 0; kb < full; ++kb) {
+            const int buf = kb & 1;
             wait_copies();
             block_barrier();                           // every wave's copies of block kb are there, block kb - 1 has been read
-            read_weights();
-            wait_lds();                                // a wave's weights have one buffer: read before the next copy
-            if (kb + 1 < full) copy_block(kb + 1, (kb + 1) & 1);
-            multiply(kb & 1);
+            if constexpr (NB == 2) {
+#pragma unroll
+                for (int i = 0; i < kScales; ++i) sw[i] = next[i];
+                if (kb + 1 < full) copy_block(kb + 1, buf ^ 1);
+                read_weights(buf);
+            } else {
+                read_weights(0);
+                wait_lds();                            // a wave's weights have one buffer: read before the next copy
+#pragma unroll
+                for (int i = 0; i < kScales; ++i) sw[i] = next[i];
+                if (kb + 1 < full) copy_block(kb + 1, buf ^ 1);
+            }
+            if (WT == 1 || half * 16 * TT < rows) multiply(buf);
         }
         if (full < g.nb) {                             // the last block is cut short: zeros past K on both sides
             const int buf = full & 1;
             const int64_t k0 = full * kFp8Block;
             const bool in = k0 + cp * 16 < m.K;
 #pragma unroll
-            for (int d = 0; d < 8; ++d) {
+            for (int e = 0; e < kShare; ++e) {
+                const uint8_t* base = ACT ? (kShare == 8 ? wbase[e / 4] : half ? wbase[ACT ? 1 : 0] : wbase[0]) : wbase[0];
                 i32x4 v = {0, 0, 0, 0};
-                if (in) v = *reinterpret_cast<const i32x4*>(wbase[ACT ? d / 4 : 0] + k0 + woff[d]);
-                weight[wave][8 * d + cr][lane % 8] = v;
+                if (in) v = *reinterpret_cast<const i32x4*>(base + k0 + woff[e]);
+                weight[NB == 2 ? buf : 0][group][8 * (half * kShare + e) + cr][lane % 8] = v;
             }
 #pragma unroll
             for (int i = 0; i < kRuns; ++i) {
@@ -445,14 +467,14 @@ __global__ __launch_bounds__(kThreads, 2) void moe_fp8_grouped_kernel(Fp8Args m,
             }
             if (threadIdx.x < BM) act_scale[buf][threadIdx.x] = ascale[full];
 #pragma unroll
-            for (int i = 0; i < kScales; ++i) next[i] = wscale[i][full];
+            for (int i = 0; i < kScales; ++i) sw[i] = wscale[i][full];
             block_barrier();
-            read_weights();
+            read_weights(NB == 2 ? buf : 0);
             multiply(buf);
         }
 #pragma unroll
         for (int j = 0; j < TT; ++j) {
-            const int x = j * 16 + r;
+            const int x = half * 16 * TT + j * 16 + r;
             if (x >= rows) continue;
             const int64_t o = pair_of[x] * cols;
 #pragma unroll
@@ -490,18 +512,27 @@ int launch_gemv(const Fp8Args& m, hipStream_t s)
                   kGemvThreads, 0, s, m, nb, nr, ntiles, by_pair);
 }
 
+// Tables of tile_m pairs a tile, walked in parts of 16*TT*WT.
+template <int TT, int WT, int NB, int OUT, bool ACT>
+int launch_tile(const Fp8Args& m, const GroupedTables& g, int64_t tile_m, int64_t max_tiles, hipStream_t s)
+{
+    const int subs = (int)(tile_m / (16 * TT * WT));
+    const int64_t grid = std::min((max_tiles * subs * g.ntn + kXcds - 1) / kXcds * kXcds, kMaxGrid);
+    return launch("moe_fp8_grouped_kernel", moe_fp8_grouped_kernel<TT, WT, NB, OUT, ACT>, grid, 64 * kGroups * WT, 0, s, m, g, subs);
+}
+
 template <int OUT, bool ACT>
 int launch_grouped(const Fp8Args& m, const GroupedTables& g, int64_t tile_m, int64_t max_tiles, hipStream_t s)
 {
-    // the exact form's fp16 operands take twice the registers: at most 64 pairs at a time
-    constexpr int kMost = OUT == FTQ_F32 ? 64 : 128;
-    const int subs = (int)((tile_m + kMost - 1) / kMost);
-    const int64_t grid = std::min((max_tiles * subs * g.ntn + kXcds - 1) / kXcds * kXcds, kMaxGrid);
-    if (tile_m / subs == 128) {
-        if constexpr (kMost == 128) return launch("moe_fp8_grouped_kernel<8>", moe_fp8_grouped_kernel<8, OUT, ACT>, grid, kThreads, 0, s, m, g, subs);
+    if constexpr (OUT == FTQ_F32) {
+        if (tile_m >= 128) return launch_tile<4, 2, 2, OUT, ACT>(m, g, tile_m, max_tiles, s);
+        if (tile_m == 64) return launch_tile<4, 1, 1, OUT, ACT>(m, g, tile_m, max_tiles, s);
+    } else {
+        if (tile_m == 256) return launch_tile<8, 2, 2, OUT, ACT>(m, g, tile_m, max_tiles, s);
+        if (tile_m == 128) return launch_tile<8, 1, 1, OUT, ACT>(m, g, tile_m, max_tiles, s);
+        if (tile_m == 64) return launch_tile<4, 1, 1, OUT, ACT>(m, g, tile_m, max_tiles, s);
     }
-    if (tile_m / subs == 64) return launch("moe_fp8_grouped_kernel<4>", moe_fp8_grouped_kernel<4, OUT, ACT>, grid, kThreads, 0, s, m, g, subs);
-    return launch("moe_fp8_grouped_kernel<2>", moe_fp8_grouped_kernel<2, OUT, ACT>, grid, kThreads, 0, s, m, g, subs);
+    return launch_tile<2, 1, 2, OUT, ACT>(m, g, tile_m, max_tiles, s);
 }
 
 // Calls f<OUT, ACT>() for the output type and activation of m.
@@ -542,7 +573,7 @@ int fp8_select_path(int64_t E, int64_t T, int64_t top_k)
 int64_t fp8_tile_m(int64_t E, int64_t T, int64_t top_k)
 {
     const int64_t per_expert = T * top_k / E;
-    return per_expert >= 96 ? 128 : per_expert >= 40 ? 64 : 32;
+    return per_expert >= 192 ? 256 : per_expert >= 96 ? 128 : per_expert >= 40 ? 64 : 32;
 }
 
 int run_fp8_gemv(const Fp8Args& m, hipStream_t s) { return dispatch(m, GemvCall{m, s}); }
@@ -550,7 +581,7 @@ int run_fp8_gemv(const Fp8Args& m, hipStream_t s) { return dispatch(m, GemvCall{
 int run_fp8_grouped(const Fp8Args& m, const BucketPlan& plan, const void* ws, hipStream_t s)
 {
     const uint8_t* base = static_cast<const uint8_t*>(ws);
-    const int64_t cols = m.act ? m.N / 2 : m.N, tile = kWaves * (m.act ? 32 : 64);
+    const int64_t cols = m.act ? m.N / 2 : m.N, tile = kGroups * (m.act ? 32 : 64);
     const GroupedTables g{reinterpret_cast<const int32_t*>(base + plan.off_tiles),
                           reinterpret_cast<const int32_t*>(base + plan.off_sorted),
                           reinterpret_cast<const int4*>(base + plan.off_tdesc),

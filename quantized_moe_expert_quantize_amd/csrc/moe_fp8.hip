@@ -107,21 +107,25 @@ __device__ __forceinline__ void store1(void* out, int64_t i, float v)
     else static_cast<uint16_t*>(out)[i] = OUT == FTQ_F16 ? f16_of_f32(v) : bf16_of_f32(v);
 }
 
-// 16 bytes of consecutive results at any element address (the hardware takes unaligned accesses).
-struct F32x4 { float v[4]; } __attribute__((packed, aligned(4)));
-struct U16x8 { uint16_t v[8]; } __attribute__((packed, aligned(2)));
+// 16 bytes of consecutive results at any element address (the hardware takes
+// unaligned accesses), past the caches: results are written once, and kept in L2
+// they drive out the weights that other workgroups are about to read (second
+// layer, bf16 results: 420 us with plain stores, 346 us so).
+typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint16_t u16x8_any __attribute__((ext_vector_type(8), aligned(2)));
 template <int OUT, int N>
 __device__ __forceinline__ void store_run(void* out, int64_t i, const float (&v)[N])
 {
     if constexpr (OUT == FTQ_F32) {
         static_assert(N == 4);
-        *reinterpret_cast<F32x4*>(static_cast<float*>(out) + i) = F32x4{{v[0], v[1], v[2], v[3]}};
+        const f32x4_any x = {v[0], v[1], v[2], v[3]};
+        __builtin_nontemporal_store(x, reinterpret_cast<f32x4_any*>(static_cast<float*>(out) + i));
     } else {
         static_assert(N == 8);
-        U16x8 h;
+        u16x8_any x;
 #pragma unroll
-        for (int q = 0; q < 8; ++q) h.v[q] = OUT == FTQ_F16 ? f16_of_f32(v[q]) : bf16_of_f32(v[q]);
-        *reinterpret_cast<U16x8*>(static_cast<uint16_t*>(out) + i) = h;
+        for (int q = 0; q < 8; ++q) x[q] = OUT == FTQ_F16 ? f16_of_f32(v[q]) : bf16_of_f32(v[q]);
+        __builtin_nontemporal_store(x, reinterpret_cast<u16x8_any*>(static_cast<uint16_t*>(out) + i));
     }
 }
 

@@ -471,7 +471,15 @@ int ftq_quantize_fp8_weight(const void* w, int dtype, int64_t E, int64_t N, int6
  * ftq_moe_fp8_route and ftq_moe_fp8_routed are the two halves of the call, as
  * ftq_moe_route and ftq_moe_q4_0_q8_1_routed are (the tables differ, so that
  * each matmul wants its own route call): one routing serves every ftq_moe_fp8
- * matmul over the same topk_ids, E, T, top_k, path and workspace.
+ * matmul over the same topk_ids, E, T, top_k, path and workspace.  Both take a
+ * path by name, since FTQ_PATH_AUTO goes by N and K too (FTQ_ERR_INVALID_ARG).
+ *
+ * ftq_moe_fp8_select_path: the path FTQ_PATH_AUTO takes, host arithmetic of the
+ * sizes alone: the GEMV path when T*top_k <= 4096 and either T*top_k <= 4*E or
+ * T*top_k*N*K <= 5e8, the grouped path otherwise; -FTQ_ERR_* for invalid sizes.
+ * ftq_moe_fp8_workspace_bytes: the exact workspace for these sizes and path (0 on
+ * the GEMV path), or -1 for invalid sizes; on the grouped path it depends on E, T
+ * and top_k alone.
  */
 int ftq_moe_fp8_select_path(int64_t E, int64_t N, int64_t K, int64_t T, int64_t top_k);
 

@@ -251,9 +251,9 @@ int check_sizes_fp8(int64_t E, int64_t N, int64_t K, int64_t T, int64_t top_k)
     return FTQ_OK;
 }
 
-int resolve_path_fp8(int path, int64_t E, int64_t T, int64_t top_k)
+int resolve_path_fp8(int path, int64_t E, int64_t N, int64_t K, int64_t T, int64_t top_k)
 {
-    if (path == FTQ_PATH_AUTO) return fp8_select_path(E, T, top_k);
+    if (path == FTQ_PATH_AUTO) return fp8_select_path(E, N, K, T, top_k);
     if (path == FTQ_PATH_GEMV || path == FTQ_PATH_GROUPED) return path;
     return -1;
 }
@@ -271,7 +271,11 @@ int fp8_common(const Fp8Args& m, bool per_pair, void* ws, size_t ws_bytes, int p
             if (m.N % 32 != 0) { set_error("a gated activation needs N %% 32 == 0 here, got %lld", (long long)m.N); return FTQ_ERR_UNSUPPORTED; }
         }
     }
-    const int rp = resolve_path_fp8(path, m.E, m.T, m.top_k);
+    if (phases != (kRoute | kMatmul) && path == FTQ_PATH_AUTO) {
+        set_error("a routing serves matmuls of several sizes: name the path (ftq_moe_fp8_select_path)");
+        return FTQ_ERR_INVALID_ARG;
+    }
+    const int rp = resolve_path_fp8(path, m.E, m.N, m.K, m.T, m.top_k);
     if (rp < 0) { set_error("unknown path %d", path); return FTQ_ERR_INVALID_ARG; }
     const int64_t pairs = m.T * m.top_k;
     if (rp == FTQ_PATH_GEMV && pairs > kFp8GemvMaxPairs) {
@@ -549,14 +553,14 @@ int ftq_moe_fp8_select_path(int64_t E, int64_t N, int64_t K, int64_t T, int64_t 
     clear_error();
     int st = check_sizes_fp8(E, N, K, T, top_k);
     if (st != FTQ_OK) return -st;
-    return fp8_select_path(E, T, top_k);
+    return fp8_select_path(E, N, K, T, top_k);
 }
 
 int64_t ftq_moe_fp8_workspace_bytes(int64_t E, int64_t N, int64_t K, int64_t T, int64_t top_k, int path)
 {
     clear_error();
     if (check_sizes_fp8(E, N, K, T, top_k) != FTQ_OK) return -1;
-    const int rp = resolve_path_fp8(path, E, T, top_k);
+    const int rp = resolve_path_fp8(path, E, N, K, T, top_k);
     if (rp < 0) { set_error("unknown path %d", path); return -1; }
     if (T == 0 || rp == FTQ_PATH_GEMV) return 0;
     return make_bucket_plan(T * top_k, E, fp8_tile_m(E, T, top_k)).bytes;

@@ -202,7 +202,7 @@ struct Fp8Args {
 };
 constexpr int64_t kFp8MaxK = int64_t(1) << 25;   // 64 rows' offsets stay below 2^31
 constexpr int64_t kFp8GemvMaxPairs = 4096;   // the GEMV path finds an expert's pairs by scanning the ids
-int fp8_select_path(int64_t E, int64_t T, int64_t top_k);
+int fp8_select_path(int64_t E, int64_t N, int64_t K, int64_t T, int64_t top_k);
 int64_t fp8_tile_m(int64_t E, int64_t T, int64_t top_k);
 int run_fp8_gemv(const Fp8Args& m, hipStream_t s);
 int run_fp8_grouped(const Fp8Args& m, const BucketPlan& plan, const void* ws, hipStream_t s);

@@ -136,24 +136,28 @@ __device__ __forceinline__ bool expert_ok(int32_t id, int64_t E) { return id >= 
 constexpr int kGemvWaves = 8;
 constexpr int kGemvThreads = 64 * kGemvWaves;
 
-// A workgroup takes 16 output columns of one expert: one 16-row weight tile, or
-// with ACT the gate and the up tile of the columns.  by_pair: workgroups are laid
-// out over the pairs, and the one of an expert's first pair serves all its
-// pairs (few pairs: no workgroup for an expert that none takes); else over the
-// experts and, last, the masked pairs.
-template <int OUT, bool ACT>
+// A workgroup takes 16*CT output columns of one expert: CT 16-row weight tiles, or
+// with ACT the gate and the up tiles of the columns, and wave v every eighth block
+// of K from block v on.  What keeps enough loads in flight is the number of waves:
+// loading two or four blocks ahead in registers costs waves and lost 10 to 40%.
+// by_pair: workgroups are laid out over the pairs, and the one of an expert's
+// first pair serves all its pairs (few pairs: no workgroup for an expert that none
+// takes); else over the experts and, last, the masked pairs.
+constexpr int64_t kGemvWideFrom = 16 * 1024;   // columns over all experts from which a workgroup takes 32
+
+template <int CT, int OUT, bool ACT>
 __global__ __launch_bounds__(kGemvThreads) void moe_fp8_gemv_kernel(Fp8Args m, int64_t nb, int64_t nr, int64_t ntiles,
                                                                     int by_pair)
 {
-    constexpr int RT = ACT ? 2 : 1;
+    constexpr int RT = ACT ? 2 * CT : CT, kCols = 16 * CT;
     __shared__ uint16_t list[kFp8GemvMaxPairs];
     __shared__ int count_lds;
     __shared__ f32x4 part[kGemvWaves][RT][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t slot = blockIdx.x / ntiles, n0 = (blockIdx.x - slot * ntiles) * 16;
+    const int lane = threadIdx.x & 63, wave = uniform((int32_t)(threadIdx.x >> 6));
+    const int64_t slot = blockIdx.x / ntiles, n0 = (blockIdx.x - slot * ntiles) * kCols;
     const int pairs = (int)(m.T * m.top_k);
     const int64_t cols = ACT ? m.N / 2 : m.N;
-    const int32_t e = by_pair ? m.ids[slot] : slot < m.E ? (int32_t)slot : -1;
+    const int32_t e = by_pair ? uniform(m.ids[slot]) : slot < m.E ? (int32_t)slot : -1;
     const bool live = expert_ok(e, m.E);
     // the pairs of this expert (or the masked ones), ascending
     if (wave == 0) {
@@ -172,8 +176,8 @@ __global__ __launch_bounds__(kGemvThreads) void moe_fp8_gemv_kernel(Fp8Args m, i
     const int count = count_lds;
     if (count == 0 || (by_pair && list[0] != slot)) return;
     if (!live) {
-        for (int i = threadIdx.x; i < count * 16; i += kGemvThreads) {
-            if (n0 + i % 16 < cols) store1<OUT>(m.out, list[i / 16] * cols + n0 + i % 16, 0.0f);
+        for (int i = threadIdx.x; i < count * kCols; i += kGemvThreads) {
+            if (n0 + i % kCols < cols) store1<OUT>(m.out, list[i / kCols] * cols + n0 + i % kCols, 0.0f);
         }
         return;
     }
@@ -182,14 +186,14 @@ __global__ __launch_bounds__(kGemvThreads) void moe_fp8_gemv_kernel(Fp8Args m, i
     const float* wscale[RT];
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
-        const int64_t n = min(n0 + r, cols - 1) + i * cols;
-        wrow[i] = m.w + ((int64_t)e * m.N + n) * m.K;
-        // this lane's results are rows 4*run .. 4*run+3: one scale, since tiles of 16 start at multiples of 16
-        wscale[i] = m.w_scale + ((int64_t)e * nr + (min(n0, cols - 1) + i * cols) / kFp8Block) * nb;
+        const int64_t c = n0 + 16 * (i % CT), up = i / CT * cols;
+        wrow[i] = m.w + ((int64_t)e * m.N + min(c + r, cols - 1) + up) * m.K;
+        // a tile has one scale: it starts at a multiple of 16
+        wscale[i] = m.w_scale + ((int64_t)e * nr + (min(c, cols - 1) + up) / kFp8Block) * nb;
     }
     for (int t0 = 0; t0 < count; t0 += 16) {
         const bool have = t0 + r < count;
-        const int64_t arow = have ? list[t0 + r] / m.act_div : 0;
+        const int64_t arow = have ? list[t0 + r] / (int)m.act_div : 0;
         f32x4 acc[RT] = {};
         for (int64_t kb = wave; kb < nb; kb += kGemvWaves) {
             i32x8 a = {};
@@ -214,19 +218,19 @@ __global__ __launch_bounds__(kGemvThreads) void moe_fp8_gemv_kernel(Fp8Args m, i
 #pragma unroll
         for (int i = 0; i < RT; ++i) part[wave][i][lane] = acc[i];
         __syncthreads();
-        if (threadIdx.x < 256) {
-            // thread h: column h%16 of activation row h/16 of this pass, its parts in wave order
-            const int c = threadIdx.x % 16, t = threadIdx.x / 16;
-            float y[RT];
+        for (int h = threadIdx.x; h < 16 * kCols; h += kGemvThreads) {
+            // column h%kCols of activation row h/kCols of this pass, its parts in wave order
+            const int c = h % kCols, t = h / kCols;
+            float y[ACT ? 2 : 1];
 #pragma unroll
-            for (int i = 0; i < RT; ++i) {
+            for (int i = 0; i < (ACT ? 2 : 1); ++i) {
                 y[i] = 0.0f;
 #pragma unroll
-                for (int v = 0; v < kGemvWaves; ++v) y[i] += part[v][i][(c / 4) * 16 + t][c % 4];
+                for (int v = 0; v < kGemvWaves; ++v) y[i] += part[v][i * CT + c / 16][c % 16 / 4 * 16 + t][c % 4];
             }
             if (t0 + t < count && n0 + c < cols) {
                 float v = y[0];
-                if constexpr (ACT) v = gated_act(m.act, y[0]) * y[RT - 1];
+                if constexpr (ACT) v = gated_act(m.act, y[0]) * y[ACT ? 1 : 0];
                 store1<OUT>(m.out, list[t0 + t] * cols + n0 + c, v);
             }
         }
@@ -505,15 +509,23 @@ __global__ __launch_bounds__(64 * kGroups * WT, 2) void moe_fp8_grouped_kernel(F
 
 constexpr int64_t kMaxGrid = int64_t(1) << 22;         // workgroups; more tiles than that are walked with a stride
 
+template <int CT, int OUT, bool ACT>
+int launch_gemv_tile(const Fp8Args& m, hipStream_t s)
+{
+    const int64_t cols = ACT ? m.N / 2 : m.N;
+    const int64_t pairs = m.T * m.top_k, ntiles = (cols + 16 * CT - 1) / (16 * CT);
+    const int by_pair = pairs <= m.E + 1;
+    const int64_t nb = (m.K + kFp8Block - 1) / kFp8Block, nr = (m.N + kFp8Block - 1) / kFp8Block;
+    return launch("moe_fp8_gemv_kernel", moe_fp8_gemv_kernel<CT, OUT, ACT>, (by_pair ? pairs : m.E + 1) * ntiles,
+                  kGemvThreads, 0, s, m, nb, nr, ntiles, by_pair);
+}
+
 template <int OUT, bool ACT>
 int launch_gemv(const Fp8Args& m, hipStream_t s)
 {
     const int64_t cols = ACT ? m.N / 2 : m.N;
-    const int64_t pairs = m.T * m.top_k, ntiles = (cols + 15) / 16;
-    const int by_pair = pairs <= m.E + 1;
-    const int64_t nb = (m.K + kFp8Block - 1) / kFp8Block, nr = (m.N + kFp8Block - 1) / kFp8Block;
-    return launch("moe_fp8_gemv_kernel", moe_fp8_gemv_kernel<OUT, ACT>, (by_pair ? pairs : m.E + 1) * ntiles,
-                  kGemvThreads, 0, s, m, nb, nr, ntiles, by_pair);
+    if (std::min(m.T * m.top_k, m.E) * cols >= kGemvWideFrom) return launch_gemv_tile<2, OUT, ACT>(m, s);
+    return launch_gemv_tile<1, OUT, ACT>(m, s);
 }
 
 // Tables of tile_m pairs a tile, walked in parts of 16*TT*WT.
@@ -528,15 +540,13 @@ int launch_tile(const Fp8Args& m, const GroupedTables& g, int64_t tile_m, int64_
 template <int OUT, bool ACT>
 int launch_grouped(const Fp8Args& m, const GroupedTables& g, int64_t tile_m, int64_t max_tiles, hipStream_t s)
 {
-    if constexpr (OUT == FTQ_F32) {
-        if (tile_m >= 128) return launch_tile<4, 2, 2, OUT, ACT>(m, g, tile_m, max_tiles, s);
-        if (tile_m == 64) return launch_tile<4, 1, 1, OUT, ACT>(m, g, tile_m, max_tiles, s);
-    } else {
+    if (tile_m == 32) return launch_tile<2, 1, 2, OUT, ACT>(m, g, tile_m, max_tiles, s);
+    // The exact form walks tall tiles in parts of 64 pairs (second layer, 8191 tokens uniform: 754 us, 803 in parts
+    // of 128 by two waves a weight group).
+    if constexpr (OUT != FTQ_F32) {
         if (tile_m == 256) return launch_tile<8, 2, 2, OUT, ACT>(m, g, tile_m, max_tiles, s);
-        if (tile_m == 128) return launch_tile<8, 1, 1, OUT, ACT>(m, g, tile_m, max_tiles, s);
-        if (tile_m == 64) return launch_tile<4, 1, 1, OUT, ACT>(m, g, tile_m, max_tiles, s);
     }
-    return launch_tile<2, 1, 2, OUT, ACT>(m, g, tile_m, max_tiles, s);
+    return launch_tile<4, 1, 1, OUT, ACT>(m, g, tile_m, max_tiles, s);
 }
 
 // Calls f<OUT, ACT>() for the output type and activation of m.
@@ -568,16 +578,28 @@ struct GroupedCall {
 
 }  // namespace
 
-int fp8_select_path(int64_t E, int64_t T, int64_t top_k)
+// The GEMV needs no routing tables, which cost the grouped path about 12 us, and
+// reads the weights as fast; the grouped path makes the products three to twenty
+// times as fast.  Measured crossovers: with large weights about 4 pairs per expert
+// (128 experts of 1408 x 2816: 4 pairs 106 against 108 us, 8 pairs 126 against
+// 113); with small ones 1 to 2 GFLOP (8 experts of 704 x 1024: 1.5 GFLOP 24
+// against 32 us, 5.9 GFLOP 94 against 34; 16 of 300 x 512: 1.3 GFLOP 38 against 27).
+int fp8_select_path(int64_t E, int64_t N, int64_t K, int64_t T, int64_t top_k)
 {
     const int64_t pairs = T * top_k;
-    return pairs <= kFp8GemvMaxPairs && pairs <= 8 * E ? FTQ_PATH_GEMV : FTQ_PATH_GROUPED;
+    if (pairs > kFp8GemvMaxPairs) return FTQ_PATH_GROUPED;
+    return pairs <= 4 * E || pairs * N <= 500000000 / K ? FTQ_PATH_GEMV : FTQ_PATH_GROUPED;
 }
 
+// Pairs per tile, from the average pairs per expert.  1408 x 2816 weights, 128
+// experts, bf16, evenly spread pairs (all on 8 experts): 32 an expert, tiles of 32
+// / 64 / 256: 129 (51) / 120 (40) / 139 (53) us; 16 an expert 114 (33) / 114 (34) /
+// 134 (52); 96 an expert, 64 / 256: 161 (91) / 161 (104); 128: 187 (106) / 171
+// (111); 256: 290 (192) / 269 (165).
 int64_t fp8_tile_m(int64_t E, int64_t T, int64_t top_k)
 {
     const int64_t per_expert = T * top_k / E;
-    return per_expert >= 192 ? 256 : per_expert >= 96 ? 128 : per_expert >= 40 ? 64 : 32;
+    return per_expert >= 112 ? 256 : per_expert >= 24 ? 64 : 32;
 }
 
 int run_fp8_gemv(const Fp8Args& m, hipStream_t s) { return dispatch(m, GemvCall{m, s}); }

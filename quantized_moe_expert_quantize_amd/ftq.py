@@ -615,8 +615,7 @@ def moe_fp8(w: torch.Tensor, w_scale: torch.Tensor, a: torch.Tensor, a_scale: to
                      stream)
 
 
-def moe_fp8_route(topk_ids: torch.Tensor, E: int, workspace: torch.Tensor | None, path: int = PATH_AUTO,
-                  stream=None) -> None:
+def moe_fp8_route(topk_ids: torch.Tensor, E: int, workspace: torch.Tensor | None, path: int, stream=None) -> None:
     """Group the pairs by expert into `workspace` for moe_fp8_routed (see ftq_moe_fp8_route)."""
     dev = _device_for(topk_ids, "topk_ids")
     T, top_k = topk_ids.shape
@@ -628,7 +627,7 @@ def moe_fp8_route(topk_ids: torch.Tensor, E: int, workspace: torch.Tensor | None
 
 def moe_fp8_routed(w: torch.Tensor, w_scale: torch.Tensor, a: torch.Tensor, a_scale: torch.Tensor,
                    topk_ids: torch.Tensor, E: int, N: int, K: int, out: torch.Tensor, workspace: torch.Tensor | None,
-                   per_pair: bool = False, act: int = 0, path: int = PATH_AUTO, stream=None) -> torch.Tensor:
+                   path: int, per_pair: bool = False, act: int = 0, stream=None) -> torch.Tensor:
     """moe_fp8 on pairs already routed into `workspace` by moe_fp8_route."""
     return _fp8_call(lib().ftq_moe_fp8_routed, w, w_scale, a, a_scale, topk_ids, E, N, K, per_pair, act, out, workspace,
                      path, stream)

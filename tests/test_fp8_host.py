@@ -120,6 +120,18 @@ def test_path_choice():
         for T in (1, 64, 512, 513, 2048, 100000):
             if T * k > 4096:
                 assert ftq.fp8_select_path(E, 64, 256, T, k) == ftq.PATH_GROUPED
+    # at most 4 pairs an expert, or little work in all
+    assert ftq.fp8_select_path(128, 1408, 2816, 64, 8) == ftq.PATH_GEMV
+    assert ftq.fp8_select_path(128, 1408, 2816, 65, 8) == ftq.PATH_GROUPED
+    assert ftq.fp8_select_path(8, 704, 1024, 256, 2) == ftq.PATH_GEMV
+    assert ftq.fp8_select_path(8, 704, 1024, 1024, 2) == ftq.PATH_GROUPED
+
+
+def test_routed_calls_name_their_path():
+    route = ftq.lib().ftq_moe_fp8_route
+    assert route(P(A), 8, 4, 2, P(A), 1 << 20, ftq.PATH_AUTO, None) == ftq.ERR_INVALID_ARG
+    assert _moe(path=0, wk=A, wkb=1 << 20, routed=True) == ftq.ERR_INVALID_ARG
+    assert "path" in ftq.last_error()
 
 
 def test_binding_refuses_host_tensors():

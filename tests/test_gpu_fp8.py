@@ -160,7 +160,8 @@ class Experts:
 # more pairs than experts and fewer, every tile height of the grouped path
 SHAPES = [(1, 1, 16, 1, 1), (2, 5, 16, 3, 1), (8, 64, 256, 4, 2), (8, 100, 144, 5, 2), (4, 130, 400, 7, 3), (8, 257, 512, 33, 2),
           (128, 48, 272, 3, 8), (128, 96, 128, 40, 8), (3, 300, 1040, 50, 2), (8, 192, 384, 300, 2), (2, 513, 640, 200, 1),
-          (16, 260, 1408, 90, 4), (1, 256, 1152, 300, 1), (4095, 16, 32, 9, 5)]
+          (16, 260, 1408, 90, 4), (1, 256, 1152, 300, 1), (4095, 16, 32, 9, 5),
+          (4, 70, 208, 270, 2), (2, 300, 96, 400, 1), (8, 600, 2048, 480, 2), (1, 33, 4112, 513, 1)]
 
 
 @pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "E{}N{}K{}T{}k{}".format(*s))
@@ -176,7 +177,7 @@ def test_shapes(shape, path):
 @pytest.mark.parametrize("path", [ftq.PATH_GEMV, ftq.PATH_GROUPED])
 @pytest.mark.parametrize("act", ["silu", "gelu"])
 def test_activations(path, act):
-    for shape in ((8, 32, 128, 4, 2), (4, 96, 272, 50, 2), (8, 544, 512, 300, 2), (16, 256, 384, 100, 4), (128, 352, 256, 5, 8), (2, 1120, 144, 260, 1)):
+    for shape in ((8, 32, 128, 4, 2), (4, 96, 272, 50, 2), (8, 544, 512, 300, 2), (16, 256, 384, 100, 4), (128, 352, 256, 5, 8), (2, 1120, 144, 260, 1), (3, 1056, 640, 500, 2)):
         say(f"[fp8] act {shape} path={path} {act}")
         Experts(*shape, seed=shape[1], masked=5).check(path, act)
 
@@ -184,7 +185,7 @@ def test_activations(path, act):
 @pytest.mark.parametrize("path", [ftq.PATH_GEMV, ftq.PATH_GROUPED])
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
 def test_output_types(path, dtype):
-    for shape in ((8, 99, 256, 20, 2), (8, 320, 512, 300, 2), (16, 96, 144, 120, 4)):
+    for shape in ((8, 99, 256, 20, 2), (8, 320, 512, 300, 2), (16, 96, 144, 120, 4), (4, 544, 400, 257, 2), (2, 70, 96, 640, 2), (1, 257, 2064, 700, 1)):
         say(f"[fp8] {shape} path={path} {dtype}")
         Experts(*shape, seed=3).check(path, None, dtype)
         if shape[1] % 32 == 0:

@@ -475,8 +475,8 @@ int ftq_quantize_fp8_weight(const void* w, int dtype, int64_t E, int64_t N, int6
  * path by name, since FTQ_PATH_AUTO goes by N and K too (FTQ_ERR_INVALID_ARG).
  *
  * ftq_moe_fp8_select_path: the path FTQ_PATH_AUTO takes, host arithmetic of the
- * sizes alone: the GEMV path when T*top_k <= 4096 and either T*top_k <= 4*E or
- * T*top_k*N*K <= 5e8, the grouped path otherwise; -FTQ_ERR_* for invalid sizes.
+ * sizes alone: the GEMV path when T*top_k <= 4096 and either T*top_k <= 2*E or
+ * T*top_k*N*K <= 2e8 (about), the grouped path otherwise; -FTQ_ERR_* for invalid sizes.
  * ftq_moe_fp8_workspace_bytes: the exact workspace for these sizes and path (0 on
  * the GEMV path), or -1 for invalid sizes; on the grouped path it depends on E, T
  * and top_k alone.

@@ -580,15 +580,17 @@ struct GroupedCall {
 
 // The GEMV needs no routing tables, which cost the grouped path about 12 us, and
 // reads the weights as fast; the grouped path makes the products three to twenty
-// times as fast.  Measured crossovers: with large weights about 4 pairs per expert
-// (128 experts of 1408 x 2816: 4 pairs 106 against 108 us, 8 pairs 126 against
-// 113); with small ones 1 to 2 GFLOP (8 experts of 704 x 1024: 1.5 GFLOP 24
-// against 32 us, 5.9 GFLOP 94 against 34; 16 of 300 x 512: 1.3 GFLOP 38 against 27).
+// times as fast, which counts sooner when the pairs crowd on few experts.  GEMV
+// against grouped, pairs evenly spread (all on the same top_k experts), in us:
+// 128 experts of 1408 x 2816, 2 pairs an expert 88 / 102 (21 / 30), 4 pairs 106 /
+// 108 (39 / 31), 8 pairs 126 / 113; 8 of 28672 x 4096, 2 pairs 162 / 170 (42 / 44),
+// 8 pairs 167 / 171 (89 / 50).  Little work in all: 16 of 300 x 512, pairs*N*K =
+// 1.6e8, 12 / 22 (24 / 22); 8 of 704 x 1024, 3.7e8, 14 / 25 (30 / 25), 3e9, 94 / 34.
 int fp8_select_path(int64_t E, int64_t N, int64_t K, int64_t T, int64_t top_k)
 {
     const int64_t pairs = T * top_k;
     if (pairs > kFp8GemvMaxPairs) return FTQ_PATH_GROUPED;
-    return pairs <= 4 * E || pairs * N <= 500000000 / K ? FTQ_PATH_GEMV : FTQ_PATH_GROUPED;
+    return pairs <= 2 * E || pairs * N <= 200000000 / K ? FTQ_PATH_GEMV : FTQ_PATH_GROUPED;
 }
 
 // Pairs per tile, from the average pairs per expert.  1408 x 2816 weights, 128

@@ -120,10 +120,10 @@ def test_path_choice():
         for T in (1, 64, 512, 513, 2048, 100000):
             if T * k > 4096:
                 assert ftq.fp8_select_path(E, 64, 256, T, k) == ftq.PATH_GROUPED
-    # at most 4 pairs an expert, or little work in all
-    assert ftq.fp8_select_path(128, 1408, 2816, 64, 8) == ftq.PATH_GEMV
-    assert ftq.fp8_select_path(128, 1408, 2816, 65, 8) == ftq.PATH_GROUPED
-    assert ftq.fp8_select_path(8, 704, 1024, 256, 2) == ftq.PATH_GEMV
+    # at most 2 pairs an expert, or little work in all
+    assert ftq.fp8_select_path(128, 1408, 2816, 32, 8) == ftq.PATH_GEMV
+    assert ftq.fp8_select_path(128, 1408, 2816, 33, 8) == ftq.PATH_GROUPED
+    assert ftq.fp8_select_path(8, 704, 1024, 128, 2) == ftq.PATH_GEMV
     assert ftq.fp8_select_path(8, 704, 1024, 1024, 2) == ftq.PATH_GROUPED
 
 

@@ -16,6 +16,10 @@
  * and 64-bit size arithmetic (mlxcel PR #652, "fix(cuda/quantized): chunk
  * long-prompt qmm launches to avoid gridDim>65535 and int overflow", Summary).
  *
+ * Around it: quantisers, the top-k combine, the fused gated activation, other
+ * GGUF weight types, the router (ftq_moe_topk), and the same matmul for experts
+ * in 8-bit floating point with one scale per 128 x 128 block (ftq_moe_fp8).
+ *
  * Block formats (GGUF; the pages name them, the layouts are the GGUF ones):
  *   Q4_0 block, 18 bytes: fp16 d, then 16 bytes; byte i holds element i in its
  *       low nibble and element i+16 in its high nibble; value = (nibble-8)*d.

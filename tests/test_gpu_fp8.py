@@ -390,6 +390,62 @@ def test_two_streams_at_once():
             assert torch.equal(a, b)
 
 
+def test_the_layer_on_another_stream():
+    """Every call on a stream that is not the current one, or that was made current."""
+    E, N2, K, k, T = 16, 128, 256, 4, 150
+    args = _layer_inputs(T, E, N2, K, 5)
+    want = _layer(*args, k, E, N2, K, ftq.ACT_SILU, ftq.PATH_AUTO)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        got = _layer(*args, k, E, N2, K, ftq.ACT_SILU, ftq.PATH_AUTO)
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    x, logits, w13, s13 = args[:4]
+    ids, gates = ftq.moe_topk(logits, k, score=ftq.SCORE_SIGMOID, bias=args[6], n_group=4, topk_group=2, group_top=2, scale=2.5, stream=s)
+    a, as_ = ftq.quantize_fp8(x, stream=s)
+    h = ftq.moe_fp8(w13, s13, a, as_, ids, E, 2 * N2, K, act=ftq.ACT_SILU, out_dtype=torch.bfloat16, stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(ids, want[0]) and torch.equal(gates, want[1]) and torch.equal(h, want[2])
+
+
+def test_no_tokens():
+    c = Experts(8, 64, 256, 4, 2)
+    z = torch.zeros(0, 2, dtype=torch.int32, device="cuda")
+    for path in (ftq.PATH_AUTO, ftq.PATH_GEMV, ftq.PATH_GROUPED):
+        assert ftq.moe_fp8(c.w, c.ws, c.a[:0], c.as_[:0], z, 8, 64, 256, path=path).shape == (0, 64)
+    assert ftq.quantize_fp8(torch.zeros(0, 256, device="cuda"))[1].shape == (0, 2)
+    assert ftq.quantize_fp8_weight(torch.zeros(0, 4, 256, device="cuda"))[0].shape == (0, 4, 256)
+
+
+def test_two_graphs_with_a_workspace_each():
+    """Two captured matmuls replayed in turn, with other routings than the ones they were captured with."""
+    cases = [Experts(8, 256, 384, 300, 2, seed=s) for s in (1, 2)]
+    graphs, outs = [], []
+    for c in cases:
+        ws = torch.empty(ftq.fp8_workspace_bytes(8, 256, 384, 300, 2, ftq.PATH_GROUPED), dtype=torch.uint8, device="cuda")
+        out = torch.empty(600, 256, device="cuda")
+        call = lambda c=c, ws=ws, out=out: ftq.moe_fp8(c.w, c.ws, c.a, c.as_, c.ids, 8, 256, 384, path=ftq.PATH_GROUPED, out=out, workspace=ws)  # noqa: E731
+        call()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call()
+        graphs.append((g, ws))
+        outs.append(out)
+    for seed in range(4):
+        want = []
+        for i, c in enumerate(cases):
+            c.ids.copy_(torch.from_numpy(inputs.routing(300, 8, 2, seed=10 * seed + i, kind="zipf")))
+            want.append(c.run(ftq.PATH_GROUPED))
+        for g, _ in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(outs, want):
+            assert torch.equal(a, b)
+
+
 def test_binding_refuses():
     c = Experts(8, 64, 256, 4, 2)
     call = lambda **kw: ftq.moe_fp8(**{**dict(w=c.w, w_scale=c.ws, a=c.a, a_scale=c.as_, topk_ids=c.ids, E=8, N=64, K=256), **kw})  # noqa: E731

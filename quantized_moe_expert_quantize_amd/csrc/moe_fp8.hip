@@ -251,14 +251,17 @@ constexpr int kGroups = 4;                             // groups of 64 weight ro
 // consecutive LDS addresses from `lds` (uniform).  Written as asm because the
 // compiler, which cannot tell the buffers of successive K blocks apart, would wait
 // for a copy in flight before every LDS read; the copies have no result
-// registers, and wait_copies() is the only thing that orders them.
+// registers, and wait_copies() is the only thing that orders them.  The wait states
+// that the compiler would put in: one between a write of m0 and the copy, and five
+// between a vector instruction's write of a scalar register and a copy that takes
+// its address from it.
 __device__ __forceinline__ uint32_t lds_address(const void* p)
 {
     return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const uint8_t*)(const uint8_t*)p;
 }
 __device__ __forceinline__ void copy16(uint32_t lds, const uint8_t* base, uint32_t off)
 {
-    __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory", "m0");
+    __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory", "m0");
 }
 __device__ __forceinline__ void copy16(uint32_t lds, const uint8_t* p)
 {

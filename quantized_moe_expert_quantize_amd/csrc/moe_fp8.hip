@@ -148,19 +148,20 @@ constexpr int kGemvThreads = 64 * kGemvWaves;
 // loading two or four blocks ahead in registers costs waves and lost 10 to 40%.
 // by_pair: workgroups are laid out over the pairs, and the one of an expert's
 // first pair serves all its pairs (few pairs: no workgroup for an expert that none
-// takes); else over the experts and, last, the masked pairs.
+// takes); else over the experts and, last, the masked pairs.  More workgroups than
+// a launch takes are several launches, each from workgroup `first` on.
 constexpr int64_t kGemvWideFrom = 16 * 1024;   // columns over all experts from which a workgroup takes 32
 
 template <int CT, int OUT, bool ACT>
 __global__ __launch_bounds__(kGemvThreads) void moe_fp8_gemv_kernel(Fp8Args m, int64_t nb, int64_t nr, int64_t ntiles,
-                                                                    int by_pair)
+                                                                    int by_pair, int64_t first)
 {
     constexpr int RT = ACT ? 2 * CT : CT, kCols = 16 * CT;
     __shared__ uint16_t list[kFp8GemvMaxPairs];
     __shared__ int count_lds;
     __shared__ f32x4 part[kGemvWaves][RT][64];
     const int lane = threadIdx.x & 63, wave = uniform((int32_t)(threadIdx.x >> 6));
-    const int64_t slot = blockIdx.x / ntiles, n0 = (blockIdx.x - slot * ntiles) * kCols;
+    const int64_t item = first + blockIdx.x, slot = item / ntiles, n0 = (item - slot * ntiles) * kCols;
     const int pairs = (int)(m.T * m.top_k);
     const int64_t cols = ACT ? m.N / 2 : m.N;
     const int32_t e = by_pair ? uniform(m.ids[slot]) : slot < m.E ? (int32_t)slot : -1;
@@ -522,7 +523,7 @@ __global__ __launch_bounds__(64 * kGroups * WT, 2) void moe_fp8_grouped_kernel(F
     }
 }
 
-constexpr int64_t kMaxGrid = int64_t(1) << 22;         // workgroups; more tiles than that are walked with a stride
+constexpr int64_t kMaxGrid = int64_t(1) << 22;         // workgroups of a launch
 
 template <int CT, int OUT, bool ACT>
 int launch_gemv_tile(const Fp8Args& m, hipStream_t s)
@@ -531,8 +532,13 @@ int launch_gemv_tile(const Fp8Args& m, hipStream_t s)
     const int64_t pairs = m.T * m.top_k, ntiles = (cols + 16 * CT - 1) / (16 * CT);
     const int by_pair = pairs <= m.E + 1;
     const int64_t nb = (m.K + kFp8Block - 1) / kFp8Block, nr = (m.N + kFp8Block - 1) / kFp8Block;
-    return launch("moe_fp8_gemv_kernel", moe_fp8_gemv_kernel<CT, OUT, ACT>, (by_pair ? pairs : m.E + 1) * ntiles,
-                  kGemvThreads, 0, s, m, nb, nr, ntiles, by_pair);
+    const int64_t items = (by_pair ? pairs : m.E + 1) * ntiles;
+    for (int64_t first = 0; first < items; first += kMaxGrid) {
+        const int st = launch("moe_fp8_gemv_kernel", moe_fp8_gemv_kernel<CT, OUT, ACT>, std::min(items - first, kMaxGrid),
+                              kGemvThreads, 0, s, m, nb, nr, ntiles, by_pair, first);
+        if (st != FTQ_OK) return st;
+    }
+    return FTQ_OK;
 }
 
 template <int OUT, bool ACT>
@@ -543,7 +549,7 @@ int launch_gemv(const Fp8Args& m, hipStream_t s)
     return launch_gemv_tile<1, OUT, ACT>(m, s);
 }
 
-// Tables of tile_m pairs a tile, walked in parts of 16*TT*WT.
+// Tables of tile_m pairs a tile, walked in parts of 16*TT*WT, with a stride if there are more than a launch takes.
 template <int TT, int WT, int NB, int OUT, bool ACT>
 int launch_tile(const Fp8Args& m, const GroupedTables& g, int64_t tile_m, int64_t max_tiles, hipStream_t s)
 {

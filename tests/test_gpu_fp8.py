@@ -311,6 +311,29 @@ def test_offsets_past_32_bits():
         del a, out
 
 
+@pytest.mark.parametrize("E", [4095, 4094], ids=["by_pair", "by_expert"])
+def test_gemv_of_more_workgroups_than_a_launch_takes(E):
+    """4096 pairs times 2049 column tiles: more than 2^32 work-items."""
+    T, N, K = 4096, 65568, 16
+    say(f"[fp8] gemv work-items past 2^32 E={E}")
+    w = torch.zeros(E, N, K, dtype=torch.uint8, device="cuda")
+    a = torch.zeros(T, K, dtype=torch.uint8, device="cuda")
+    w[:, :2] = w[:, -3:] = 0x38                     # 1.0
+    a[:, 5] = 0x40                                  # 2.0
+    ws, as_ = torch.ones(E, 513, 1, device="cuda"), torch.ones(T, 1, device="cuda")
+    ids = torch.full((T, 1), -1, dtype=torch.int32, device="cuda")
+    live = {0: 0, 2047: 17, 2048: 17, 3000: 2049, T - 1: E - 1}
+    for p, e in live.items():
+        ids[p] = e
+    out = torch.full((T, N), 5.0, dtype=torch.bfloat16, device="cuda")
+    ftq.moe_fp8(w.view(ftq.FP8), ws, a.view(ftq.FP8), as_, ids, E, N, K, path=ftq.PATH_GEMV, out=out)
+    torch.cuda.synchronize()
+    p = list(live)
+    assert (out[p, :2] == 2.0).all() and (out[p, -3:] == 2.0).all() and (out[p, 2:-3] == 0).all()
+    out[p] = 0
+    assert (out == 0).all()
+
+
 # ---- streams, graphs, the whole layer ----------------------------------------------
 
 def _layer(x, logits, w13, s13, w2, s2, bias, k, E, N2, K, act, path, bufs=None):

@@ -245,10 +245,10 @@ __device__ __forceinline__ uint32_t order_of(float f)
 }
 __device__ __forceinline__ float value_of(uint32_t k) { return as_f(k ^ (~(uint32_t)((int32_t)k >> 31) | 0x80000000u)); }
 
-// Bytes of LDS of one row: candidates' values and ids, the lanes' two best values, runs' scores, logits.
+// Bytes of LDS of one row: candidates' values and ids, the lanes' two best values, runs' scores with their errors, logits.
 __host__ __device__ constexpr int64_t quick_lds(int64_t E, int64_t n_group, int64_t lanes)
 {
-    return lanes * 8 + lanes * 4 + (n_group > 1 ? lanes * 8 + (n_group + 1) / 2 * 8 : 0) + (E + 1) / 2 * 8;
+    return lanes * 8 + lanes * 4 + (n_group > 1 ? (lanes + n_group) * 8 : 0) + (E + 1) / 2 * 8;
 }
 
 // A row in 32 bits, its candidates in 64.  False (for all the row's lanes): the row needs exact_row.
@@ -257,8 +257,8 @@ __device__ __forceinline__ bool quick_row(const TopkArgs& m, int64_t row, int su
 {
     double* cand = mem;
     float2* best_lds = reinterpret_cast<float2*>(cand + LPR);
-    float* run_lds = reinterpret_cast<float*>(best_lds + (m.n_group > 1 ? LPR : 0));
-    float* logit_lds = run_lds + (m.n_group > 1 ? (m.n_group + 1) / 2 * 2 : 0);
+    float2* run_lds = best_lds + (m.n_group > 1 ? LPR : 0);
+    float* logit_lds = reinterpret_cast<float*>(run_lds + (m.n_group > 1 ? m.n_group : 0));
     int32_t* cand_id = reinterpret_cast<int32_t*>(logit_lds + (m.E + 1) / 2 * 2);
     constexpr uint32_t kPlace = LPR * EPL - 1;            // low bits of a key: kPlace - expert
     // this lane's experts: e0 + i for i >= first; the last lane's run is moved back to end with the row
@@ -322,7 +322,9 @@ __device__ __forceinline__ bool quick_row(const TopkArgs& m, int64_t row, int su
         const int lanes = m.E / m.n_group / EPL;
         best_lds[sub] = float2{a, b};
         wave_lds_fence();
-        float mine = -kInf;
+        // A run's score and a bound of its error.  Each of the two best values is off by its score's error and by a rounding
+        // of its own size, which the sum of two large ones of opposite sign keeps; the sum adds one more rounding.
+        float mine = -kInf, err = 0.0f;
         if (sub < m.n_group) {
             a = b = -kInf;
 #pragma unroll 4
@@ -332,14 +334,15 @@ __device__ __forceinline__ bool quick_row(const TopkArgs& m, int64_t row, int su
                 a = fmaxf(a, v.x);
             }
             mine = m.group_top == 2 ? a + b : a;
-            run_lds[sub] = mine;
+            const float size = (a > -kInf ? fabsf(a) : 0.0f) + (m.group_top == 2 && b > -kInf ? fabsf(b) : 0.0f);
+            if (by_score) err = 2 * off + 2 * kUlp * size;
+            run_lds[sub] = float2{mine, err};
         }
         wave_lds_fence();
         int above = 0, near = 0;
-        const float tol = by_score ? 4 * off + 4 * kUlp * fabsf(mine) : 0.0f;
 #pragma unroll 4
         for (int g = 0; g < m.n_group; ++g) {
-            const float v = run_lds[g];
+            const float v = run_lds[g].x, tol = err + run_lds[g].y;
             above += by_score ? v > mine + tol : v > mine || (v == mine && g < sub);
             near += !(v < mine - tol);                    // itself among them
         }

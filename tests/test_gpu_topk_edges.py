@@ -3,7 +3,9 @@ import math
 
 import numpy as np
 import pytest
+import torch
 
+from quantized_moe_expert_quantize_amd import ftq
 from tests._cases import say
 from tests.test_gpu_topk import check, logits
 
@@ -50,3 +52,42 @@ def test_group_scores_past_the_range_of_32_bits(score):
         bias = np.repeat(np.float32([b, b / 2, b, b / 4]), 4)
         check(l, 3, "f32", score, bias.astype(np.float32), 4, 2, 2, renorm=False)
         check(l, 3, "f32", score, bias.astype(np.float32), 4, 2, 1, renorm=False)
+
+
+# ---- groups without an available expert -------------------------------------------
+
+def route(l, k, bias=None, n_group=1, topk_group=1, group_top=1, score="sigmoid", renorm=False):
+    ids, gates = ftq.moe_topk(torch.from_numpy(l).cuda(), k, score=ftq.SCORE_SOFTMAX if score == "softmax" else ftq.SCORE_SIGMOID,
+                              bias=None if bias is None else torch.from_numpy(bias).cuda(), n_group=n_group,
+                              topk_group=topk_group, group_top=group_top, renorm=renorm)
+    return ids.cpu().numpy(), gates.cpu().numpy()
+
+
+@pytest.mark.parametrize("E, n_group, alive", [(256, 8, 3), (256, 8, 1), (64, 8, 2), (1024, 16, 5), (8, 4, 1)])
+def test_masked_groups_cost_nothing(E, n_group, alive):
+    """Fewer groups with an available expert than are kept: the choice is that of the same rows without groups, and so
+    are the gates' bits, which the evaluation in 64 bits would round otherwise in some row of many."""
+    T, run = 3000, E // n_group
+    l = logits(T, E, E + alive).reshape(T, n_group, run)
+    rng = np.random.default_rng(E)
+    for t in range(T):
+        l[t, rng.permutation(n_group)[alive:]] = -math.inf
+    l = l.reshape(T, E)
+    k = min(4, alive * run)
+    for group_top in (1, 2):
+        for bias in (None, np.zeros(E, np.float32)):
+            check(l[:200], k, "f32", "sigmoid", bias, n_group, alive + 1, group_top)
+            got = route(l, k, bias, n_group, alive + 1, group_top)
+            want = route(l, k, bias)
+            assert np.array_equal(got[0], want[0]) and np.array_equal(got[1], want[1]), (group_top, bias is None)
+
+
+def test_groups_that_tie_at_minus_infinity():
+    """One available expert in each group, two wanted for a group's score: all groups score -inf, the lower ones stay."""
+    l = np.full((40, 32), -math.inf, np.float32)
+    x = logits(40, 8, 3)
+    l[:, ::4] = x
+    for bias in (None, np.zeros(32, np.float32)):
+        for score in ("softmax", "sigmoid"):
+            gi, _ = check(l, 3, "f32", score, bias, 8, 4, 2)
+            assert (gi < 16).all()

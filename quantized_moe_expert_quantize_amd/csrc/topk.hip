@@ -245,6 +245,32 @@ __device__ __forceinline__ uint32_t order_of(float f)
 }
 __device__ __forceinline__ float value_of(uint32_t k) { return as_f(k ^ (~(uint32_t)((int32_t)k >> 31) | 0x80000000u)); }
 
+constexpr float kLog2e = 1.44269504f, kLog2eRest = 1.92596299e-8f, kLn2 = 0.693147181f;
+
+// x of an exponential, brought to where e^x stays finite; the gates made of what is cut off are below kTiny.
+__device__ __forceinline__ float clamped(float x) { return __builtin_amdgcn_fmed3f(x, -200.0f, 80.0f); }
+
+// e^x by the base-2 exponential of a rounded product: relative error 1.5 |x| 2^-24 and a unit in the last place.
+__device__ __forceinline__ float coarse_exp(float x) { return __builtin_amdgcn_exp2f(clamped(x) * kLog2e); }
+
+// e^(x + rest), rest being small against x: what the product leaves out (its own rounding, that of log2 e, and rest)
+// goes into a factor of its own, so that a unit in the last place and one rounding remain, 3 * 2^-24, whatever x is.
+__device__ __forceinline__ float fine_exp(float x, float rest)
+{
+    const float c = clamped(x), t = c * kLog2e;
+    const float left = __builtin_fmaf(rest, kLog2e, __builtin_fmaf(c, kLog2eRest, __builtin_fmaf(c, kLog2e, -t)));
+    const float e = __builtin_amdgcn_exp2f(t);
+    return __builtin_fmaf(e, left * kLn2, e);
+}
+
+// e^(v - mx): the difference with its rounding error (the sum of two values and what it lacks, after Knuth).
+__device__ __forceinline__ float exp_below(float v, float mx)
+{
+    const float x = v - mx, back = x - v;
+    const float rest = (v - (x - back)) + (-mx - back);
+    return fine_exp(x, x > -200.0f ? rest : 0.0f);        // -inf and what is clamped has none
+}
+
 // Bytes of LDS of one row: candidates' values and ids, the lanes' two best values, runs' scores with their errors, logits.
 __host__ __device__ constexpr int64_t quick_lds(int64_t E, int64_t n_group, int64_t lanes)
 {
@@ -279,11 +305,8 @@ __device__ __forceinline__ bool quick_row(const TopkArgs& m, int64_t row, int su
         mx = fmaxf(mx, l[i]);
     }
     if (row_vote<LPR>(nan, base)) return false;
-    // Scores: sigmoid, or e^(l - max) (the common divisor only where it matters); 0 for -inf.  The exponential is
-    // the base-2 one of a rounded product: relative error 1.5 |x| 2^-24 and a unit in the last place.
+    // Scores: sigmoid, or e^(l - max) (the common divisor only where it matters); 0 for -inf.
     if (softmax) mx = row_max<LPR>(mx);
-    const auto exponential = [&](float x) { return __builtin_amdgcn_exp2f(__builtin_amdgcn_fmed3f(x, -200.0f, 120.0f) * 1.44269504f); };
-    const auto score = [&](float v) { return softmax ? exponential(v - mx) : __builtin_amdgcn_rcpf(1.0f + exponential(-v)); };
     const bool by_score = m.bias || (m.n_group > 1 && m.group_top > 1);
     float s[EPL];
     float inv = 1.0f;
@@ -291,16 +314,15 @@ __device__ __forceinline__ bool quick_row(const TopkArgs& m, int64_t row, int su
         float sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
-            s[i] = score(l[i]);
+            s[i] = softmax ? exp_below(l[i], mx) : __builtin_amdgcn_rcpf(1.0f + coarse_exp(-l[i]));
             sum += s[i];
         }
         if (softmax) inv = 1.0f / row_sum<LPR>(sum);
     }
-    // `off` bounds the error of a score.  Sigmoid, in units of 2^-23: s (1 - s) (0.75 |x| + 1) <= 0.6 from the
-    // exponential, 0.5 from the sum, 1 from the reciprocal.  Softmax: s (0.75 |x| + 2) <= 2.3 for its own exponential
-    // and quotient, and the same error averaged over all experts (|x| averages at most ln 1024 = 7) and up to 11 for
-    // the sum of 1024: 20.
-    const float off = softmax ? 24 * kUlp : 2.5f * kUlp;
+    // `off` bounds the error of these scores, in units of 2^-23.  Sigmoid: s (1 - s) (0.75 |x| + 1) <= 0.6 from the
+    // exponential, 0.5 from the sum, 1 from the reciprocal.  Softmax: 1.5 for the exponential, the same and half a
+    // unit for each of the 21 (EPL - 1 and 6) additions that a term of the divisor goes through, 1 for the quotient.
+    const float off = softmax ? 16 * kUlp : 2.5f * kUlp;
     uint32_t key[EPL];
     float a = -kInf, b = -kInf;                           // the lane's two largest values for its run's score
 #pragma unroll
@@ -375,7 +397,9 @@ __device__ __forceinline__ bool quick_row(const TopkArgs& m, int64_t row, int su
     wave_lds_fence();
     const int id = mine ? (int)(kPlace - (mine & kPlace)) : -1;
     const float logit = id >= 0 ? logit_lds[id] : -kInf;
-    float g = id >= 0 ? score(logit) : 0.0f;
+    // The gate's score: sigmoid 3 * 2^-24 from the exponential, 1 and 2 from the sum and the reciprocal.
+    float g = softmax ? exp_below(logit, mx) : __builtin_amdgcn_rcpf(1.0f + fine_exp(-logit, 0.0f));
+    if (id < 0) g = 0.0f;
     int rank = sub;
     if (!complete) {
         double v = logit;

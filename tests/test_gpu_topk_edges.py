@@ -7,7 +7,7 @@ import torch
 
 from quantized_moe_expert_quantize_amd import ftq
 from tests._cases import say
-from tests.test_gpu_topk import check, logits
+from tests.test_gpu_topk import check, logits, topk64
 
 pytestmark = pytest.mark.gpu
 
@@ -91,3 +91,27 @@ def test_groups_that_tie_at_minus_infinity():
         for score in ("softmax", "sigmoid"):
             gi, _ = check(l, 3, "f32", score, bias, 8, 4, 2)
             assert (gi < 16).all()
+
+
+# ---- gates to a few units in the last place ----------------------------------------
+
+# Roundings that a gate goes through, in units of 2^-24 relative: softmax: exponential 3 (one unit in the last place, 2,
+# and a product), divisor 3 + 10 (a tree of at most 1024), its reciprocal, the product, the scale: 19; renormalised 3 + (3
+# + 6) + 2 = 14.  Sigmoid: exponential 3, sum 1, reciprocal 2 (one unit in the last place): 6; renormalised 6 + (6 + 6)
+# + 2 = 20.  One more for the products of these.
+GATE_UNITS = 21
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E, k", [(8, 2), (64, 6), (100, 8), (128, 8), (256, 8), (384, 8), (1000, 16), (1024, 64)])
+def test_gates_hold_their_last_places(score, E, k):
+    """Whatever the size of the logits, a gate is within a constant number of roundings."""
+    say(f"[topk] gates {score} E={E} k={k}")
+    for i, (mean, std) in enumerate(((0, 1.5), (0, 12), (-12, 1), (-35, 3), (-60, 1), (1000, 5), (1e6, 3), (17, 0.01))):
+        l = (mean + logits(300, E, 10 * E + i, std)).astype(np.float32)
+        for renorm in (True, False):
+            for bias in (None, np.linspace(-0.5, 0.5, E).astype(np.float32)):
+                gi, gg = check(l, k, "f32", score, bias, renorm=renorm, scale=2.5)
+                _, want = topk64(l, bias, k, score, 1, 1, 1, renorm, 2.5)
+                off = np.abs(gg - want) / np.maximum(want, 2.0 ** -100)
+                assert off.max() <= GATE_UNITS * 2.0 ** -24, (mean, std, renorm, bias is not None, off.max() * 2 ** 24)

@@ -311,18 +311,32 @@ __device__ __forceinline__ bool quick_row(const TopkArgs& m, int64_t row, int su
     float s[EPL];
     float inv = 1.0f;
     if (by_score || (softmax && !m.renorm)) {
-        float sum = 0.0f;
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-            s[i] = softmax ? exp_below(l[i], mx) : __builtin_amdgcn_rcpf(1.0f + coarse_exp(-l[i]));
-            sum += s[i];
+        for (int i = 0; i < EPL; ++i) s[i] = softmax ? exp_below(l[i], mx) : __builtin_amdgcn_rcpf(1.0f + coarse_exp(-l[i]));
+        if (softmax) {
+            // a balanced tree over the experts, whatever the lanes: a row's gates do not go by the launch's layout
+            float part[EPL];
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) part[i] = s[i];
+            if (m.E % EPL != 0) {                         // the last lane's run was moved back: down to its places again
+#pragma unroll
+                for (int d = 1; d < EPL; d *= 2) {
+#pragma unroll
+                    for (int i = 0; i < EPL; ++i) part[i] = first & d ? (i + d < EPL ? part[i + d] : 0.0f) : part[i];
+                }
+            }
+#pragma unroll
+            for (int d = 1; d < EPL; d *= 2) {
+#pragma unroll
+                for (int i = 0; i < EPL; i += 2 * d) part[i] += part[i + d];
+            }
+            inv = 1.0f / row_sum<LPR>(part[0]);
         }
-        if (softmax) inv = 1.0f / row_sum<LPR>(sum);
     }
     // `off` bounds the error of these scores, in units of 2^-23.  Sigmoid: s (1 - s) (0.75 |x| + 1) <= 0.6 from the
     // exponential, 0.5 from the sum, 1 from the reciprocal.  Softmax: 1.5 for the exponential, the same and half a
-    // unit for each of the 21 (EPL - 1 and 6) additions that a term of the divisor goes through, 1 for the quotient.
-    const float off = softmax ? 16 * kUlp : 2.5f * kUlp;
+    // unit for each of the 10 additions that a term of the divisor goes through, 1 for the quotient.
+    const float off = softmax ? 10 * kUlp : 2.5f * kUlp;
     uint32_t key[EPL];
     float a = -kInf, b = -kInf;                           // the lane's two largest values for its run's score
 #pragma unroll
@@ -501,15 +515,12 @@ int run_topk(const TopkArgs& m, hipStream_t s)
     }
     // Many rows: more experts a lane, so that a reduction serves more rows (8191 x 128, bf16: 16 lanes of 8 take 5.7 us,
     // 64 of 2 9.5; 32768 x 256, groups: 16 of 16 take 36, 64 of 4 63).  Few: more lanes, a shorter chain (2048 x 128:
-    // 4.9 against 4.7; 2048 x 256, groups: 12.0 against 10.1).
-    if (m.T >= 4096) {
-        if (fits(16, 8)) return launch_topk<16, 8>(m, lim, s);
-        if (fits(16, 16)) return launch_topk<16, 16>(m, lim, s);
-        if (fits(32, 16)) return launch_topk<32, 16>(m, lim, s);
-    }
-    if (fits(64, 2)) return launch_topk<64, 2>(m, lim, s);
-    if (fits(64, 4)) return launch_topk<64, 4>(m, lim, s);
-    if (fits(64, 8)) return launch_topk<64, 8>(m, lim, s);
+    // 4.9 against 4.7; 2048 x 256, groups: 12.0 against 10.1).  Both layouts of a size have the same product, and so the
+    // same keys and the same bits of a row in either.
+    const bool many = m.T >= 4096;
+    if (fits(64, 2)) return many && fits(16, 8) ? launch_topk<16, 8>(m, lim, s) : launch_topk<64, 2>(m, lim, s);
+    if (fits(64, 4)) return many && fits(16, 16) ? launch_topk<16, 16>(m, lim, s) : launch_topk<64, 4>(m, lim, s);
+    if (fits(64, 8)) return many && fits(32, 16) ? launch_topk<32, 16>(m, lim, s) : launch_topk<64, 8>(m, lim, s);
     if (fits(64, 16)) return launch_topk<64, 16>(m, lim, s);
     return launch_topk<64, 0>(m, lim, s);                  // runs that no lane count splits evenly
 }

@@ -7,7 +7,7 @@ import torch
 
 from quantized_moe_expert_quantize_amd import ftq
 from tests._cases import say
-from tests.test_gpu_topk import check, logits, topk64
+from tests.test_gpu_topk import balance, check, logits, topk64
 
 pytestmark = pytest.mark.gpu
 
@@ -115,3 +115,19 @@ def test_gates_hold_their_last_places(score, E, k):
                 _, want = topk64(l, bias, k, score, 1, 1, 1, renorm, 2.5)
                 off = np.abs(gg - want) / np.maximum(want, 2.0 ** -100)
                 assert off.max() <= GATE_UNITS * 2.0 ** -24, (mean, std, renorm, bias is not None, off.max() * 2 ** 24)
+
+
+# ---- a row's bits and the number of rows ---------------------------------------------
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E, k, n_group", [(128, 8, 1), (256, 8, 1), (256, 8, 8), (100, 8, 1), (130, 5, 1), (100, 20, 1), (255, 9, 1), (384, 8, 4),
+                                           (511, 3, 1), (64, 6, 1)])
+def test_rows_do_not_depend_on_the_number_of_rows(score, E, k, n_group):
+    """Few rows and many are laid out otherwise over the lanes; a row's ids and gates keep their bits."""
+    l, b = logits(5001, E, E), balance(E, E)
+    for bias in (None, b):
+        for renorm in (False, True):
+            whole = route(l, k, bias, n_group, max(1, n_group // 2), 1, score, renorm)
+            for a, z in ((0, 1), (0, 4095), (17, 300), (5000, 5001)):
+                part = route(l[a:z], k, bias, n_group, max(1, n_group // 2), 1, score, renorm)
+                assert np.array_equal(part[0], whole[0][a:z]) and np.array_equal(part[1], whole[1][a:z]), (a, z, renorm)

@@ -4,6 +4,11 @@ Argument marshalling only: every step of the computation runs in the HIP
 kernels of libftq.so.  PyTorch supplies device memory and the current stream.
 There is no fallback: if the library is missing or the device is not a GPU,
 the calls raise.
+
+Every call takes the stream to work on (None: the current one).  What a call
+allocates belongs to that stream and stays valid for the current one; the tensors
+passed to it are the caller's to keep, and to order before the call and after
+it, as for any work on another stream.
 """
 from __future__ import annotations
 
@@ -146,6 +151,17 @@ def _stream(stream=None) -> int:
     return s.cuda_stream
 
 
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """Memory for work on `stream`, from that stream's pool: a block of the current stream's may still be in use by work
+    queued there, which `stream` does not wait for.  The caller goes on with it on the current stream."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(t.device))
+    return t
+
+
 def _dev(t: torch.Tensor, name: str, dtype=None):
     if not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
@@ -167,7 +183,7 @@ def quantize_q8_1(x: torch.Tensor, out: torch.Tensor | None = None, stream=None)
     """fp32 [T, K] -> uint8 [T, K/32*36] Q8_1 blocks."""
     T, K = x.shape
     if out is None:
-        out = torch.empty((T, K // QK * Q8_1_BYTES), dtype=torch.uint8, device=x.device)
+        out = _empty((T, K // QK * Q8_1_BYTES), torch.uint8, x.device, stream)
     _check(lib().ftq_quantize_q8_1(_dev(x, "x", torch.float32), T, K, _out(out, T * (K // QK) * Q8_1_BYTES, "out", torch.uint8),
                                    _stream(stream)))
     return out
@@ -178,7 +194,7 @@ def quantize_q4_0(w: torch.Tensor, out: torch.Tensor | None = None, stream=None)
     K = w.shape[-1]
     rows = w.numel() // K if K else 0
     if out is None:
-        out = torch.empty(tuple(w.shape[:-1]) + (K // QK * Q4_0_BYTES,), dtype=torch.uint8, device=w.device)
+        out = _empty(tuple(w.shape[:-1]) + (K // QK * Q4_0_BYTES,), torch.uint8, w.device, stream)
     _check(lib().ftq_quantize_q4_0(_dev(w, "w", torch.float32), rows, K, _out(out, rows * (K // QK) * Q4_0_BYTES, "out", torch.uint8),
                                    _stream(stream)))
     return out
@@ -230,11 +246,11 @@ def _moe_args(w, a, topk_ids, E, N, K, per_pair=False):
     return T, top_k
 
 
-def _workspace(ws, need, device):
+def _workspace(ws, need, device, stream):
     if need == 0:
         return None, 0
     if ws is None:
-        ws = torch.empty(need, dtype=torch.uint8, device=device)
+        ws = _empty(need, torch.uint8, device, stream)
     if ws.numel() < need:
         raise ValueError(f"workspace needs {need} bytes")
     return ws, ws.numel()
@@ -246,9 +262,9 @@ def moe(w: torch.Tensor, a: torch.Tensor, topk_ids: torch.Tensor, E: int, N: int
     """MoE expert matmul: fp32 out [T*top_k, N]."""
     T, top_k = _moe_args(w, a, topk_ids, E, N, K)
     if out is None:
-        out = torch.empty((T * top_k, N), dtype=torch.float32, device=a.device)
+        out = _empty((T * top_k, N), torch.float32, a.device, stream)
     need = workspace_bytes(E, N, K, T, top_k, path)
-    ws, ws_n = _workspace(workspace, need, a.device)
+    ws, ws_n = _workspace(workspace, need, a.device, stream)
     _check(lib().ftq_moe_q4_0_q8_1(
         _dev(w, "w", torch.uint8), _dev(a, "a", torch.uint8), _dev(topk_ids, "topk_ids", torch.int32),
         _out(out, T * top_k * N, "out", torch.float32), E, N, K, T, top_k,
@@ -294,9 +310,9 @@ def moe_partials(w: torch.Tensor, a: torch.Tensor, topk_ids: torch.Tensor, E: in
                  path: int = PATH_AUTO, stream=None) -> torch.Tensor:
     """Exact integer block partials int32 [T*top_k, N, K/32]."""
     T, top_k = _moe_args(w, a, topk_ids, E, N, K)
-    out = torch.empty((T * top_k, N, K // QK), dtype=torch.int32, device=a.device)
+    out = _empty((T * top_k, N, K // QK), torch.int32, a.device, stream)
     need = workspace_bytes(E, N, K, T, top_k, path)
-    ws, ws_n = _workspace(None, need, a.device)
+    ws, ws_n = _workspace(None, need, a.device, stream)
     _check(lib().ftq_moe_q4_0_q8_1_partials(
         _dev(w, "w", torch.uint8), _dev(a, "a", torch.uint8), _dev(topk_ids, "topk_ids", torch.int32),
         _dev(out, "partials", torch.int32), E, N, K, T, top_k,
@@ -320,9 +336,9 @@ def moe_pairs(w: torch.Tensor, a_pairs: torch.Tensor, topk_ids: torch.Tensor, E:
     fp32 out [T*top_k, N]."""
     T, top_k = _moe_args(w, a_pairs, topk_ids, E, N, K, per_pair=True)
     if out is None:
-        out = torch.empty((T * top_k, N), dtype=torch.float32, device=a_pairs.device)
+        out = _empty((T * top_k, N), torch.float32, a_pairs.device, stream)
     need = pairs_workspace_bytes(E, N, K, T, top_k, path)
-    ws, ws_n = _workspace(workspace, need, a_pairs.device)
+    ws, ws_n = _workspace(workspace, need, a_pairs.device, stream)
     _check(lib().ftq_moe_q4_0_q8_1_pairs(
         _dev(w, "w", torch.uint8), _dev(a_pairs, "a_pairs", torch.uint8), _dev(topk_ids, "topk_ids", torch.int32),
         _out(out, T * top_k * N, "out", torch.float32), E, N, K, T, top_k,
@@ -347,9 +363,9 @@ def moe_pairs_partials(w: torch.Tensor, a_pairs: torch.Tensor, topk_ids: torch.T
                        path: int = PATH_AUTO, stream=None) -> torch.Tensor:
     """Exact integer block partials int32 [T*top_k, N, K/32] on per-pair activations."""
     T, top_k = _moe_args(w, a_pairs, topk_ids, E, N, K, per_pair=True)
-    out = torch.empty((T * top_k, N, K // QK), dtype=torch.int32, device=a_pairs.device)
+    out = _empty((T * top_k, N, K // QK), torch.int32, a_pairs.device, stream)
     need = pairs_workspace_bytes(E, N, K, T, top_k, path)
-    ws, ws_n = _workspace(None, need, a_pairs.device)
+    ws, ws_n = _workspace(None, need, a_pairs.device, stream)
     _check(lib().ftq_moe_q4_0_q8_1_pairs_partials(
         _dev(w, "w", torch.uint8), _dev(a_pairs, "a_pairs", torch.uint8), _dev(topk_ids, "topk_ids", torch.int32),
         _dev(out, "partials", torch.int32), E, N, K, T, top_k,
@@ -365,9 +381,9 @@ def moe_act(w: torch.Tensor, a: torch.Tensor, topk_ids: torch.Tensor, E: int, N:
     """act(gate) * up: fp32 out [T*top_k, N/2] from N = 2*(N/2) weight rows per expert."""
     T, top_k = _moe_args(w, a, topk_ids, E, N, K)
     if out is None:
-        out = torch.empty((T * top_k, N // 2), dtype=torch.float32, device=a.device)
+        out = _empty((T * top_k, N // 2), torch.float32, a.device, stream)
     need = workspace_bytes(E, N, K, T, top_k, path)
-    ws, ws_n = _workspace(workspace, need, a.device)
+    ws, ws_n = _workspace(workspace, need, a.device, stream)
     _check(lib().ftq_moe_q4_0_q8_1_act(
         _dev(w, "w", torch.uint8), _dev(a, "a", torch.uint8), _dev(topk_ids, "topk_ids", torch.int32),
         _out(out, T * top_k * (N // 2), "out", torch.float32), E, N, K, T, top_k, act,
@@ -409,9 +425,9 @@ def moe_gguf(w: torch.Tensor, wtype: int, a: torch.Tensor, topk_ids: torch.Tenso
     """Matmul with weights of GGUF type `wtype` (W_*): fp32 out [T*top_k, N]."""
     T, top_k = _gguf_args(w, wtype, a, topk_ids, E, N, K, per_pair)
     if out is None:
-        out = torch.empty((T * top_k, N), dtype=torch.float32, device=a.device)
+        out = _empty((T * top_k, N), torch.float32, a.device, stream)
     need = workspace_bytes(E, N, K, T, top_k, PATH_GEMV if wtype in GEMV_ONLY else path)
-    ws, ws_n = _workspace(workspace, need, a.device)
+    ws, ws_n = _workspace(workspace, need, a.device, stream)
     _check(lib().ftq_moe_gguf_q8_1(
         _dev(w, "w", torch.uint8), wtype, _dev(a, "a", torch.uint8), _dev(topk_ids, "topk_ids", torch.int32),
         _out(out, T * top_k * N, "out", torch.float32), E, N, K, T, top_k, int(per_pair),
@@ -423,9 +439,9 @@ def moe_gguf_partials(w: torch.Tensor, wtype: int, a: torch.Tensor, topk_ids: to
                       per_pair: bool = False, path: int = PATH_AUTO, stream=None) -> torch.Tensor:
     """Integer parts sum((q - z) * q8), int32 [T*top_k, N, K/32]."""
     T, top_k = _gguf_args(w, wtype, a, topk_ids, E, N, K, per_pair)
-    out = torch.empty((T * top_k, N, K // QK), dtype=torch.int32, device=a.device)
+    out = _empty((T * top_k, N, K // QK), torch.int32, a.device, stream)
     need = workspace_bytes(E, N, K, T, top_k, PATH_GEMV if wtype in GEMV_ONLY else path)
-    ws, ws_n = _workspace(None, need, a.device)
+    ws, ws_n = _workspace(None, need, a.device, stream)
     _check(lib().ftq_moe_gguf_q8_1_partials(
         _dev(w, "w", torch.uint8), wtype, _dev(a, "a", torch.uint8), _dev(topk_ids, "topk_ids", torch.int32),
         _dev(out, "partials", torch.int32), E, N, K, T, top_k, int(per_pair),
@@ -440,7 +456,7 @@ def combine_topk(y: torch.Tensor, gates: torch.Tensor, out: torch.Tensor | None 
         raise ValueError("y must be [T*top_k, N]")
     N = y.shape[1]
     if out is None:
-        out = torch.empty((T, N), dtype=torch.float32, device=y.device)
+        out = _empty((T, N), torch.float32, y.device, stream)
     _check(lib().ftq_moe_combine_topk(_dev(y, "y", torch.float32), _dev(gates, "gates", torch.float32),
                                       _out(out, T * N, "out", torch.float32), T, top_k, N, _stream(stream)))
     return out
@@ -504,14 +520,6 @@ def _stream_here(stream, dev: int) -> int:
     return stream.cuda_stream
 
 
-def _keep(stream, *tensors):
-    """Memory allocated here for work on `stream` is not reused before that work is done."""
-    if stream is not None:
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
-
-
 def moe_topk(logits: torch.Tensor, top_k: int, score: int = SCORE_SOFTMAX, bias: torch.Tensor | None = None,
              n_group: int = 1, topk_group: int = 1, group_top: int = 1, renorm: bool = True, scale: float = 1.0,
              ids: torch.Tensor | None = None, gates: torch.Tensor | None = None, stream=None):
@@ -521,11 +529,9 @@ def moe_topk(logits: torch.Tensor, top_k: int, score: int = SCORE_SOFTMAX, bias:
     T, E = logits.shape
     shape = (T, max(top_k, 0))
     if ids is None:
-        ids = torch.empty(shape, dtype=torch.int32, device=logits.device)
-        _keep(stream, ids)
+        ids = _empty(shape, torch.int32, logits.device, stream)
     if gates is None:
-        gates = torch.empty(shape, dtype=torch.float32, device=logits.device)
-        _keep(stream, gates)
+        gates = _empty(shape, torch.float32, logits.device, stream)
     _check(lib().ftq_moe_topk(p, dt, ld, _here(bias, "bias", torch.float32, dev, (E,)) if bias is not None else None,
                               _here(ids, "ids", torch.int32, dev, shape), _here(gates, "gates", torch.float32, dev, shape),
                               T, E, top_k, score, n_group, topk_group, group_top, int(renorm), scale, _stream_here(stream, dev)))
@@ -539,11 +545,9 @@ def quantize_fp8(x: torch.Tensor, out: torch.Tensor | None = None, scales: torch
     T, K = x.shape
     shape = (T, -(-K // FP8_BLOCK))
     if out is None:
-        out = torch.empty((T, K), dtype=FP8, device=x.device)
-        _keep(stream, out)
+        out = _empty((T, K), FP8, x.device, stream)
     if scales is None:
-        scales = torch.empty(shape, dtype=torch.float32, device=x.device)
-        _keep(stream, scales)
+        scales = _empty(shape, torch.float32, x.device, stream)
     _check(lib().ftq_quantize_fp8(p, dt, ld, T, K, _here(out, "out", FP8, dev, (T, K)),
                                   _here(scales, "scales", torch.float32, dev, shape), _stream_here(stream, dev)))
     return out, scales
@@ -557,11 +561,9 @@ def quantize_fp8_weight(w: torch.Tensor, out: torch.Tensor | None = None, scales
     E, N, K = w.shape
     shape = (E, -(-N // FP8_BLOCK), -(-K // FP8_BLOCK))
     if out is None:
-        out = torch.empty((E, N, K), dtype=FP8, device=w.device)
-        _keep(stream, out)
+        out = _empty((E, N, K), FP8, w.device, stream)
     if scales is None:
-        scales = torch.empty(shape, dtype=torch.float32, device=w.device)
-        _keep(stream, scales)
+        scales = _empty(shape, torch.float32, w.device, stream)
     _check(lib().ftq_quantize_fp8_weight(_here(w, "w", w.dtype, dev), _DTYPE[w.dtype], E, N, K, _here(out, "out", FP8, dev, (E, N, K)),
                                          _here(scales, "scales", torch.float32, dev, shape), _stream_here(stream, dev)))
     return out, scales
@@ -605,12 +607,10 @@ def moe_fp8(w: torch.Tensor, w_scale: torch.Tensor, a: torch.Tensor, a_scale: to
     out [T*top_k, N], or with act (ACT_*) act(gate) * up [T*top_k, N/2]."""
     T, top_k = topk_ids.shape
     if out is None:
-        out = torch.empty((T * top_k, N // 2 if act else N), dtype=out_dtype, device=a.device)
-        _keep(stream, out)
+        out = _empty((T * top_k, N // 2 if act else N), out_dtype, a.device, stream)
     if workspace is None:
         need = fp8_workspace_bytes(E, N, K, T, top_k, path)
-        workspace = torch.empty(need, dtype=torch.uint8, device=a.device) if need else None
-        _keep(stream, workspace)
+        workspace = _empty(need, torch.uint8, a.device, stream) if need else None
     return _fp8_call(lib().ftq_moe_fp8, w, w_scale, a, a_scale, topk_ids, E, N, K, per_pair, act, out, workspace, path,
                      stream)
 

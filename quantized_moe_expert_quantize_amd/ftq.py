@@ -467,8 +467,13 @@ def combine_topk(y: torch.Tensor, gates: torch.Tensor, out: torch.Tensor | None 
 # These calls may take no longer on the GPU than a few microseconds, so the
 # marshalling is kept to about one: the raw-handle queries of torch._C stand in
 # for torch.cuda.current_device() and current_stream() (0.1 us against 2.8 us).
-_device = torch._C._cuda_getDevice
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# They are looked up in the call: a torch without GPU support lacks them.
+def _device() -> int:
+    return torch._C._cuda_getDevice()
+
+
+def _raw_stream(dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 def _device_for(t: torch.Tensor, name: str) -> int:

@@ -383,6 +383,10 @@ typedef enum {
 
 #define FTQ_FP8_BLOCK 128
 
+/* Or'ed to out_dtype of ftq_moe_fp8 and ftq_moe_fp8_routed: exact products for
+ * 16-bit results on every path (see there). */
+#define FTQ_EXACT 0x100
+
 /*
  * Router: every token's top_k experts and their gate weights, in the layout
  * the matmuls (topk_ids) and ftq_moe_combine_topk (gates) take.
@@ -454,8 +458,10 @@ int ftq_quantize_fp8_weight(const void* w, int dtype, int64_t E, int64_t N, int6
  * The sum over blocks is held in fp32.  P is an fp32 sum of exact products, with
  * one exception: for 16-bit out the grouped path leaves P to the matrix units'
  * 8-bit instructions, which drop bits below 2^-13 of the largest of every eight
- * products (about 1.5e-5 of a result's norm on normal values, a hundredth of what
- * rounding to bf16 costs).  act == 0: out[p][n] = y[p][n],
+ * products: about 1.5e-5 of a result's norm on normal values, a hundredth of what
+ * rounding to bf16 costs and a tenth of fp16's; more of a result whose terms
+ * cancel.  out_dtype | FTQ_EXACT asks for exact products there too, as the
+ * GEMV path and fp32 out always have them.  act == 0: out[p][n] = y[p][n],
  * N columns; act FTQ_ACT_*: out[p][c] = act(y[p][c]) * y[p][N/2 + c], N/2 columns
  * (gate rows, then up rows, as ftq_moe_q4_0_q8_1_act).
  *   w        [E][N][K] e4m3 codes, 16-byte aligned; w_scale fp32
@@ -468,7 +474,7 @@ int ftq_quantize_fp8_weight(const void* w, int dtype, int64_t E, int64_t N, int6
  *   workspace, path: as ftq_moe_q4_0_q8_1, with ftq_moe_fp8_workspace_bytes
  *            and ftq_moe_fp8_select_path in place of that call's.
  * A row's bits depend neither on the other rows nor on the batch size while the
- * path is the same.  A NaN code or scale reaches only the results it is a term of.
+ * path and the form of P are the same.  A NaN code or scale reaches only the results it is a term of.
  * Limits: K % 16 == 0, K <= 2^25; with act, N % 32 == 0 (FTQ_ERR_UNSUPPORTED otherwise;
  * odd N: FTQ_ERR_INVALID_ARG); FTQ_PATH_GEMV takes at most 4096 pairs
  * (FTQ_ERR_UNSUPPORTED above); E, N, T, top_k as ftq_moe_q4_0_q8_1.

@@ -571,7 +571,7 @@ int ftq_moe_fp8(const void* w, const float* w_scale, const void* a, const float*
                 int act_per_pair, int act, void* workspace, size_t workspace_bytes, int path, hipStream_t stream)
 {
     const Fp8Args m{static_cast<const uint8_t*>(w), w_scale, static_cast<const uint8_t*>(a), a_scale, topk_ids, out,
-                    E, N, K, T, top_k, 0, act, out_dtype};
+                    E, N, K, T, top_k, 0, act, out_dtype & ~FTQ_EXACT, (out_dtype & FTQ_EXACT) != 0};
     return fp8_common(m, act_per_pair != 0, workspace, workspace_bytes, path, stream, kRoute | kMatmul);
 }
 
@@ -579,7 +579,7 @@ int ftq_moe_fp8_route(const int32_t* topk_ids, int64_t E, int64_t T, int64_t top
                       size_t workspace_bytes, int path, hipStream_t stream)
 {
     // N and K do not enter the routing; any valid values pass the size checks
-    const Fp8Args m{nullptr, nullptr, nullptr, nullptr, topk_ids, nullptr, E, 1, kFp8Block, T, top_k, 0, 0, FTQ_F32};
+    const Fp8Args m{nullptr, nullptr, nullptr, nullptr, topk_ids, nullptr, E, 1, kFp8Block, T, top_k, 0, 0, FTQ_F32, true};
     return fp8_common(m, false, workspace, workspace_bytes, path, stream, kRoute);
 }
 
@@ -589,7 +589,7 @@ int ftq_moe_fp8_routed(const void* w, const float* w_scale, const void* a, const
                        hipStream_t stream)
 {
     const Fp8Args m{static_cast<const uint8_t*>(w), w_scale, static_cast<const uint8_t*>(a), a_scale, topk_ids, out,
-                    E, N, K, T, top_k, 0, act, out_dtype};
+                    E, N, K, T, top_k, 0, act, out_dtype & ~FTQ_EXACT, (out_dtype & FTQ_EXACT) != 0};
     return fp8_common(m, act_per_pair != 0, workspace, workspace_bytes, path, stream, kMatmul);
 }
 

@@ -199,6 +199,7 @@ struct Fp8Args {
     int64_t act_div;       // activation row of pair p: p / act_div (top_k: per token; 1: per pair)
     int act;               // 0: N columns; FTQ_ACT_*: N/2
     int out_dtype;
+    bool exact;            // 16-bit results of the grouped path from exact products too
 };
 constexpr int64_t kFp8MaxK = int64_t(1) << 25;   // 64 rows' offsets stay below 2^31
 constexpr int64_t kFp8GemvMaxPairs = 4096;   // the GEMV path finds an expert's pairs by scanning the ids

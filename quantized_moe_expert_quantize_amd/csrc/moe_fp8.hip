@@ -23,8 +23,11 @@
 //          drops bits below 2^-13 of it (measured: 1.5e-5 relative to the result's
 //          norm, 1.1e-5 of the sum of the terms' magnitudes at most).
 // fp32 results take the exact form.  fp16 and bf16 results of the grouped path
-// take the fast one: what it drops is a hundredth of their own rounding (2^-9,
-// 2^-12).  The GEMV, which waits for memory, takes the exact form always.
+// take the fast one, unless the caller asks for the exact one (FTQ_EXACT): what it
+// drops is a hundredth of bf16's own rounding and a tenth of fp16's, but it is
+// relative to the terms, so that a result which cancels loses more.  (8191 tokens
+// evenly spread, bf16 results: first layer 736 us fast, 1192 exact; second 484 and
+// 635.)  The GEMV, which waits for memory, takes the exact form always.
 //
 // Two kernels.  The GEMV splits K over the waves of a workgroup and reads each
 // weight once for up to 16 pairs of its expert; it is bound by HBM (8 experts of
@@ -309,11 +312,11 @@ struct GroupedTables {
 // tile i is column 16*i + r, four columns a lane and tile; 16 bits, column
 // 32*(i/2) + 8*(r/4) + 4*(i%2) + r%4, eight a lane and pair of tiles.
 // A table tile of more than 16*TT pairs is made by `subs` items.
-template <int TT, int WT, int NB, int OUT, bool ACT>
+template <int TT, int WT, int NB, int OUT, bool ACT, bool EXACT>
 __global__ __launch_bounds__(64 * kGroups * WT, 2) void moe_fp8_grouped_kernel(Fp8Args m, GroupedTables g, int subs)
 {
     static_assert(NB == 2 || WT == 1);
-    constexpr bool kExact = OUT == FTQ_F32;
+    static_assert(EXACT || OUT != FTQ_F32);
     constexpr int kWaves = kGroups * WT, kThreads = 64 * kWaves;
     constexpr int BM = 16 * TT * WT;                   // pairs per workgroup
     constexpr int kShare = 8 / WT;                     // copies of its group's weight rows that a wave makes
@@ -405,9 +408,9 @@ __global__ __launch_bounds__(64 * kGroups * WT, 2) void moe_fp8_grouped_kernel(F
         };
         f32x4 acc[4][TT] = {};
         const auto multiply = [&](int buf) {
-            Operand<kExact> w[4];
+            Operand<EXACT> w[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = Operand<kExact>(wv[i]);
+            for (int i = 0; i < 4; ++i) w[i] = Operand<EXACT>(wv[i]);
             // Two weight tiles at a time: their products are made while the last two's are added up, and the next
             // activation tile is read meanwhile.  (The scheduling barriers keep the compiler from making all products
             // first, which takes registers that are not there.)
@@ -426,7 +429,7 @@ __global__ __launch_bounds__(64 * kGroups * WT, 2) void moe_fp8_grouped_kernel(F
                     sa_ahead = act_scale[buf][half * 16 * TT + (j + 1) * 16 + r];
                 }
                 if (h < 2 * TT) {
-                    const Operand<kExact> b(codes);
+                    const Operand<EXACT> b(codes);
                     block_products(w, i0, b, p[h & 1]);
                 }
                 if (h > 0) {
@@ -443,7 +446,7 @@ __global__ __launch_bounds__(64 * kGroups * WT, 2) void moe_fp8_grouped_kernel(F
                     sa = sa_ahead;
                     codes = ahead;
                 }
-                if constexpr (!kExact) {               // a product, then the four sums of one made two products ago
+                if constexpr (!EXACT) {               // a product, then the four sums of one made two products ago
                     __builtin_amdgcn_sched_group_barrier(0x100, 3, 0);
                     __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
                     __builtin_amdgcn_sched_group_barrier(0x002, 5, 0);
@@ -550,24 +553,24 @@ int launch_gemv(const Fp8Args& m, hipStream_t s)
 }
 
 // Tables of tile_m pairs a tile, walked in parts of 16*TT*WT, with a stride if there are more than a launch takes.
-template <int TT, int WT, int NB, int OUT, bool ACT>
+template <int TT, int WT, int NB, int OUT, bool ACT, bool EXACT>
 int launch_tile(const Fp8Args& m, const GroupedTables& g, int64_t tile_m, int64_t max_tiles, hipStream_t s)
 {
     const int subs = (int)(tile_m / (16 * TT * WT));
     const int64_t grid = std::min((max_tiles * subs * g.ntn + kXcds - 1) / kXcds * kXcds, kMaxGrid);
-    return launch("moe_fp8_grouped_kernel", moe_fp8_grouped_kernel<TT, WT, NB, OUT, ACT>, grid, 64 * kGroups * WT, 0, s, m, g, subs);
+    return launch("moe_fp8_grouped_kernel", moe_fp8_grouped_kernel<TT, WT, NB, OUT, ACT, EXACT>, grid, 64 * kGroups * WT, 0, s, m, g, subs);
 }
 
-template <int OUT, bool ACT>
+template <int OUT, bool ACT, bool EXACT>
 int launch_grouped(const Fp8Args& m, const GroupedTables& g, int64_t tile_m, int64_t max_tiles, hipStream_t s)
 {
-    if (tile_m == 32) return launch_tile<2, 1, 2, OUT, ACT>(m, g, tile_m, max_tiles, s);
+    if (tile_m == 32) return launch_tile<2, 1, 2, OUT, ACT, EXACT>(m, g, tile_m, max_tiles, s);
     // The exact form walks tall tiles in parts of 64 pairs (second layer, 8191 tokens uniform: 754 us, 803 in parts
     // of 128 by two waves a weight group).
-    if constexpr (OUT != FTQ_F32) {
-        if (tile_m == 256) return launch_tile<8, 2, 2, OUT, ACT>(m, g, tile_m, max_tiles, s);
+    if constexpr (!EXACT) {
+        if (tile_m == 256) return launch_tile<8, 2, 2, OUT, ACT, EXACT>(m, g, tile_m, max_tiles, s);
     }
-    return launch_tile<4, 1, 1, OUT, ACT>(m, g, tile_m, max_tiles, s);
+    return launch_tile<4, 1, 1, OUT, ACT, EXACT>(m, g, tile_m, max_tiles, s);
 }
 
 // Calls f<OUT, ACT>() for the output type and activation of m.
@@ -594,7 +597,13 @@ struct GroupedCall {
     const GroupedTables& g;
     int64_t tile_m, max_tiles;
     hipStream_t s;
-    template <int OUT, bool ACT> int operator()() const { return launch_grouped<OUT, ACT>(m, g, tile_m, max_tiles, s); }
+    template <int OUT, bool ACT> int operator()() const
+    {
+        if constexpr (OUT != FTQ_F32) {
+            if (!m.exact) return launch_grouped<OUT, ACT, false>(m, g, tile_m, max_tiles, s);
+        }
+        return launch_grouped<OUT, ACT, true>(m, g, tile_m, max_tiles, s);
+    }
 };
 
 }  // namespace

@@ -36,6 +36,7 @@ F32, F16, BF16 = 0, 1, 2
 _DTYPE = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
 SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 FP8, FP8_BLOCK = torch.float8_e4m3fn, 128
+EXACT = 0x100   # or'ed to the out type of the 8-bit floating-point matmul
 
 EXPORTS = (
     "ftq_quantize_q8_1", "ftq_quantize_q4_0", "ftq_moe_select_path", "ftq_moe_workspace_bytes",
@@ -588,7 +589,7 @@ def fp8_workspace_bytes(E: int, N: int, K: int, T: int, top_k: int, path: int = 
     return r
 
 
-def _fp8_call(entry, w, w_scale, a, a_scale, topk_ids, E, N, K, per_pair, act, out, workspace, path, stream):
+def _fp8_call(entry, w, w_scale, a, a_scale, topk_ids, E, N, K, per_pair, act, out, workspace, path, exact, stream):
     dev = _device_for(w, "w")
     T, top_k = topk_ids.shape
     rows, nb = T * top_k if per_pair else T, -(-K // FP8_BLOCK)
@@ -599,7 +600,7 @@ def _fp8_call(entry, w, w_scale, a, a_scale, topk_ids, E, N, K, per_pair, act, o
         _here(w, "w", FP8, dev, (E, N, K)), _here(w_scale, "w_scale", torch.float32, dev, (E, -(-N // FP8_BLOCK), nb)),
         _here(a, "a", FP8, dev, (rows, K)), _here(a_scale, "a_scale", torch.float32, dev, (rows, nb)),
         _here(topk_ids, "topk_ids", torch.int32, dev), _here(out, "out", out.dtype, dev, (T * top_k, N // 2 if act else N)),
-        _DTYPE[out.dtype], E, N, K, T, top_k, int(per_pair), act,
+        _DTYPE[out.dtype] | (EXACT if exact else 0), E, N, K, T, top_k, int(per_pair), act,
         _here(workspace, "workspace", torch.uint8, dev) if workspace is not None else None, ws_n, path, _stream_here(stream, dev)))
     return out
 
@@ -607,9 +608,10 @@ def _fp8_call(entry, w, w_scale, a, a_scale, topk_ids, E, N, K, per_pair, act, o
 def moe_fp8(w: torch.Tensor, w_scale: torch.Tensor, a: torch.Tensor, a_scale: torch.Tensor, topk_ids: torch.Tensor,
             E: int, N: int, K: int, per_pair: bool = False, act: int = 0, path: int = PATH_AUTO,
             out: torch.Tensor | None = None, out_dtype: torch.dtype = torch.float32,
-            workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+            workspace: torch.Tensor | None = None, stream=None, exact: bool = False) -> torch.Tensor:
     """Expert matmul on e4m3 weights [E, N, K] and activations [T or T*top_k, K] with their block scales:
-    out [T*top_k, N], or with act (ACT_*) act(gate) * up [T*top_k, N/2]."""
+    out [T*top_k, N], or with act (ACT_*) act(gate) * up [T*top_k, N/2].  exact: exact products also for 16-bit
+    results of the grouped path, which drop small bits without it (see ftq_moe_fp8)."""
     T, top_k = topk_ids.shape
     if out is None:
         out = _empty((T * top_k, N // 2 if act else N), out_dtype, a.device, stream)
@@ -617,7 +619,7 @@ def moe_fp8(w: torch.Tensor, w_scale: torch.Tensor, a: torch.Tensor, a_scale: to
         need = fp8_workspace_bytes(E, N, K, T, top_k, path)
         workspace = _empty(need, torch.uint8, a.device, stream) if need else None
     return _fp8_call(lib().ftq_moe_fp8, w, w_scale, a, a_scale, topk_ids, E, N, K, per_pair, act, out, workspace, path,
-                     stream)
+                     exact, stream)
 
 
 def moe_fp8_route(topk_ids: torch.Tensor, E: int, workspace: torch.Tensor | None, path: int, stream=None) -> None:
@@ -632,7 +634,7 @@ def moe_fp8_route(topk_ids: torch.Tensor, E: int, workspace: torch.Tensor | None
 
 def moe_fp8_routed(w: torch.Tensor, w_scale: torch.Tensor, a: torch.Tensor, a_scale: torch.Tensor,
                    topk_ids: torch.Tensor, E: int, N: int, K: int, out: torch.Tensor, workspace: torch.Tensor | None,
-                   path: int, per_pair: bool = False, act: int = 0, stream=None) -> torch.Tensor:
+                   path: int, per_pair: bool = False, act: int = 0, stream=None, exact: bool = False) -> torch.Tensor:
     """moe_fp8 on pairs already routed into `workspace` by moe_fp8_route."""
     return _fp8_call(lib().ftq_moe_fp8_routed, w, w_scale, a, a_scale, topk_ids, E, N, K, per_pair, act, out, workspace,
-                     path, stream)
+                     path, exact, stream)

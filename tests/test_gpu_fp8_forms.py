@@ -1,11 +1,13 @@
 """The two forms of the 8-bit floating-point products on the GPU: exact ones for 16-bit results when
-they are asked for."""
+they are asked for; what the fast one loses, and that a row keeps its bits in it."""
+import math
+
 import pytest
 import torch
 
-from quantized_moe_expert_quantize_amd import ftq
+from quantized_moe_expert_quantize_amd import ftq, inputs
 from tests._cases import say
-from tests._fp8 import DTYPES, assert_close, moe64
+from tests._fp8 import DTYPES, _act64, assert_close, moe64
 from tests.test_gpu_fp8 import Experts
 
 pytestmark = pytest.mark.gpu
@@ -78,3 +80,54 @@ def test_exact_on_routed_pairs():
         out = torch.empty(300, 320 if act is None else 160, dtype=torch.bfloat16, device="cuda")
         ftq.moe_fp8_routed(c.w, c.ws, c.a, c.as_, c.ids, 8, 320, 512, out, ws, ftq.PATH_GROUPED, act=ACTS[act], exact=True)
         assert torch.equal(out, call(c, ftq.PATH_GROUPED, act, "bf16", True))
+
+
+# What the fast form loses of a result's norm on normal values is given as 1.5e-5; twice that is allowed.
+FAST = 3e-5
+
+
+@pytest.mark.parametrize("act", [None, "silu", "gelu"])
+@pytest.mark.parametrize("T", [60, 300, 1300], ids=["tiles of 32", "tiles of 64", "tiles of 256"])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_fast_products_lose_little_of_the_norm(dtype, T, act):
+    """Against the 64-bit results rounded to the type, in norm.
+
+    With d the fast form's error of an element and u the step of the type there, the rounded results differ by u with
+    probability |d| / u (the 64-bit results lie anywhere between two numbers of the type), so that the squares add up to
+    sum |d| u <= |d| |u| in norms.  u is at most 2^-10 (fp16) or 2^-7 (bf16) of the element.  A dropped
+    product or three more lost bits do not pass."""
+    E, N, K, k = 8, 320, 2048, 2
+    g = torch.Generator().manual_seed(T)
+    w, ws = ftq.quantize_fp8_weight((torch.randn(E, N, K, generator=g) / math.sqrt(K)).cuda())
+    a, as_ = ftq.quantize_fp8(torch.randn(T, K, generator=g).cuda())
+    ids = torch.from_numpy(inputs.routing(T, E, k, seed=T)).cuda()
+    got = ftq.moe_fp8(w, ws, a, as_, ids, E, N, K, act=ACTS[act], path=ftq.PATH_GROUPED, out_dtype=DTYPES[dtype])
+    y, _ = moe64(w, ws, a, as_, ids, False)
+    loss = FAST * y.square().mean().sqrt()               # of an element without activation
+    if act is None:
+        ref, d = y, torch.full_like(y, loss)
+    else:
+        gate, up = y[:, : N // 2], y[:, N // 2:]
+        ref = _act64(act, gate) * up
+        slope = (_act64(act, gate + 1e-6) - _act64(act, gate - 1e-6)) / 2e-6
+        d = loss * ((slope * up).square() + _act64(act, gate).square()).sqrt()
+    step = {"f16": 2.0 ** -10, "bf16": 2.0 ** -7}[dtype]
+    off = (got.double() - ref.to(DTYPES[dtype]).double()).norm()
+    lim = (d.norm() * step * ref.norm() + d.norm() ** 2).sqrt()
+    say(f"[fp8] fast {dtype} T={T} {act}: {float(off / ref.norm()):.2e} of {float(lim / ref.norm()):.2e}")
+    assert off <= lim
+
+
+@pytest.mark.parametrize("act", [None, "silu"])
+@pytest.mark.parametrize("exact", [False, True])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_a_16_bit_row_does_not_depend_on_the_batch(dtype, exact, act):
+    """A pair's bits alone, in a part and in the whole batch, by kernels of every tile height."""
+    E, N, K, k = 8, 224, 1424, 2
+    for T in (60, 300, 1300):
+        c = Experts(E, N, K, T, k, seed=T)
+        whole = call(c, ftq.PATH_GROUPED, act, dtype, exact)
+        for a, b in ((0, 1), (0, 7), (T // 3, T // 3 + 200), (T // 2, T), (T - 1, T)):
+            part = ftq.moe_fp8(c.w, c.ws, c.a[a:b], c.as_[a:b], c.ids[a:b].contiguous(), E, N, K, path=ftq.PATH_GROUPED, act=ACTS[act],
+                               out_dtype=DTYPES[dtype], exact=exact)
+            assert torch.equal(part, whole[a * k: min(b, T) * k]), (T, a, b)

@@ -131,3 +131,37 @@ def test_a_16_bit_row_does_not_depend_on_the_batch(dtype, exact, act):
             part = ftq.moe_fp8(c.w, c.ws, c.a[a:b], c.as_[a:b], c.ids[a:b].contiguous(), E, N, K, path=ftq.PATH_GROUPED, act=ACTS[act],
                                out_dtype=DTYPES[dtype], exact=exact)
             assert torch.equal(part, whole[a * k: min(b, T) * k]), (T, a, b)
+
+
+def test_quantiser_offsets_past_32_bits():
+    """Activations by rows and by their stride, and weights, whose offsets pass 2^32."""
+    g = torch.Generator().manual_seed(2)
+    x = torch.randn(6, 272, generator=g).bfloat16().cuda()
+    q, s = ftq.quantize_fp8(x)
+    far = torch.empty(5 * (1 << 30) + 272, dtype=torch.bfloat16, device="cuda")
+    rows = far.as_strided((6, 272), (1 << 30, 1))
+    rows.copy_(x)
+    say("[fp8] quantise far rows by stride")
+    q2, s2 = ftq.quantize_fp8(rows)
+    assert torch.equal(q2.view(torch.uint8), q.view(torch.uint8)) and torch.equal(s2, s)
+    T = (1 << 24) + 6
+    many = far[: T * 272].view(T, 272)
+    many.zero_()
+    many[-6:] = x
+    say("[fp8] quantise far rows by number")
+    q2, s2 = ftq.quantize_fp8(many)
+    assert torch.equal(q2[-6:].view(torch.uint8), q.view(torch.uint8)) and torch.equal(s2[-6:], s)
+    assert not q2[:-6].view(torch.uint8).any() and not s2[:-6].any()
+    del q2, s2
+    E, N, K = 17, 16384, 16400
+    w = far[: E * N * K].view(E, N, K)
+    w.zero_()
+    w[-1, -6:, -272:] = x
+    say("[fp8] quantise far weights")
+    q2, s2 = ftq.quantize_fp8_weight(w)
+    alone = torch.zeros(1, 128, K, dtype=torch.bfloat16, device="cuda")
+    alone[0, -6:, -272:] = x
+    q1, s1 = ftq.quantize_fp8_weight(alone)
+    assert torch.equal(q2[-1, -128:].view(torch.uint8), q1[0].view(torch.uint8)) and torch.equal(s2[-1, -1], s1[0, 0])
+    q2[-1, -6:, -272:] = 0
+    assert not q2.view(torch.uint8).any() and not s2[:-1].any() and not s2[-1, :-1].any()

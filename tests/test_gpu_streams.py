@@ -100,3 +100,35 @@ def test_a_chain_beside_work_of_the_current_stream():
         got = chain(s)
         torch.cuda.synchronize()
         assert torch.equal(got, want) and (total == 4.0 * i).all()
+
+
+@pytest.mark.parametrize("tokens", [3, 600])
+def test_a_captured_chain_on_a_forked_stream(tokens):
+    """A graph whose calls run on a stream forked from the captured one and joined again, replayed with other inputs and
+    eager work between the replays."""
+    g = torch.Generator().manual_seed(4)
+    x, logits = torch.randn(tokens, K, generator=g).cuda(), torch.randn(tokens, E, generator=g).cuda()
+    w, ws = ftq.quantize_fp8_weight((torch.randn(E, N, K, generator=g) * 0.05).cuda())
+    s = torch.cuda.Stream()
+
+    def chain(stream):
+        ids, gates = ftq.moe_topk(logits, TOP_K, stream=stream)
+        a, as_ = ftq.quantize_fp8(x, stream=stream)
+        y = ftq.moe_fp8(w, ws, a, as_, ids, E, N, K, out_dtype=torch.float32, stream=stream)
+        return ids, gates, y, ftq.combine_topk(y, gates, stream=stream)
+    chain(None)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        s.wait_stream(torch.cuda.current_stream())
+        got = chain(s)
+        torch.cuda.current_stream().wait_stream(s)
+    for seed in range(4):
+        g.manual_seed(10 + seed)
+        x.copy_(torch.randn(tokens, K, generator=g))
+        logits.copy_(torch.randn(tokens, E, generator=g))
+        want = chain(None)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))

@@ -131,3 +131,27 @@ def test_rows_do_not_depend_on_the_number_of_rows(score, E, k, n_group):
             for a, z in ((0, 1), (0, 4095), (17, 300), (5000, 5001)):
                 part = route(l[a:z], k, bias, n_group, max(1, n_group // 2), 1, score, renorm)
                 assert np.array_equal(part[0], whole[0][a:z]) and np.array_equal(part[1], whole[1][a:z]), (a, z, renorm)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_offsets_past_32_bits(score):
+    """Logits whose element and byte offsets pass 2^32: by their rows' stride, and by their number."""
+    E, k = 64, 4
+    kw = dict(score=ftq.SCORE_SOFTMAX if score == "softmax" else ftq.SCORE_SIGMOID, bias=torch.from_numpy(balance(E, 1)).cuda())
+    x = torch.from_numpy(logits(6, E, 8)).bfloat16().cuda()
+    want = ftq.moe_topk(x, k, **kw)
+    far = torch.empty(5 * (1 << 30) + E, dtype=torch.bfloat16, device="cuda")
+    rows = far.as_strided((6, E), (1 << 30, 1))
+    rows.copy_(x)
+    say(f"[topk] far rows by stride {score}")
+    got = ftq.moe_topk(rows, k, **kw)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    T = (1 << 26) + 6
+    many = far[: T * E].view(T, E)
+    many.zero_()
+    many[-6:] = x
+    say(f"[topk] far rows by number {score}")
+    got = ftq.moe_topk(many, k, **kw)
+    assert torch.equal(got[0][-6:], want[0]) and torch.equal(got[1][-6:], want[1])
+    first = ftq.moe_topk(many[:1], k, **kw)
+    assert (got[0][:-6] == first[0]).all() and (got[1][:-6] == first[1]).all()

@@ -407,10 +407,10 @@ typedef enum {
  *   gates_j = scale * s[topk_ids_j], with renorm divided by the sum of the
  *     chosen s (0 if that sum is 0).
  * The choice is the one 64-bit arithmetic makes; gates are computed in fp32 and
- * are within 21 * 2^-24 of their size (about ten units in the last place at most),
- * whatever the size of the logits.  A row that holds a NaN (for softmax also
- * +inf) has no scores: its ids are -1 and its gates NaN.  Rows are independent: a
- * row's bits depend neither on other rows nor on their number.
+ * are within 21 * 2^-24 of their size, whatever the size of the logits.  A row
+ * that holds a NaN (for softmax also +inf) has no scores: its ids are -1 and its
+ * gates NaN.  Rows are independent: a row's bits depend neither on other rows nor
+ * on their number.
  * Limits: 1 <= E <= 1024, 1 <= top_k <= 64 (FTQ_ERR_UNSUPPORTED above), n_group
  * >= 1 divides E, n_group <= 64 (FTQ_ERR_UNSUPPORTED above), 1 <= topk_group <=
  * n_group, 1 <= group_top <= min(2, E/n_group), top_k <= topk_group*E/n_group, T >= 0

@@ -516,7 +516,8 @@ int run_topk(const TopkArgs& m, hipStream_t s)
     // Many rows: more experts a lane, so that a reduction serves more rows (8191 x 128, bf16: 16 lanes of 8 take 5.7 us,
     // 64 of 2 9.5; 32768 x 256, groups: 16 of 16 take 36, 64 of 4 63).  Few: more lanes, a shorter chain (2048 x 128:
     // 4.9 against 4.7; 2048 x 256, groups: 12.0 against 10.1).  Both layouts of a size have the same product, and so the
-    // same keys and the same bits of a row in either.
+    // same keys and the same bits of a row in either.  (More than 14 choices do not fit 16 lanes and keep the 64: 32768 x
+    // 256, 16 of them 64 us and in bf16 20 of them 45; 32 lanes of 16, whose product is another, took 59 and 50.)
     const bool many = m.T >= 4096;
     if (fits(64, 2)) return many && fits(16, 8) ? launch_topk<16, 8>(m, lim, s) : launch_topk<64, 2>(m, lim, s);
     if (fits(64, 4)) return many && fits(16, 16) ? launch_topk<16, 16>(m, lim, s) : launch_topk<64, 4>(m, lim, s);

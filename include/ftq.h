@@ -18,7 +18,9 @@
  *
  * Around it: quantisers, the top-k combine, the fused gated activation, other
  * GGUF weight types, the router (ftq_moe_topk), and the same matmul for experts
- * in 8-bit floating point with one scale per 128 x 128 block (ftq_moe_fp8).
+ * in 8-bit floating point with one scale per 128 x 128 block (ftq_moe_fp8); and what
+ * trains beside frozen experts: balance loss, gradients of router and combine, and
+ * low-rank adapters, which also serve many requests at once (ftq_lora).
  *
  * Block formats (GGUF; the pages name them, the layouts are the GGUF ones):
  *   Q4_0 block, 18 bytes: fp16 d, then 16 bytes; byte i holds element i in its
@@ -507,6 +509,146 @@ int ftq_moe_fp8_routed(const void* w, const float* w_scale, const void* a, const
                        const int32_t* topk_ids, void* out, int out_dtype, int64_t E, int64_t N, int64_t K, int64_t T,
                        int64_t top_k, int act_per_pair, int act, void* workspace, size_t workspace_bytes, int path,
                        hipStream_t stream);
+
+/*
+ * ---- Training the router and low-rank adapters beside frozen experts ----------
+ *
+ * The experts' weights stay as they are; what learns beside them are the router
+ * (through its gates and a balance loss) and low-rank adapters, which also serve
+ * many requests at once beside any shared projection.  From the gradient of a
+ * layer's output:
+ *
+ *   ftq_moe_combine_topk_backward -> d_gates -> ftq_moe_topk_backward (with the loss of ftq_moe_balance)
+ *                                 -> d_y     -> ftq_lora_backward
+ */
+
+/*
+ * Balance loss and per-expert counts of packed sequences.  For sequence s with n_s
+ * counted rows, c_se their (token, choice) pairs that name expert e, and p_te the
+ * share of expert e in the sum of row t's scores (softmax or sigmoid):
+ *
+ *   loss[s] = E / (top_k * n_s^2) * sum_e c_se * sum_{t in s} p_te      (0 if n_s == 0)
+ *
+ * which is 1 when pairs and probabilities are spread evenly.
+ *   logits   dtype [T][E], row t at element t*ld, as ftq_moe_topk takes them.
+ *   topk_ids int32 [T][top_k]; ids outside [0, E) count for no expert, an id that
+ *            occurs twice in a row counts twice.
+ *   valid    uint8 [T] or NULL: rows with 0 (padding) count nowhere, whatever they
+ *            hold.
+ *   offsets  int32 [S + 1] or NULL (then S == 1: all rows): sequence s is rows
+ *            offsets[s] .. offsets[s + 1] - 1, ascending, at most T; sequences may be
+ *            empty, and rows before the first and behind the last belong to none.
+ *   counts   int32 [S][E], tokens int32 [S] (n_s), loss fp32 [S], written.
+ *   workspace: ftq_moe_balance_workspace_bytes(T, E, top_k, S) bytes, 256-byte aligned.
+ * Counts are exact; probabilities are fp32 and summed in fp32 over at most T/512
+ * (or 64) rows and then in fp64, in a fixed order: the same call gives the same bits.
+ * A row without a finite logit has p = 0; one that holds a NaN (for softmax also +inf) makes
+ * its sequence's loss NaN.  T == 0 writes zeros.  Limits: E <= 1024, top_k <= 64
+ * (FTQ_ERR_UNSUPPORTED above), S >= 1, T*top_k < 2^31, S < 2^31.
+ */
+int64_t ftq_moe_balance_workspace_bytes(int64_t T, int64_t E, int64_t top_k, int64_t S);
+
+int ftq_moe_balance(const void* logits, int dtype, int64_t ld, const int32_t* topk_ids, const uint8_t* valid,
+                    const int32_t* offsets, int32_t* counts, int32_t* tokens, float* loss, int64_t T, int64_t E,
+                    int64_t top_k, int64_t S, int score, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Gradient of the router's logits from those of its gates (as ftq_moe_topk made
+ * them: score, renorm, scale; the choice itself has none) and of the balance losses:
+ *   d_gates  fp32 [T][top_k], or NULL.
+ *   d_loss   fp32 [S], or NULL; with it counts [S][E] and tokens [S] of
+ *            ftq_moe_balance (which are taken as constants), offsets and S as there.
+ *   valid    uint8 [T] or NULL: rows with 0 get zeros.
+ *   d_logits dtype [T][E], row t at element t*ld_d, all T rows written: fp32 sums,
+ *            rounded once to dtype.
+ * Ids outside [0, E) take no part; an id that occurs twice stands for two choices of
+ * one expert.  Experts whose logit is -inf have gradient 0.  A row whose logits hold a NaN
+ * has NaN from the balance loss, and nothing from gates if its ids name no expert.
+ * Renormalised gates have their gradient relative to the largest chosen logit, so that
+ * choices far below the row's largest keep theirs.  At least one of d_gates
+ * and d_loss; other limits as ftq_moe_balance.  T == 0: no-op.
+ */
+int ftq_moe_topk_backward(const void* logits, int dtype, int64_t ld, const int32_t* topk_ids, const float* d_gates,
+                          const int32_t* counts, const int32_t* tokens, const float* d_loss, const uint8_t* valid,
+                          const int32_t* offsets, void* d_logits, int64_t ld_d, int64_t T, int64_t E, int64_t top_k,
+                          int64_t S, int score, int renorm, float scale, hipStream_t stream);
+
+/*
+ * Gradient of ftq_moe_combine_topk: d_y[t*top_k + j][n] = gates[t][j] * d_out[t][n],
+ * d_gates[t][j] = sum_n y[t*top_k + j][n] * d_out[t][n].
+ *   d_out fp32 [T][N]; y fp32 [T*top_k][N] (may be NULL without d_gates); gates fp32
+ *   [T][top_k] (may be NULL without d_y);
+ *   d_y   d_y_dtype [T*top_k][N], or NULL: the fp32 product, rounded to d_y_dtype;
+ *   d_gates fp32 [T][top_k], or NULL: fp32 sums in a fixed order.
+ * Outputs must not overlap inputs.  Pointers are aligned to their element size.  A pair's bits
+ * depend on its own row alone.  T == 0 is a no-op; errors as ftq_moe_combine_topk.
+ */
+int ftq_moe_combine_topk_backward(const float* d_out, const float* y, const float* gates, void* d_y, int d_y_dtype,
+                                  float* d_gates, int64_t T, int64_t top_k, int64_t N, hipStream_t stream);
+
+/*
+ * Low-rank adapters of many requests beside a shared projection.  For pair p =
+ * t*top_k + j, l = topk_ids[t][j], activation row r = t (act_per_pair == 0) or p:
+ *
+ *   h[p] = A[l] x[r]        out[p] = base[p] + scale[l] * B[l] h[p]
+ *
+ * With top_k == 1 the ids are the requests' adapters and base the projection's result;
+ * with the router's ids (or combinations of them and a request's adapter) it
+ * adapts the experts, base being what the expert matmuls write.
+ *   x        dtype [T or T*top_k][K], row r at element r*ldx.
+ *   a, b     dtype [L][R][K] and [L][N][R]; ranks below R are padded with zeros.
+ *   scale    fp32 [L] or NULL (1).
+ *   topk_ids int32 [T][top_k]; ids outside [0, L) have no adapter: out[p] = base[p], h[p] = 0.
+ *   base     out_dtype [T*top_k][N], row p at element p*ld_base, or NULL (0).
+ *   out      out_dtype [T*top_k][N], row p at element p*ld_out, written; may be base
+ *            itself (then ld_out == ld_base), must not overlap anything else.
+ *   h        fp32 [T*top_k][R] or NULL: written, for ftq_lora_backward.
+ *   workspace: ftq_lora_workspace_bytes(...) bytes, 256-byte aligned (NULL if 0).
+ *   path     FTQ_PATH_GEMV takes the pairs in their order: best when rows of an
+ *            adapter lie together, as a request's do, or are few.  FTQ_PATH_GROUPED
+ *            sorts them by adapter first.  FTQ_PATH_AUTO: ftq_lora_select_path,
+ *            in order for top_k == 1 or few pairs, else sorted.
+ * Products and sums are fp32 (h too), out is rounded once.  A row's bits depend neither on other rows
+ * nor on the path, but for h's sums the number of parts they are split into goes by the sizes.  NaN and infinities of an
+ * adapter or a row reach only the pairs that use them.
+ * x, a, b, base, out and h are 16-byte aligned, their row strides whole 16-byte units.
+ * Limits: K, N and R multiples of 8; R <= 128 (FTQ_ERR_UNSUPPORTED above); L, K, N, R >= 1;
+ * L <= 4095 on the grouped path; T*top_k < 2^31; L, K and N < 2^31.  T == 0: no-op.
+ */
+int ftq_lora_select_path(int64_t L, int64_t T, int64_t top_k);
+
+int64_t ftq_lora_workspace_bytes(int64_t L, int64_t R, int64_t K, int64_t N, int64_t T, int64_t top_k, int dtype, int path);
+
+int ftq_lora(const void* x, int64_t ldx, const void* a, const void* b, const float* scale, const int32_t* topk_ids,
+             const void* base, int64_t ld_base, void* out, int64_t ld_out, float* h, int dtype, int out_dtype,
+             int64_t L, int64_t R, int64_t K, int64_t N, int64_t T, int64_t top_k, int act_per_pair, void* workspace,
+             size_t workspace_bytes, int path, hipStream_t stream);
+
+/*
+ * Gradients of ftq_lora.  With g[p] = scale[l] * B[l]^T d_out[p] (fp32):
+ *
+ *   d_x[r] = d_x_base[r] + sum over the pairs of row r of A[l]^T g[p]
+ *   d_a[l] = sum over the pairs of adapter l of g[p] x[r]^T
+ *   d_b[l] = scale[l] * sum over them of d_out[p] h[p]^T
+ *
+ *   d_out    dtype [T*top_k][N], row p at element p*ld_d (the gradient of base is d_out itself).
+ *   x, a, b, scale, topk_ids: as in the forward call (x is not read without d_a, a not without d_x,
+ *            b not without d_x and d_a: they may be NULL then).
+ *   h        fp32 [T*top_k][R] as ftq_lora wrote it (not read without d_b).
+ *   d_x_base dtype [rows][K] or NULL (0); may be d_x itself.
+ *   d_x      dtype [rows][K], or NULL: not wanted.  Rounded once.
+ *   d_a, d_b fp32 [L][R][K] and [L][N][R], or NULL: not wanted.  Written: adapters without a
+ *            pair get zeros.
+ *   workspace: ftq_lora_backward_workspace_bytes(...) bytes, 256-byte aligned.
+ * Sums are fp32 in a fixed order: the same call gives the same bits.  Alignment and limits as ftq_lora;
+ * L <= 4095, top_k <= 64 (FTQ_ERR_UNSUPPORTED above); at least one output.  T == 0 writes zeros to d_a and d_b.
+ */
+int64_t ftq_lora_backward_workspace_bytes(int64_t L, int64_t R, int64_t K, int64_t N, int64_t T, int64_t top_k, int dtype);
+
+int ftq_lora_backward(const void* d_out, int64_t ld_d, const void* x, int64_t ldx, const void* a, const void* b,
+                      const float* scale, const int32_t* topk_ids, const float* h, const void* d_x_base, void* d_x,
+                      float* d_a, float* d_b, int dtype, int64_t L, int64_t R, int64_t K, int64_t N, int64_t T,
+                      int64_t top_k, int act_per_pair, void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /*
  * Message for the last failing call on this thread ("" if none): for a

@@ -48,7 +48,79 @@ __global__ __launch_bounds__(kThreads) void combine_topk_kernel(const float* __r
     }
 }
 
+// The gradient: d_y[t*k+j][n] = gates[t][j] * d_out[t][n], and d_gates[t][j] the
+// dot product of y[t*k+j] and d_out[t].  One workgroup per pair reads its row of y
+// and its token's row of d_out once (the token's pairs follow one another, so that
+// d_out comes from the caches after the first) and writes its row of d_y.  A dot
+// product is summed by thread, then by a fixed tree.
+template <int VEC> struct RunF { float v[VEC]; } __attribute__((packed, aligned(4)));
+template <int VEC> struct RunH { uint16_t v[VEC]; } __attribute__((packed, aligned(2)));
+
+template <int VEC, int DT>
+__global__ __launch_bounds__(kThreads) void combine_topk_backward_kernel(const float* __restrict__ d_out, const float* __restrict__ y,
+                                                                         const float* __restrict__ gates, void* __restrict__ d_y,
+                                                                         float* __restrict__ d_gates, int64_t pairs, int64_t k, int64_t N)
+{
+    __shared__ float part[2][kThreads / 64];
+    int turn = 0;
+    for (int64_t p = blockIdx.x; p < pairs; p += gridDim.x, turn ^= 1) {
+        const float g = d_y ? gates[p] : 0.0f;        // (gates may be null without d_y, y without d_gates)
+        const float* dr = d_out + p / k * N;
+        const float* yr = y + p * N;
+        float dot = 0.0f;
+        for (int64_t c = (int64_t)threadIdx.x * VEC; c < N; c += kThreads * VEC) {
+            const RunF<VEC> d = *reinterpret_cast<const RunF<VEC>*>(dr + c);
+            if (d_gates) {
+                const RunF<VEC> v = *reinterpret_cast<const RunF<VEC>*>(yr + c);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) dot = __builtin_fmaf(v.v[i], d.v[i], dot);
+            }
+            if (d_y) {
+                if constexpr (DT == FTQ_F32) {
+                    RunF<VEC> o;
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) o.v[i] = g * d.v[i];
+                    *reinterpret_cast<RunF<VEC>*>(static_cast<float*>(d_y) + p * N + c) = o;
+                } else {
+                    RunH<VEC> o;
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) o.v[i] = DT == FTQ_F16 ? f16_of_f32(g * d.v[i]) : bf16_of_f32(g * d.v[i]);
+                    *reinterpret_cast<RunH<VEC>*>(static_cast<uint16_t*>(d_y) + p * N + c) = o;
+                }
+            }
+        }
+        if (!d_gates) continue;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) dot += __shfl_xor(dot, o);
+        if (threadIdx.x % 64 == 0) part[turn][threadIdx.x / 64] = dot;
+        __syncthreads();   // the next pair writes the other half of part
+        if (threadIdx.x == 0) {
+            dot = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kThreads / 64; ++w) dot += part[turn][w];
+            d_gates[p] = dot;
+        }
+    }
+}
+
 }  // namespace
+
+int run_combine_topk_backward(const float* d_out, const float* y, const float* gates, void* d_y, int dtype, float* d_gates,
+                              int64_t T, int64_t top_k, int64_t N, hipStream_t s)
+{
+    const int64_t pairs = T * top_k, grid = std::min<int64_t>(pairs, int64_t(1) << 20);
+    const auto go = [&](auto* kernel) {
+        return launch("combine_topk_backward_kernel", kernel, grid, kThreads, 0, s, d_out, y, gates, d_y, d_gates, pairs, top_k, N);
+    };
+    if (N % 4 == 0) {
+        if (dtype == FTQ_F32) return go(combine_topk_backward_kernel<4, FTQ_F32>);
+        if (dtype == FTQ_F16) return go(combine_topk_backward_kernel<4, FTQ_F16>);
+        return go(combine_topk_backward_kernel<4, FTQ_BF16>);
+    }
+    if (dtype == FTQ_F32) return go(combine_topk_backward_kernel<1, FTQ_F32>);
+    if (dtype == FTQ_F16) return go(combine_topk_backward_kernel<1, FTQ_F16>);
+    return go(combine_topk_backward_kernel<1, FTQ_BF16>);
+}
 
 int run_combine_topk(const float* y, const float* gates, float* out, int64_t T, int64_t top_k, int64_t N,
                      hipStream_t s)

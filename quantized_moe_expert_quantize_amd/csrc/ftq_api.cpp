@@ -1,5 +1,6 @@
 // The C entry points of libftq: argument validation, path choice, workspace
 // planning and dispatch.  No allocation, no synchronisation, no readback.
+#include <algorithm>
 #include <cstdarg>
 #include <mutex>
 
@@ -306,6 +307,69 @@ int fp8_common(const Fp8Args& m, bool per_pair, void* ws, size_t ws_bytes, int p
     return (phases & kMatmul) ? run_fp8_grouped(args, plan, ws, stream) : FTQ_OK;
 }
 
+// Sizes shared by the balance loss and the router's gradient.
+int check_router_rows(int dtype, int64_t ld, int64_t T, int64_t E, int64_t top_k, int64_t S, int score)
+{
+    if (!dtype_bytes(dtype)) { set_error("unknown element type %d", dtype); return FTQ_ERR_INVALID_ARG; }
+    if (score != FTQ_SCORE_SOFTMAX && score != FTQ_SCORE_SIGMOID) { set_error("unknown score function %d", score); return FTQ_ERR_INVALID_ARG; }
+    if (T < 0 || E < 1 || top_k < 1 || S < 1 || ld < E) {
+        set_error("need T >= 0, E >= 1, top_k >= 1, S >= 1 and row strides of at least E (got T=%lld E=%lld top_k=%lld S=%lld stride %lld)",
+                  (long long)T, (long long)E, (long long)top_k, (long long)S, (long long)ld);
+        return FTQ_ERR_INVALID_ARG;
+    }
+    if (E > kTopkMaxExperts || top_k > kTopkMaxK) {
+        set_error("at most %lld experts and %lld choices are supported (got %lld, %lld)", (long long)kTopkMaxExperts, (long long)kTopkMaxK,
+                  (long long)E, (long long)top_k);
+        return FTQ_ERR_UNSUPPORTED;
+    }
+    if (T > kMaxPairs / top_k || S > kMaxPairs || ld > INT64_MAX / 16 || T > INT64_MAX / 16 / ld) {
+        set_error("T*top_k and S are limited to 2^31-1, T*stride to 64-bit byte offsets");
+        return FTQ_ERR_UNSUPPORTED;
+    }
+    return FTQ_OK;
+}
+
+int check_lora_sizes(int dtype, int64_t L, int64_t R, int64_t K, int64_t N, int64_t T, int64_t top_k)
+{
+    if (!dtype_bytes(dtype)) { set_error("unknown element type %d", dtype); return FTQ_ERR_INVALID_ARG; }
+    if (L < 1 || R < 1 || K < 1 || N < 1 || top_k < 1 || T < 0 || R % 8 != 0 || K % 8 != 0 || N % 8 != 0) {
+        set_error("need L >= 1, top_k >= 1, T >= 0 and R, K, N positive multiples of 8 (got L=%lld R=%lld K=%lld N=%lld T=%lld top_k=%lld)",
+                  (long long)L, (long long)R, (long long)K, (long long)N, (long long)T, (long long)top_k);
+        return FTQ_ERR_INVALID_ARG;
+    }
+    if (R > kLoraMaxRank) { set_error("rank %lld exceeds the supported %lld", (long long)R, (long long)kLoraMaxRank); return FTQ_ERR_UNSUPPORTED; }
+    if (L > INT32_MAX || K > INT32_MAX || N > INT32_MAX || T > kMaxPairs / top_k) {
+        set_error("L, K, N and T*top_k are limited to 2^31-1");
+        return FTQ_ERR_UNSUPPORTED;
+    }
+    // byte offsets: L*R*max(K, N)*4, with room for sums of a few
+    if (std::max(K, N) > INT64_MAX / 64 / R / L || (T > 0 && std::max({K, N, R}) > INT64_MAX / 64 / (T * top_k))) {
+        set_error("tensor sizes overflow 64-bit byte offsets");
+        return FTQ_ERR_UNSUPPORTED;
+    }
+    return FTQ_OK;
+}
+
+// A row stride of `cols` elements of `esz` bytes: at least cols, whole 16-byte units.
+bool stride_ok(int64_t ld, int64_t cols, int64_t esz) { return ld >= cols && ld <= INT64_MAX / 64 / kMaxPairs && ld * esz % 16 == 0; }
+
+int check_lora_path(int path, int64_t L)
+{
+    if (path != FTQ_PATH_GEMV && path != FTQ_PATH_GROUPED) { set_error("unknown path %d", path); return FTQ_ERR_INVALID_ARG; }
+    if (path == FTQ_PATH_GROUPED && L > kMaxExperts) {
+        set_error("sorting by adapter takes at most %lld adapters (got %lld)", (long long)kMaxExperts, (long long)L);
+        return FTQ_ERR_UNSUPPORTED;
+    }
+    return FTQ_OK;
+}
+
+// What FTQ_PATH_AUTO takes: in order where sorting does not pay or the tables cannot hold the adapters.
+int resolve_lora_path(int path, int64_t L, int64_t T, int64_t top_k)
+{
+    if (path != FTQ_PATH_AUTO) return path;
+    return L > kMaxExperts ? FTQ_PATH_GEMV : lora_select_path(T, top_k);
+}
+
 }  // namespace
 
 int moe_q4_0_q8_1_call(const void* w, const void* a, const int32_t* ids, float* out, int64_t E, int64_t N, int64_t K,
@@ -591,6 +655,180 @@ int ftq_moe_fp8_routed(const void* w, const float* w_scale, const void* a, const
     const Fp8Args m{static_cast<const uint8_t*>(w), w_scale, static_cast<const uint8_t*>(a), a_scale, topk_ids, out,
                     E, N, K, T, top_k, 0, act, out_dtype & ~FTQ_EXACT, (out_dtype & FTQ_EXACT) != 0};
     return fp8_common(m, act_per_pair != 0, workspace, workspace_bytes, path, stream, kMatmul);
+}
+
+int64_t ftq_moe_balance_workspace_bytes(int64_t T, int64_t E, int64_t top_k, int64_t S)
+{
+    clear_error();
+    if (check_router_rows(FTQ_F32, std::max<int64_t>(E, 1), T, E, top_k, S, FTQ_SCORE_SOFTMAX) != FTQ_OK) return -1;
+    return balance_workspace(T, E, S);
+}
+
+int ftq_moe_balance(const void* logits, int dtype, int64_t ld, const int32_t* topk_ids, const uint8_t* valid,
+                    const int32_t* offsets, int32_t* counts, int32_t* tokens, float* loss, int64_t T, int64_t E,
+                    int64_t top_k, int64_t S, int score, void* workspace, size_t workspace_bytes, hipStream_t stream)
+{
+    clear_error();
+    int st = check_router_rows(dtype, ld, T, E, top_k, S, score);
+    if (st != FTQ_OK) return st;
+    if (!offsets && S != 1) { set_error("%lld sequences need offsets", (long long)S); return FTQ_ERR_INVALID_ARG; }
+    if (!counts || !tokens || !loss || (T > 0 && (!logits || !topk_ids))) {
+        set_error("null pointer argument (logits, topk_ids, counts, tokens or loss)");
+        return FTQ_ERR_INVALID_ARG;
+    }
+    if (!aligned(logits, dtype_bytes(dtype)) || !aligned(topk_ids, 4) || !aligned(offsets, 4) || !aligned(counts, 4) || !aligned(tokens, 4) ||
+        !aligned(loss, 4)) {
+        set_error("misaligned pointer (logits need their element's alignment, the others 4 bytes)");
+        return FTQ_ERR_INVALID_ARG;
+    }
+    st = check_workspace(balance_workspace(T, E, S), workspace, workspace_bytes);
+    if (st != FTQ_OK) return st;
+    const BalanceArgs m{logits, topk_ids, valid, offsets, counts, tokens, loss, T, S, ld, dtype, (int32_t)E, (int32_t)top_k, score};
+    return run_balance(m, workspace, stream);
+}
+
+int ftq_moe_topk_backward(const void* logits, int dtype, int64_t ld, const int32_t* topk_ids, const float* d_gates,
+                          const int32_t* counts, const int32_t* tokens, const float* d_loss, const uint8_t* valid,
+                          const int32_t* offsets, void* d_logits, int64_t ld_d, int64_t T, int64_t E, int64_t top_k,
+                          int64_t S, int score, int renorm, float scale, hipStream_t stream)
+{
+    clear_error();
+    int st = check_router_rows(dtype, std::min(ld, ld_d), T, E, top_k, S, score);
+    if (st == FTQ_OK) st = check_router_rows(dtype, std::max(ld, ld_d), T, E, top_k, S, score);
+    if (st != FTQ_OK) return st;
+    if (d_loss && !offsets && S != 1) { set_error("%lld sequences need offsets", (long long)S); return FTQ_ERR_INVALID_ARG; }
+    if (T == 0) return FTQ_OK;
+    if (!d_gates && !d_loss) { set_error("neither d_gates nor d_loss"); return FTQ_ERR_INVALID_ARG; }
+    if (!logits || !d_logits || (d_gates && !topk_ids) || (d_loss && (!counts || !tokens))) {
+        set_error("null pointer argument (logits, d_logits, topk_ids, or counts and tokens)");
+        return FTQ_ERR_INVALID_ARG;
+    }
+    const int64_t esz = dtype_bytes(dtype);
+    if (!aligned(logits, esz) || !aligned(d_logits, esz) || !aligned(topk_ids, 4) || !aligned(d_gates, 4) || !aligned(counts, 4) ||
+        !aligned(tokens, 4) || !aligned(d_loss, 4) || !aligned(offsets, 4)) {
+        set_error("misaligned pointer (logits and d_logits need their element's alignment, the others 4 bytes)");
+        return FTQ_ERR_INVALID_ARG;
+    }
+    const TopkBackwardArgs m{logits, topk_ids, d_gates, counts, tokens, d_loss, valid, offsets, d_logits, T, S, ld, ld_d, dtype, (int32_t)E,
+                             (int32_t)top_k, score, renorm != 0, scale};
+    return run_topk_backward(m, stream);
+}
+
+int ftq_moe_combine_topk_backward(const float* d_out, const float* y, const float* gates, void* d_y, int d_y_dtype,
+                                  float* d_gates, int64_t T, int64_t top_k, int64_t N, hipStream_t stream)
+{
+    clear_error();
+    if (T < 0 || top_k < 1 || N < 1) {
+        set_error("need T >= 0, top_k >= 1, N >= 1 (got T=%lld top_k=%lld N=%lld)", (long long)T, (long long)top_k, (long long)N);
+        return FTQ_ERR_INVALID_ARG;
+    }
+    const int64_t esz = dtype_bytes(d_y_dtype);
+    if (!esz) { set_error("unknown element type %d", d_y_dtype); return FTQ_ERR_INVALID_ARG; }
+    if (T > INT64_MAX / 8 / top_k / N) { set_error("T*top_k*N overflows 64-bit byte offsets"); return FTQ_ERR_UNSUPPORTED; }
+    if (T == 0) return FTQ_OK;
+    if (!d_y && !d_gates) { set_error("neither d_y nor d_gates"); return FTQ_ERR_INVALID_ARG; }
+    if (!d_out || (d_y && !gates) || (d_gates && !y)) { set_error("null pointer argument (d_out, gates or y)"); return FTQ_ERR_INVALID_ARG; }
+    if (!aligned(d_out, 4) || !aligned(y, 4) || !aligned(gates, 4) || !aligned(d_y, esz) || !aligned(d_gates, 4)) {
+        set_error("misaligned pointer (every array needs its element's alignment)");
+        return FTQ_ERR_INVALID_ARG;
+    }
+    return run_combine_topk_backward(d_out, y, gates, d_y, d_y_dtype, d_gates, T, top_k, N, stream);
+}
+
+int ftq_lora_select_path(int64_t L, int64_t T, int64_t top_k)
+{
+    clear_error();
+    const int st = check_lora_sizes(FTQ_F32, L, 8, 8, 8, T, top_k);
+    if (st != FTQ_OK) return -st;
+    return resolve_lora_path(FTQ_PATH_AUTO, L, T, top_k);
+}
+
+int64_t ftq_lora_workspace_bytes(int64_t L, int64_t R, int64_t K, int64_t N, int64_t T, int64_t top_k, int dtype, int path)
+{
+    clear_error();
+    if (check_lora_sizes(dtype, L, R, K, N, T, top_k) != FTQ_OK) return -1;
+    const int rp = resolve_lora_path(path, L, T, top_k);
+    if (check_lora_path(rp, L) != FTQ_OK) return -1;
+    return T == 0 ? 0 : lora_workspace(L, R, K, N, T, top_k, dtype, rp);
+}
+
+int ftq_lora(const void* x, int64_t ldx, const void* a, const void* b, const float* scale, const int32_t* topk_ids,
+             const void* base, int64_t ld_base, void* out, int64_t ld_out, float* h, int dtype, int out_dtype,
+             int64_t L, int64_t R, int64_t K, int64_t N, int64_t T, int64_t top_k, int act_per_pair, void* workspace,
+             size_t workspace_bytes, int path, hipStream_t stream)
+{
+    clear_error();
+    int st = check_lora_sizes(dtype, L, R, K, N, T, top_k);
+    if (st != FTQ_OK) return st;
+    const int64_t esz = dtype_bytes(dtype), osz = dtype_bytes(out_dtype);
+    if (!osz) { set_error("unknown element type %d", out_dtype); return FTQ_ERR_INVALID_ARG; }
+    const int rp = resolve_lora_path(path, L, T, top_k);
+    st = check_lora_path(rp, L);
+    if (st != FTQ_OK) return st;
+    if (!stride_ok(ldx, K, esz) || (base && !stride_ok(ld_base, N, osz)) || !stride_ok(ld_out, N, osz)) {
+        set_error("row strides must hold a row and be whole 16-byte units (x %lld, base %lld, out %lld elements)", (long long)ldx,
+                  (long long)ld_base, (long long)ld_out);
+        return FTQ_ERR_INVALID_ARG;
+    }
+    if (base && base == out && ld_base != ld_out) { set_error("out may be base only with the same row stride"); return FTQ_ERR_INVALID_ARG; }
+    if (T == 0) return FTQ_OK;
+    if (!x || !a || !b || !topk_ids || !out) { set_error("null pointer argument (x, a, b, topk_ids or out)"); return FTQ_ERR_INVALID_ARG; }
+    if (!aligned(x, 16) || !aligned(a, 16) || !aligned(b, 16) || !aligned(base, 16) || !aligned(out, 16) || !aligned(h, 16) ||
+        !aligned(scale, 4) || !aligned(topk_ids, 4)) {
+        set_error("misaligned pointer (x, a, b, base, out and h need 16-byte, scale and topk_ids 4-byte alignment)");
+        return FTQ_ERR_INVALID_ARG;
+    }
+    const int64_t need = lora_workspace(L, R, K, N, T, top_k, dtype, rp);
+    if (need > 0) {
+        st = check_workspace(need, workspace, workspace_bytes);
+        if (st != FTQ_OK) return st;
+    }
+    const LoraArgs m{x, a, b, scale, topk_ids, base, out, h, ldx, ld_base, ld_out, dtype, out_dtype, L, R, K, N, T, top_k,
+                     act_per_pair ? 1 : top_k};
+    return run_lora(m, workspace, rp, stream);
+}
+
+int64_t ftq_lora_backward_workspace_bytes(int64_t L, int64_t R, int64_t K, int64_t N, int64_t T, int64_t top_k, int dtype)
+{
+    clear_error();
+    if (check_lora_sizes(dtype, L, R, K, N, T, top_k) != FTQ_OK || check_lora_path(FTQ_PATH_GROUPED, L) != FTQ_OK) return -1;
+    return lora_backward_workspace(L, R, K, N, T, top_k, dtype);
+}
+
+int ftq_lora_backward(const void* d_out, int64_t ld_d, const void* x, int64_t ldx, const void* a, const void* b,
+                      const float* scale, const int32_t* topk_ids, const float* h, const void* d_x_base, void* d_x,
+                      float* d_a, float* d_b, int dtype, int64_t L, int64_t R, int64_t K, int64_t N, int64_t T,
+                      int64_t top_k, int act_per_pair, void* workspace, size_t workspace_bytes, hipStream_t stream)
+{
+    clear_error();
+    int st = check_lora_sizes(dtype, L, R, K, N, T, top_k);
+    if (st == FTQ_OK) st = check_lora_path(FTQ_PATH_GROUPED, L);
+    if (st != FTQ_OK) return st;
+    if (top_k > kTopkMaxK) { set_error("at most %lld pairs a token are supported (got %lld)", (long long)kTopkMaxK, (long long)top_k); return FTQ_ERR_UNSUPPORTED; }
+    const int64_t esz = dtype_bytes(dtype);
+    if (!stride_ok(ld_d, N, esz) || (d_a && !stride_ok(ldx, K, esz))) {
+        set_error("row strides must hold a row and be whole 16-byte units (d_out %lld, x %lld elements)", (long long)ld_d, (long long)ldx);
+        return FTQ_ERR_INVALID_ARG;
+    }
+    if (T == 0 && !d_a && !d_b) return FTQ_OK;
+    if (!d_x && !d_a && !d_b) { set_error("no output (d_x, d_a or d_b)"); return FTQ_ERR_INVALID_ARG; }
+    if (T > 0 && (!d_out || !topk_ids || (d_a && !x) || (d_x && !a) || ((d_x || d_a) && !b) || (d_b && !h))) {
+        set_error("null pointer argument (d_out, x, a, b, topk_ids or h)");
+        return FTQ_ERR_INVALID_ARG;
+    }
+    if (!aligned(d_out, 16) || !aligned(x, 16) || !aligned(a, 16) || !aligned(b, 16) || !aligned(h, 16) || !aligned(d_x_base, 16) ||
+        !aligned(d_x, 16) || !aligned(d_a, 16) || !aligned(d_b, 16) || !aligned(scale, 4) || !aligned(topk_ids, 4)) {
+        set_error("misaligned pointer (scale and topk_ids need 4-byte, the others 16-byte alignment)");
+        return FTQ_ERR_INVALID_ARG;
+    }
+    const int64_t need = lora_backward_workspace(L, R, K, N, T, top_k, dtype);
+    if (need > 0) {
+        st = check_workspace(need, workspace, workspace_bytes);
+        if (st != FTQ_OK) return st;
+    }
+    const LoraBackwardArgs m{d_out, x, a, b, scale, topk_ids, h, d_x_base, d_x, d_a, d_b, ld_d, ldx, dtype, L, R, K, N, T, top_k,
+                             act_per_pair ? 1 : top_k};
+    return run_lora_backward(m, workspace, stream);
 }
 
 const char* ftq_last_error(void) { return g_error.c_str(); }

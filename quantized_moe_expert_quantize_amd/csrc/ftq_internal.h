@@ -181,6 +181,81 @@ constexpr int64_t kTopkMaxK = 64;          // one lane of a wave per chosen expe
 constexpr int64_t kTopkMaxGroups = 64;     // one lane per group
 int run_topk(const TopkArgs& m, hipStream_t s);
 
+// Balance loss, and the gradient of gates and losses (balance.hip).
+struct BalanceArgs {
+    const void* logits;
+    const int32_t* ids;
+    const uint8_t* valid;      // [T] or null: rows that count
+    const int32_t* offsets;    // [S + 1] or null: one sequence of all rows
+    int32_t* counts;           // [S][E]
+    int32_t* tokens;           // [S]
+    float* loss;               // [S]
+    int64_t T, S, ld;
+    int dtype;
+    int32_t E, top_k, score;
+};
+struct TopkBackwardArgs {
+    const void* logits;
+    const int32_t* ids;
+    const float* d_gates;      // [T][top_k] or null
+    const int32_t* counts;
+    const int32_t* tokens;
+    const float* d_loss;       // [S] or null
+    const uint8_t* valid;
+    const int32_t* offsets;
+    void* d_logits;
+    int64_t T, S, ld, ld_d;
+    int dtype;
+    int32_t E, top_k, score, renorm;
+    float scale;
+};
+int64_t balance_workspace(int64_t T, int64_t E, int64_t S);
+int run_balance(const BalanceArgs& m, void* ws, hipStream_t s);
+int run_topk_backward(const TopkBackwardArgs& m, hipStream_t s);
+
+// Gradient of the top-k combine (combine.hip); d_y or d_gates may be null.
+int run_combine_topk_backward(const float* d_out, const float* y, const float* gates, void* d_y, int dtype, float* d_gates,
+                              int64_t T, int64_t top_k, int64_t N, hipStream_t s);
+
+// Low-rank adapters (lora.hip).
+struct LoraArgs {
+    const void* x;             // dtype [rows][K], row stride ldx
+    const void* a;             // dtype [L][R][K]
+    const void* b;             // dtype [L][N][R]
+    const float* scale;        // [L] or null
+    const int32_t* ids;        // [T][top_k]
+    const void* base;          // out_dtype [T*top_k][N] or null, row stride ld_base
+    void* out;                 // out_dtype [T*top_k][N], row stride ld_out
+    float* h;                  // [T*top_k][R] or null
+    int64_t ldx, ld_base, ld_out;
+    int dtype, out_dtype;
+    int64_t L, R, K, N, T, top_k;
+    int64_t act_div;           // row of pair p: p / act_div (top_k: per token; 1: per pair)
+};
+struct LoraBackwardArgs {
+    const void* d_out;         // dtype [T*top_k][N], row stride ld_d
+    const void* x;
+    const void* a;
+    const void* b;
+    const float* scale;
+    const int32_t* ids;
+    const float* h;            // [T*top_k][R]
+    const void* base;          // dtype [rows][K] or null: added to d_x
+    void* d_x;                 // dtype [rows][K] or null
+    float* d_a;                // [L][R][K] or null
+    float* d_b;                // [L][N][R] or null
+    int64_t ld_d, ldx;
+    int dtype;
+    int64_t L, R, K, N, T, top_k;
+    int64_t act_div;
+};
+constexpr int64_t kLoraMaxRank = 128;
+int64_t lora_workspace(int64_t L, int64_t R, int64_t K, int64_t N, int64_t T, int64_t top_k, int dtype, int path);
+int64_t lora_backward_workspace(int64_t L, int64_t R, int64_t K, int64_t N, int64_t T, int64_t top_k, int dtype);
+int lora_select_path(int64_t T, int64_t top_k);
+int run_lora(const LoraArgs& m, void* ws, int path, hipStream_t s);
+int run_lora_backward(const LoraBackwardArgs& m, void* ws, hipStream_t s);
+
 // 8-bit floating-point quantisers (fp8_quantize.hip).
 constexpr int kFp8Block = 128;
 int run_quantize_fp8(const void* x, int dtype, int64_t ld, int64_t T, int64_t K, void* y, float* scales, hipStream_t s);

@@ -49,6 +49,8 @@ EXPORTS = (
     "ftq_debug_force_block_threads", "ftq_debug_grouped_kernel", "ftq_debug_route_kernels", "ftq_debug_gemv_plan", "ftq_moe_q4_0_q8_1_noalloc",
     "ftq_moe_topk", "ftq_quantize_fp8", "ftq_quantize_fp8_weight",
     "ftq_moe_fp8_select_path", "ftq_moe_fp8_workspace_bytes", "ftq_moe_fp8", "ftq_moe_fp8_route", "ftq_moe_fp8_routed",
+    "ftq_moe_balance_workspace_bytes", "ftq_moe_balance", "ftq_moe_topk_backward", "ftq_moe_combine_topk_backward",
+    "ftq_lora_select_path", "ftq_lora_workspace_bytes", "ftq_lora", "ftq_lora_backward_workspace_bytes", "ftq_lora_backward",
 )
 
 
@@ -130,6 +132,24 @@ def lib() -> ctypes.CDLL:
         f.restype = I32
     L.ftq_moe_fp8_route.argtypes = [P, I64, I64, I64, P, SZ, I32, P]
     L.ftq_moe_fp8_route.restype = I32
+    L.ftq_moe_balance_workspace_bytes.argtypes = [I64, I64, I64, I64]
+    L.ftq_moe_balance_workspace_bytes.restype = I64
+    L.ftq_moe_balance.argtypes = [P, I32, I64, P, P, P, P, P, P, I64, I64, I64, I64, I32, P, SZ, P]
+    L.ftq_moe_balance.restype = I32
+    L.ftq_moe_topk_backward.argtypes = [P, I32, I64, P, P, P, P, P, P, P, P, I64, I64, I64, I64, I64, I32, I32, F, P]
+    L.ftq_moe_topk_backward.restype = I32
+    L.ftq_moe_combine_topk_backward.argtypes = [P, P, P, P, I32, P, I64, I64, I64, P]
+    L.ftq_moe_combine_topk_backward.restype = I32
+    L.ftq_lora_select_path.argtypes = [I64, I64, I64]
+    L.ftq_lora_select_path.restype = I32
+    L.ftq_lora_workspace_bytes.argtypes = [I64, I64, I64, I64, I64, I64, I32, I32]
+    L.ftq_lora_workspace_bytes.restype = I64
+    L.ftq_lora.argtypes = [P, I64, P, P, P, P, P, I64, P, I64, P, I32, I32, I64, I64, I64, I64, I64, I64, I32, P, SZ, I32, P]
+    L.ftq_lora.restype = I32
+    L.ftq_lora_backward_workspace_bytes.argtypes = [I64, I64, I64, I64, I64, I64, I32]
+    L.ftq_lora_backward_workspace_bytes.restype = I64
+    L.ftq_lora_backward.argtypes = [P, I64, P, I64, P, P, P, P, P, P, P, P, P, I32, I64, I64, I64, I64, I64, I64, I32, P, SZ, P]
+    L.ftq_lora_backward.restype = I32
     _lib = L
     return L
 
@@ -638,3 +658,195 @@ def moe_fp8_routed(w: torch.Tensor, w_scale: torch.Tensor, a: torch.Tensor, a_sc
     """moe_fp8 on pairs already routed into `workspace` by moe_fp8_route."""
     return _fp8_call(lib().ftq_moe_fp8_routed, w, w_scale, a, a_scale, topk_ids, E, N, K, per_pair, act, out, workspace,
                      path, exact, stream)
+
+
+# ---- training the router and low-rank adapters beside frozen experts ---------
+
+def balance_workspace_bytes(T: int, E: int, top_k: int, sequences: int = 1) -> int:
+    r = lib().ftq_moe_balance_workspace_bytes(T, E, top_k, sequences)
+    if r < 0:
+        raise FtqError(ERR_INVALID_ARG, last_error())
+    return r
+
+
+def _sequences(offsets, valid, T, dev):
+    """(address of offsets, number of sequences, address of valid)."""
+    if offsets is not None and (offsets.dim() != 1 or offsets.shape[0] < 2):
+        raise ValueError("offsets must be [sequences + 1]")
+    return (_here(offsets, "offsets", torch.int32, dev) if offsets is not None else None,
+            offsets.shape[0] - 1 if offsets is not None else 1,
+            _here(valid, "valid", torch.bool, dev, (T,)) if valid is not None else None)
+
+
+def _ids(topk_ids, T, dev):
+    if topk_ids.dim() != 2 or topk_ids.shape[0] != T:
+        raise ValueError(f"topk_ids must be [{T}, top_k]")
+    return _here(topk_ids, "topk_ids", torch.int32, dev), topk_ids.shape[1]
+
+
+def moe_balance(logits: torch.Tensor, topk_ids: torch.Tensor, score: int = SCORE_SOFTMAX, offsets: torch.Tensor | None = None,
+                valid: torch.Tensor | None = None, loss: torch.Tensor | None = None, counts: torch.Tensor | None = None,
+                tokens: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
+    """Balance loss of the sequences offsets [S + 1] delimits (None: one of all rows), rows where valid [T] is False
+    left out -> (fp32 loss [S], int32 counts [S, E], int32 tokens [S]) (see ftq_moe_balance)."""
+    dev = _device_for(logits, "logits")
+    p, dt, ld = _rows(logits, "logits", dev)
+    T, E = logits.shape
+    ids, top_k = _ids(topk_ids, T, dev)
+    off, S, ok = _sequences(offsets, valid, T, dev)
+    if loss is None:
+        loss = _empty((S,), torch.float32, logits.device, stream)
+    if counts is None:
+        counts = _empty((S, E), torch.int32, logits.device, stream)
+    if tokens is None:
+        tokens = _empty((S,), torch.int32, logits.device, stream)
+    if workspace is None:
+        workspace = _empty(balance_workspace_bytes(T, E, top_k, S), torch.uint8, logits.device, stream)
+    _check(lib().ftq_moe_balance(p, dt, ld, ids, ok, off, _here(counts, "counts", torch.int32, dev, (S, E)),
+                                 _here(tokens, "tokens", torch.int32, dev, (S,)), _here(loss, "loss", torch.float32, dev, (S,)),
+                                 T, E, top_k, S, score, _here(workspace, "workspace", torch.uint8, dev), workspace.numel(),
+                                 _stream_here(stream, dev)))
+    return loss, counts, tokens
+
+
+def moe_topk_backward(logits: torch.Tensor, topk_ids: torch.Tensor, d_gates: torch.Tensor | None = None,
+                      score: int = SCORE_SOFTMAX, renorm: bool = True, scale: float = 1.0, d_loss: torch.Tensor | None = None,
+                      counts: torch.Tensor | None = None, tokens: torch.Tensor | None = None,
+                      offsets: torch.Tensor | None = None, valid: torch.Tensor | None = None,
+                      out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Gradient of the logits from those of moe_topk's gates and of moe_balance's losses (either may be None), in the
+    logits' type (see ftq_moe_topk_backward)."""
+    dev = _device_for(logits, "logits")
+    p, dt, ld = _rows(logits, "logits", dev)
+    T, E = logits.shape
+    ids, top_k = _ids(topk_ids, T, dev)
+    off, S, ok = _sequences(offsets, valid, T, dev)
+    if d_loss is not None and (counts is None or tokens is None):
+        raise ValueError("d_loss needs counts and tokens")
+    if out is None:
+        out = _empty((T, E), logits.dtype, logits.device, stream)
+    if out.shape != (T, E) or out.dtype != logits.dtype:
+        raise ValueError(f"out must be {logits.dtype} {(T, E)}")
+    po, _, ldo = _rows(out, "out", dev)
+    _check(lib().ftq_moe_topk_backward(
+        p, dt, ld, ids, _here(d_gates, "d_gates", torch.float32, dev, (T, top_k)) if d_gates is not None else None,
+        _here(counts, "counts", torch.int32, dev, (S, E)) if d_loss is not None else None,
+        _here(tokens, "tokens", torch.int32, dev, (S,)) if d_loss is not None else None,
+        _here(d_loss, "d_loss", torch.float32, dev, (S,)) if d_loss is not None else None, ok, off, po, ldo, T, E, top_k, S,
+        score, int(renorm), scale, _stream_here(stream, dev)))
+    return out
+
+
+def combine_topk_backward(d_out: torch.Tensor, y: torch.Tensor, gates: torch.Tensor, d_y: torch.Tensor | None = None,
+                          d_y_dtype: torch.dtype = torch.float32, d_gates: torch.Tensor | None = None, stream=None):
+    """Gradient of combine_topk: fp32 d_out [T, N], y [T*top_k, N], gates [T, top_k] -> (d_y [T*top_k, N] in the type
+    of the given buffer or d_y_dtype, fp32 d_gates [T, top_k])."""
+    dev = _device_for(d_out, "d_out")
+    if d_out.dim() != 2 or gates.dim() != 2:
+        raise ValueError("d_out must be [T, N] and gates [T, top_k]")
+    (T, N), top_k = d_out.shape, gates.shape[1]
+    if d_y is None:
+        d_y = _empty((T * top_k, N), d_y_dtype, d_out.device, stream)
+    if d_gates is None:
+        d_gates = _empty((T, top_k), torch.float32, d_out.device, stream)
+    if d_y.dtype not in _DTYPE:
+        raise ValueError(f"d_y must be float32, float16 or bfloat16, got {d_y.dtype}")
+    _check(lib().ftq_moe_combine_topk_backward(
+        _here(d_out, "d_out", torch.float32, dev), _here(y, "y", torch.float32, dev, (T * top_k, N)),
+        _here(gates, "gates", torch.float32, dev, (T, top_k)), _here(d_y, "d_y", d_y.dtype, dev, (T * top_k, N)), _DTYPE[d_y.dtype],
+        _here(d_gates, "d_gates", torch.float32, dev, (T, top_k)), T, top_k, N, _stream_here(stream, dev)))
+    return d_y, d_gates
+
+
+def lora_select_path(L: int, T: int, top_k: int) -> int:
+    r = lib().ftq_lora_select_path(L, T, top_k)
+    if r < 0:
+        raise FtqError(-r, last_error())
+    return r
+
+
+def lora_workspace_bytes(L: int, R: int, K: int, N: int, T: int, top_k: int, dtype: torch.dtype, path: int = PATH_AUTO) -> int:
+    r = lib().ftq_lora_workspace_bytes(L, R, K, N, T, top_k, _DTYPE[dtype], path)
+    if r < 0:
+        raise FtqError(ERR_INVALID_ARG, last_error())
+    return r
+
+
+def lora_backward_workspace_bytes(L: int, R: int, K: int, N: int, T: int, top_k: int, dtype: torch.dtype) -> int:
+    r = lib().ftq_lora_backward_workspace_bytes(L, R, K, N, T, top_k, _DTYPE[dtype])
+    if r < 0:
+        raise FtqError(ERR_INVALID_ARG, last_error())
+    return r
+
+
+def _adapters(x, a, b, topk_ids, per_pair, scale, dev):
+    """(L, R, K, N, T, top_k) of a call, with its shapes checked, and the addresses of a, b, scale and topk_ids."""
+    if a.dim() != 3 or b.dim() != 3 or topk_ids.dim() != 2 or x.dim() != 2:
+        raise ValueError("need x [rows, K], a [L, R, K], b [L, N, R] and topk_ids [T, top_k]")
+    (L, R, K), N, (T, top_k) = a.shape, b.shape[1], topk_ids.shape
+    rows = T * top_k if per_pair else T
+    if x.shape != (rows, K):
+        raise ValueError(f"x must have the shape {(rows, K)}, got {tuple(x.shape)}")
+    return (L, R, K, N, T, top_k), (_here(a, "a", x.dtype, dev), _here(b, "b", x.dtype, dev, (L, N, R)),
+                                    _here(scale, "scale", torch.float32, dev, (L,)) if scale is not None else None,
+                                    _here(topk_ids, "topk_ids", torch.int32, dev))
+
+
+def lora(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, topk_ids: torch.Tensor, scale: torch.Tensor | None = None,
+         base: torch.Tensor | None = None, per_pair: bool = False, path: int = PATH_AUTO, out: torch.Tensor | None = None,
+         out_dtype: torch.dtype | None = None, h: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+         stream=None) -> torch.Tensor:
+    """Low-rank adapters a [L, R, K], b [L, N, R] on the rows x [T or T*top_k, K] (may be strided): out [T*top_k, N] =
+    base + scale * b (a x) with the adapter that topk_ids [T, top_k] names (ids outside [0, L): base alone).  out may be
+    base itself; h (fp32 [T*top_k, R]) keeps a x for lora_backward (see ftq_lora)."""
+    dev = _device_for(x, "x")
+    px, dt, ldx = _rows(x, "x", dev)
+    (L, R, K, N, T, top_k), (pa, pb, ps, ids) = _adapters(x, a, b, topk_ids, per_pair, scale, dev)
+    pairs = T * top_k
+    pbase, dbase, ldbase = _rows(base, "base", dev) if base is not None else (None, None, 0)
+    if out is None:
+        out = _empty((pairs, N), base.dtype if base is not None else out_dtype or x.dtype, x.device, stream)
+    po, do, ldo = _rows(out, "out", dev)
+    if out.shape != (pairs, N) or (base is not None and (base.shape != (pairs, N) or dbase != do)):
+        raise ValueError(f"out and base must be {(pairs, N)} of one type")
+    if base is not None and pbase == po:               # one row has no stride of its own
+        ldbase = ldo = max(ldbase, ldo)
+    if workspace is None:
+        need = lora_workspace_bytes(L, R, K, N, T, top_k, x.dtype, path)
+        workspace = _empty(need, torch.uint8, x.device, stream) if need else None
+    _check(lib().ftq_lora(
+        px, ldx, pa, pb, ps, ids, pbase, ldbase, po, ldo, _here(h, "h", torch.float32, dev, (pairs, R)) if h is not None else None,
+        dt, do, L, R, K, N, T, top_k, int(per_pair), _here(workspace, "workspace", torch.uint8, dev) if workspace is not None else None,
+        workspace.numel() if workspace is not None else 0, path, _stream_here(stream, dev)))
+    return out
+
+
+def lora_backward(d_out: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, topk_ids: torch.Tensor,
+                  h: torch.Tensor, scale: torch.Tensor | None = None, base: torch.Tensor | None = None, per_pair: bool = False,
+                  d_x: torch.Tensor | None = None, d_a: torch.Tensor | None = None, d_b: torch.Tensor | None = None,
+                  workspace: torch.Tensor | None = None, stream=None):
+    """Gradients of lora: d_out [T*top_k, N] (x's type; may be strided) and the forward call's inputs and h -> (d_x
+    [rows, K] in x's type, plus base if given; fp32 d_a [L, R, K], d_b [L, N, R]) (see ftq_lora_backward)."""
+    dev = _device_for(x, "x")
+    px, dt, ldx = _rows(x, "x", dev)
+    (L, R, K, N, T, top_k), (pa, pb, ps, ids) = _adapters(x, a, b, topk_ids, per_pair, scale, dev)
+    pd, dd, ldd = _rows(d_out, "d_out", dev)
+    if d_out.shape != (T * top_k, N) or dd != dt:
+        raise ValueError(f"d_out must be {x.dtype} {(T * top_k, N)}")
+    if d_x is None:
+        d_x = _empty(tuple(x.shape), x.dtype, x.device, stream)
+    if d_a is None:
+        d_a = _empty((L, R, K), torch.float32, x.device, stream)
+    if d_b is None:
+        d_b = _empty((L, N, R), torch.float32, x.device, stream)
+    if workspace is None:
+        need = lora_backward_workspace_bytes(L, R, K, N, T, top_k, x.dtype)
+        workspace = _empty(need, torch.uint8, x.device, stream) if need else None
+    shape = tuple(x.shape)
+    _check(lib().ftq_lora_backward(
+        pd, ldd, px, ldx, pa, pb, ps, ids, _here(h, "h", torch.float32, dev, (T * top_k, R)),
+        _here(base, "base", x.dtype, dev, shape) if base is not None else None, _here(d_x, "d_x", x.dtype, dev, shape),
+        _here(d_a, "d_a", torch.float32, dev, (L, R, K)), _here(d_b, "d_b", torch.float32, dev, (L, N, R)), dt, L, R, K, N, T, top_k,
+        int(per_pair), _here(workspace, "workspace", torch.uint8, dev) if workspace is not None else None,
+        workspace.numel() if workspace is not None else 0, _stream_here(stream, dev)))
+    return d_x, d_a, d_b

@@ -7,148 +7,1041 @@
 //
 //   d_x = sum over a row's pairs of A_l^T g[p],
 //   dA_l = sum over the adapter's pairs of g[p] x^T,   dB_l = s_l * the same of d_out[p] h[p]^T.
+//
+// Everything is bound by the long rows (x, base, out, d_out, d_x), which are read or
+// written once each but for d_out, read for g and for dB; the rank-sized values between
+// are small.  Three products, each on the matrix units:
+//
+//   shrink   [R x C] times a row: rows and weights come through LDS in 128-byte pieces
+//            by asynchronous copies several pieces ahead; the row's length is split over
+//            workgroups, whose parts the reader adds up in their order;
+//   expand   [C x R] times an R-vector, added to base: one pass over the columns;
+//   outer    sums over an adapter's pairs of R-vector times row: pairs sorted by adapter
+//            (bucket.hip) in tiles of 32, each workgroup a run of tiles and 512 bytes of columns.
+//
+// A tile of rows may hold several adapters: shrink and expand go through them one by
+// one, each time for the whole tile, and keep each row's results of its own adapter
+// alone, so that no row ever sees another's weights.  An adapter's R-vectors are fp32.
+// As operands beside 16-bit weights or rows they are split into a sum of 16-bit
+// pieces, three in bf16 (24 bits) or two in fp16 (22 bits, scaled by a power of two to
+// the middle of its range), and every piece is multiplied: products are as exact as fp32's.
+#include <type_traits>
+
 #include "ftq_internal.h"
+#include "lds_copy.h"
 
 namespace ftq {
 namespace {
 
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short i16x4 __attribute__((ext_vector_type(4)));
+
 constexpr int kThreads = 256;
+constexpr int kLine = 128;                             // bytes of a row in one piece
+constexpr float kInf = __builtin_inff();
+
+template <int DT> constexpr int kSize = DT == FTQ_F32 ? 4 : 2;
+template <int DT> constexpr int kPieces = DT == FTQ_F32 ? 1 : DT == FTQ_F16 ? 2 : 3;
+
+__device__ const u32x4 kZeros = {0u, 0u, 0u, 0u};      // what a copy reads in place of what is not there
+
+__device__ __forceinline__ bool adapter_ok(int32_t id, int32_t L) { return id >= 0 && id < L; }
+
+// 16 rows x 16 columns += 64 bytes of 16 rows on either side.  Lane l holds 16 bytes of
+// row l%16 of each operand, and results 4*(l/16) .. +3 of the left's rows for row l%16
+// of the right.  (fp32: four instructions, one element of every lane's each; the order
+// of the products within the 64 bytes does not matter while both sides have the same.)
+template <int DT>
+__device__ __forceinline__ f32x4 multiply(u32x4 a, u32x4 b, f32x4 c)
+{
+    if constexpr (DT == FTQ_F16) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+    } else if constexpr (DT == FTQ_BF16) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+    } else {
+        const f32x4 x = __builtin_bit_cast(f32x4, a), y = __builtin_bit_cast(f32x4, b);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(x[e], y[e], c, 0, 0, 0);
+        return c;
+    }
+}
+
+// The next 16-bit piece of v; v becomes what is left of it.
+template <int DT>
+__device__ __forceinline__ uint16_t take_piece(float& v)
+{
+    if constexpr (DT == FTQ_F16) {
+        const uint16_t h = f16_of_f32(v);
+        v -= f32_of_f16(h);
+        return h;
+    } else {
+        const uint16_t h = bf16_of_f32(v);
+        v -= f32_of_bf16(h);
+        return h;
+    }
+}
+
+// The exponent e for which size * 2^-e lies in [2^12, 2^13), in the middle of fp16's range
+// (0 for sizes that have none; bounded, so that 2^e and 2^-e are normal numbers).
+__device__ __forceinline__ int middle_exponent(float size)
+{
+    if (!(size > 0.0f && size < kInf)) return 0;
+    const int e = __builtin_amdgcn_frexp_expf(size) - 13;
+    return min(max(e, -110), 110);
+}
+
+// ---- shrink: z[p] = W_l v[row of p] ---------------------------------------------
+
+struct ShrinkArgs {
+    const uint8_t* v;          // rows
+    int64_t ldv;               // bytes from row to row
+    const uint8_t* w;          // [L][R][C]
+    const int32_t* ids;        // [pairs]
+    const int32_t* sorted;     // [pairs] or null: pairs in the order of tiles
+    float* part;               // [splits][pairs][R]
+    int64_t pairs, row_bytes;  // bytes of C elements
+    int32_t div, L, R;
+    int32_t splits, steps;     // 128-byte steps of a split
+    int32_t groups;            // workgroups that share a tile's adapters
+};
+
+constexpr int kDepth = 4;      // pieces in LDS: one is multiplied while three are on their way
+
+// A workgroup takes 16 rows a wave.  LDS: run c (16 bytes) of row x sits at c ^ (x % 8).
+template <int DT, int WAVES, int RT>
+__global__ __launch_bounds__(64 * WAVES) void lora_shrink_kernel(ShrinkArgs m)
+{
+    constexpr int BM = 16 * WAVES;
+    constexpr int kW = 2 * RT, kShare = (kW + WAVES - 1) / WAVES;   // copies of the weights' rows: in all, and a wave's
+    constexpr int kPer = 2 + kShare;                               // copies of a wave and step
+    __shared__ u32x4 xs[kDepth][BM][8];
+    __shared__ u32x4 ws[kDepth][16 * RT][8];
+    const int lane = threadIdx.x & 63, wave = uniform((int32_t)(threadIdx.x >> 6));
+    const int r16 = lane & 15, q = lane >> 4;
+    const int64_t item = blockIdx.x, at = item / m.splits;
+    const int ks = (int)(item - at * m.splits), g = (int)(at % m.groups);
+    const int64_t slot0 = at / m.groups * BM;
+    const int rows = (int)min((int64_t)BM, m.pairs - slot0);
+    // lane i: row i of the tile
+    int32_t pair = 0, id = -1;
+    if (lane < rows) {
+        pair = m.sorted ? m.sorted[slot0 + lane] : (int32_t)(slot0 + lane);
+        id = m.ids[pair];
+        if (!adapter_ok(id, m.L)) id = -1;
+    }
+    uint64_t todo = __ballot(id >= 0);
+    const int cr = lane >> 3, run = (lane & 7) ^ cr;               // row of eight and 16-byte run that this lane copies
+    const uint8_t* xsrc[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) xsrc[i] = m.v + (int64_t)(__shfl(pair, min((wave * 2 + i) * 8 + cr, rows - 1)) / m.div) * m.ldv;
+    const int64_t total = (m.row_bytes + kLine - 1) / kLine, first = (int64_t)ks * m.steps;
+    const int n = (int)max((int64_t)0, min((int64_t)m.steps, total - first));
+    const int32_t my_pair = __shfl(pair, wave * 16 + r16);
+    for (int index = 0; todo; ++index) {
+        const int32_t l = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
+        const uint64_t mine = __ballot(id == l);
+        todo &= ~mine;
+        if (index % m.groups != g) continue;
+        const uint8_t* wsrc[kShare];
+#pragma unroll
+        for (int i = 0; i < kShare; ++i) wsrc[i] = m.w + ((int64_t)l * m.R + min((wave + i * WAVES) % kW * 8 + cr, m.R - 1)) * m.row_bytes;
+        const auto copy_step = [&](int s) {
+            const int64_t byte = (first + s) * kLine + run * 16;
+            const bool in = byte < m.row_bytes;
+            const uint8_t* none = reinterpret_cast<const uint8_t*>(&kZeros);
+            const int buf = s % kDepth;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) copy16(lds_address(&xs[buf][(wave * 2 + i) * 8][0]), in ? xsrc[i] + byte : none);
+#pragma unroll
+            for (int i = 0; i < kShare; ++i) copy16(lds_address(&ws[buf][(wave + i * WAVES) % kW * 8][0]), in ? wsrc[i] + byte : none);
+        };
+        f32x4 acc[RT] = {};
+        block_barrier();                                           // the last adapter's pieces have been read
+        for (int s = 0; s < kDepth - 1 && s < n; ++s) copy_step(s);
+        for (int s = 0; s < n; ++s) {
+            if (n - 1 - s >= 2) wait_copies_but<2 * kPer>();
+            else if (n - 1 - s == 1) wait_copies_but<kPer>();
+            else wait_copies();
+            block_barrier();                                       // all waves' copies of step s are there, step s - 1 has been read
+            if (s + kDepth - 1 < n) copy_step(s + kDepth - 1);
+            const int buf = s % kDepth;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const u32x4 x = xs[buf][wave * 16 + r16][(4 * h + q) ^ (r16 & 7)];
+#pragma unroll
+                for (int i = 0; i < RT; ++i) acc[i] = multiply<DT>(ws[buf][16 * i + r16][(4 * h + q) ^ (r16 & 7)], x, acc[i]);
+            }
+        }
+        if (mine >> (wave * 16 + r16) & 1) {
+            float* z = m.part + ((int64_t)ks * m.pairs + my_pair) * m.R;
+#pragma unroll
+            for (int i = 0; i < RT; ++i) {
+                if (16 * i + 4 * q < m.R) *reinterpret_cast<f32x4*>(z + 16 * i + 4 * q) = acc[i];
+            }
+        }
+    }
+}
+
+// ---- expand: out[row] = base[row] + f_l * W_l z[p] ---------------------------------
+
+struct ExpandArgs {
+    const float* part;         // [splits][pairs][R]
+    const uint8_t* w;          // [L][C][R]
+    const float* scale;        // [L] or null
+    const int32_t* ids;
+    const int32_t* sorted;     // or null
+    const void* base;          // or null
+    void* out;
+    float* h;                  // [pairs][R] or null: the sum of the parts
+    int64_t ld_base, ld_out, pairs, C;
+    int32_t L, R, splits, groups;
+    int64_t col_items;         // workgroups along the columns
+    int32_t cols;              // columns of a workgroup, a multiple of 256
+};
 
 template <int DT> __device__ __forceinline__ float load1(const void* p, int64_t i)
 {
     if constexpr (DT == FTQ_F32) return static_cast<const float*>(p)[i];
     else return DT == FTQ_F16 ? f32_of_f16(static_cast<const uint16_t*>(p)[i]) : f32_of_bf16(static_cast<const uint16_t*>(p)[i]);
 }
-template <int DT> __device__ __forceinline__ void store1(void* p, int64_t i, float v)
-{
-    if constexpr (DT == FTQ_F32) static_cast<float*>(p)[i] = v;
-    else static_cast<uint16_t*>(p)[i] = DT == FTQ_F16 ? f16_of_f32(v) : bf16_of_f32(v);
-}
-__device__ __forceinline__ bool adapter_ok(int32_t id, int64_t L) { return id >= 0 && id < L; }
 
-// z[p][r] = f_l * sum_c w[l*w_l + r*w_r + c*w_c] * v[row][c]: a wave per pair.
-template <int DT>
-__global__ __launch_bounds__(kThreads) void lora_shrink_kernel(const void* v, int64_t ldv, int64_t div, const void* w, int64_t w_l,
-                                                               int64_t w_r, int64_t w_c, const float* scale, const int32_t* ids,
-                                                               float* z, int64_t L, int64_t R, int64_t C, int64_t pairs)
+// N consecutive results v added to 16 bytes of base, rounded to OT and stored.
+template <int OT, int N>
+__device__ __forceinline__ void add_and_store(void* out, int64_t i, u32x4 base, const float (&v)[N])
 {
-    const int lane = threadIdx.x % 64;
-    for (int64_t p = (int64_t)blockIdx.x * 4 + threadIdx.x / 64; p < pairs; p += (int64_t)gridDim.x * 4) {
-        const int32_t id = ids[p];
-        for (int64_t r = 0; r < R; ++r) {
-            float sum = 0.0f;
-            if (adapter_ok(id, L)) {
-                for (int64_t c = lane; c < C; c += 64) sum = __builtin_fmaf(load1<DT>(w, id * w_l + r * w_r + c * w_c), load1<DT>(v, p / div * ldv + c), sum);
-                if (scale) sum *= scale[id];
+    if constexpr (OT == FTQ_F32) {
+        static_assert(N == 4);
+        f32x4 b = __builtin_bit_cast(f32x4, base);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) b[e] += v[e];
+        *reinterpret_cast<f32x4*>(static_cast<float*>(out) + i) = b;
+    } else {
+        static_assert(N == 8);
+        u32x4 r;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint16_t lo = (uint16_t)base[e], hi = (uint16_t)(base[e] >> 16);
+            if constexpr (OT == FTQ_F16) {
+                r[e] = f16_of_f32(f32_of_f16(lo) + v[2 * e]) | (uint32_t)f16_of_f32(f32_of_f16(hi) + v[2 * e + 1]) << 16;
+            } else {
+                r[e] = bf16_of_f32(f32_of_bf16(lo) + v[2 * e]) | (uint32_t)bf16_of_f32(f32_of_bf16(hi) + v[2 * e + 1]) << 16;
             }
-            for (int o = 1; o < 64; o <<= 1) sum += __shfl_xor(sum, o);
-            if (lane == 0) z[p * R + r] = sum;
         }
+        *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(out) + i) = r;
     }
 }
 
-// out[row][c] = base[row][c] + sum over the row's `per` pairs of f_l * sum_r z[p][r] * w[l*w_l + r*w_r + c*w_c].
-template <int DT, int OT>
-__global__ __launch_bounds__(kThreads) void lora_expand_kernel(const float* z, const void* w, int64_t w_l, int64_t w_r, int64_t w_c,
-                                                               const float* scale, const int32_t* ids, const void* base, int64_t ldb,
-                                                               void* out, int64_t ldo, int64_t L, int64_t R, int64_t C, int64_t rows,
-                                                               int64_t per)
+// A workgroup takes 16*BT rows and m.cols columns, a wave 64 of every 256.  W is the left
+// operand, so that a lane holds four columns of one row; which row of a 16-row tile is
+// which column is free and chosen so that a lane's results are whole 16-byte stores and
+// the four lanes of a row 64 bytes side by side: 32-bit results, row r of tile i is column
+// 16*i + r; 16-bit ones, column 32*(i/2) + 8*(r/4) + 4*(i%2) + r%4.
+// KST: 64-byte steps of an R-vector.
+template <int DT, int OT, int BT, int KST>
+__global__ __launch_bounds__(kThreads) void lora_expand_kernel(ExpandArgs m)
 {
-    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < rows * C; i += (int64_t)gridDim.x * kThreads) {
-        const int64_t row = i / C, c = i - row * C;
-        float sum = 0.0f;
-        for (int64_t p = row * per; p < (row + 1) * per; ++p) {
-            const int32_t id = ids[p];
-            if (!adapter_ok(id, L)) continue;
-            float part = 0.0f;
-            for (int64_t r = 0; r < R; ++r) part = __builtin_fmaf(z[p * R + r], load1<DT>(w, id * w_l + r * w_r + c * w_c), part);
-            sum += scale ? scale[id] * part : part;
+    constexpr int BM = 16 * BT, kElems = 64 / kSize<DT>;           // elements of a step
+    constexpr int kRank = KST * kElems, kQuads = kRank / 4;        // R rounded up
+    constexpr int kPad = KST > 1 ? 16 / kSize<DT> : 0;             // rows of 64 bytes meet no bank twice, longer ones are set apart
+    constexpr bool kWide = OT == FTQ_F32;
+    constexpr int kRun = kWide ? 4 : 8, kLoads = 64 / (4 * kRun);  // columns of a lane's store, stores of a row and wave
+    static_assert((kQuads & (kQuads - 1)) == 0 && kQuads <= 64);
+    using Elem = std::conditional_t<DT == FTQ_F32, float, uint16_t>;
+    __shared__ __attribute__((aligned(16))) Elem zs[kPieces<DT>][BM][kRank + kPad];
+    __shared__ float back[BM];                                     // 2^e of a row's pieces
+    __shared__ int32_t pair_lds[BM], id_lds[BM];
+    const int lane = threadIdx.x & 63, wave = uniform((int32_t)(threadIdx.x >> 6));
+    const int r16 = lane & 15, q = lane >> 4;
+    const int64_t item = blockIdx.x, at = item / m.col_items;
+    const int64_t c_first = (item - at * m.col_items) * m.cols;
+    const int g = (int)(at % m.groups);
+    const int64_t slot0 = at / m.groups * BM;
+    const int rows = (int)min((int64_t)BM, m.pairs - slot0);
+    int32_t pair = 0, id = INT32_MIN;                              // rows that are not there
+    if (lane < rows) {
+        pair = m.sorted ? m.sorted[slot0 + lane] : (int32_t)(slot0 + lane);
+        id = m.ids[pair];
+        if (!adapter_ok(id, m.L)) id = -1;
+    }
+    if (wave == 0 && lane < BM) {
+        pair_lds[lane] = pair;
+        id_lds[lane] = id;
+    }
+    uint64_t todo = __ballot(id != INT32_MIN);
+    int32_t pair_of[BT];
+#pragma unroll
+    for (int b = 0; b < BT; ++b) pair_of[b] = __shfl(pair, 16 * b + r16);
+    for (int index = 0; todo; ++index) {
+        const int32_t l = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
+        const uint64_t mine = __ballot(id == l);
+        todo &= ~mine;
+        if (index % m.groups != g) continue;
+        block_barrier();                                           // pair_lds is written, the last adapter's zs read
+        const float scale = l >= 0 && m.scale ? m.scale[l] : 1.0f;
+        for (int i = threadIdx.x; i < BM * kQuads; i += kThreads) {
+            const int row = i / kQuads, r = i % kQuads * 4;
+            const bool own = id_lds[row] == l && r < m.R;
+            f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};
+            if (own) {
+                const int64_t o = (int64_t)pair_lds[row] * m.R + r;
+                if (l >= 0) {
+                    for (int k = 0; k < m.splits; ++k) z += *reinterpret_cast<const f32x4*>(m.part + k * m.pairs * m.R + o);
+                }
+                if (m.h && c_first == 0) *reinterpret_cast<f32x4*>(m.h + o) = z;
+                z *= scale;
+            }
+            if constexpr (DT == FTQ_F32) {
+                *reinterpret_cast<f32x4*>(&zs[0][row][r]) = z;
+            } else {
+                if constexpr (DT == FTQ_F16) {
+                    float size = 0.0f;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) size = fmaxf(size, __builtin_fabsf(z[e]));
+#pragma unroll
+                    for (int o = 1; o < kQuads; o <<= 1) size = fmaxf(size, __shfl_xor(size, o));
+                    const int e2 = middle_exponent(size);
+                    z *= __builtin_ldexpf(1.0f, -e2);
+                    if (r == 0) back[row] = __builtin_ldexpf(1.0f, e2);
+                }
+#pragma unroll
+                for (int c = 0; c < kPieces<DT>; ++c) {
+                    u16x4 p;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float v = z[e];
+                        p[e] = take_piece<DT>(v);
+                        z[e] = v;
+                    }
+                    *reinterpret_cast<u16x4*>(&zs[c][row][r]) = p;
+                }
+            }
         }
-        store1<OT>(out, row * ldo + c, base ? load1<OT>(base, row * ldb + c) + sum : sum);
+        block_barrier();
+        for (int64_t c0 = c_first + wave * 64; c0 < min(c_first + m.cols, m.C); c0 += 256) {
+            u32x4 w[4][KST] = {}, base[BT][kLoads] = {};
+            if (l >= 0) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int c = kWide ? 16 * i + r16 : 32 * (i / 2) + 8 * (r16 / 4) + 4 * (i % 2) + r16 % 4;
+                    const uint8_t* src = m.w + (((int64_t)l * m.C + min(c0 + c, m.C - 1)) * m.R) * kSize<DT> + q * 16;
+#pragma unroll
+                    for (int k = 0; k < KST; ++k) {
+                        if (k * kElems + q * (16 / kSize<DT>) < m.R) w[i][k] = *reinterpret_cast<const u32x4*>(src + k * 64);
+                    }
+                }
+            }
+            if (m.base) {
+#pragma unroll
+                for (int b = 0; b < BT; ++b) {
+                    const bool own = mine >> (16 * b + r16) & 1;
+#pragma unroll
+                    for (int t = 0; t < kLoads; ++t) {
+                        const int64_t c = c0 + t * 4 * kRun + q * kRun;
+                        if (own && c < m.C) base[b][t] = *reinterpret_cast<const u32x4*>(static_cast<const uint8_t*>(m.base) + (pair_of[b] * m.ld_base + c) * kSize<OT>);
+                    }
+                }
+            }
+#pragma unroll
+            for (int b = 0; b < BT; ++b) {
+                f32x4 acc[4] = {};
+#pragma unroll
+                for (int k = 0; k < KST; ++k) {
+#pragma unroll
+                    for (int c = 0; c < kPieces<DT>; ++c) {
+                        const u32x4 z = *reinterpret_cast<const u32x4*>(&zs[c][16 * b + r16][k * kElems + q * (16 / kSize<DT>)]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) acc[i] = multiply<DT>(w[i][k], z, acc[i]);
+                    }
+                }
+                if (!(mine >> (16 * b + r16) & 1)) continue;
+                if (l < 0 && m.base == m.out) continue;            // in place: rows without an adapter stay as they are
+                const float f = DT == FTQ_F16 ? back[16 * b + r16] : 1.0f;
+#pragma unroll
+                for (int t = 0; t < kLoads; ++t) {
+                    const int64_t c = c0 + t * 4 * kRun + q * kRun;
+                    float v[kRun];
+#pragma unroll
+                    for (int e = 0; e < kRun; ++e) v[e] = kWide ? acc[t][e % 4] * f : acc[(2 * t + e / 4) & 3][e % 4] * f;
+                    if (c < m.C) add_and_store<OT>(m.out, pair_of[b] * m.ld_out + c, base[b][t], v);
+                }
+            }
+        }
     }
 }
 
-// d[l*w_l + r*w_r + c*w_c] = f_l * sum over the adapter's pairs of z[p][r] * v[row][c].
+// ---- d_x of rows that several pairs share -----------------------------------------
+//
+// d_x[t] = base[t] + sum over the pairs of t of A_l^T g[p]: a pair's adapter is its own, so
+// nothing is shared but A in the caches, and the vector units do it: a wave takes a
+// token and 16 bytes of columns a lane, g comes in scalar registers.  Workgroups of an XCD
+// work on the same columns, so that its L2 holds them of all adapters.
+
+struct GatherArgs {
+    const float* g;            // [T*k][R]
+    const uint8_t* a;          // [L][R][C]
+    const int32_t* ids;
+    const uint8_t* base;       // or null
+    uint8_t* out;
+    int64_t T, C, slices, groups;
+    int32_t L, R, k;
+};
+
+constexpr int kXcds = 8, kGatherTokens = 4;            // tokens of a workgroup, one a wave
+
 template <int DT>
-__global__ __launch_bounds__(kThreads) void lora_outer_kernel(const float* z, const void* v, int64_t ldv, int64_t div, const float* scale,
-                                                              const int32_t* ids, float* d, int64_t w_l, int64_t w_r, int64_t w_c,
-                                                              int64_t L, int64_t R, int64_t C, int64_t pairs)
+__global__ __launch_bounds__(kThreads) void lora_gather_kernel(GatherArgs m)
 {
-    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < L * R * C; i += (int64_t)gridDim.x * kThreads) {
-        const int64_t l = i / (R * C), r = i / C % R, c = i % C;
-        float sum = 0.0f;
-        for (int64_t p = 0; p < pairs; ++p) {
-            if (ids[p] == l) sum = __builtin_fmaf(z[p * R + r], load1<DT>(v, p / div * ldv + c), sum);
+    constexpr int kCols = 16 / kSize<DT>;
+    const int lane = threadIdx.x & 63, wave = uniform((int32_t)(threadIdx.x >> 6));
+    const int64_t total = m.slices * m.groups, per = (total + kXcds - 1) / kXcds;
+    const int64_t item = blockIdx.x % kXcds * per + blockIdx.x / kXcds;
+    if (item >= total || blockIdx.x / kXcds >= per) return;
+    const int64_t slice = item / m.groups, t = (item - slice * m.groups) * kGatherTokens + wave;
+    const int64_t c = slice * 64 * kCols + lane * kCols;
+    if (t >= m.T || c >= m.C) return;
+    float acc[kCols] = {};
+    for (int j = 0; j < m.k; ++j) {
+        const int64_t p = t * m.k + j;
+        const int32_t l = uniform(m.ids[p]);
+        if (!adapter_ok(l, m.L)) continue;
+        const float* g = m.g + p * m.R;
+        const uint8_t* a = m.a + ((int64_t)l * m.R * m.C + c) * kSize<DT>;
+        for (int r = 0; r < m.R; r += 8) {
+            u32x4 row[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) row[e] = *reinterpret_cast<const u32x4*>(a + (r + e) * m.C * kSize<DT>);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float f = g[r + e];
+#pragma unroll
+                for (int i = 0; i < kCols; ++i) acc[i] = __builtin_fmaf(f, load1<DT>(&row[e], i), acc[i]);
+            }
         }
-        d[l * w_l + r * w_r + c * w_c] = scale ? scale[l] * sum : sum;
+    }
+    u32x4 base = {0u, 0u, 0u, 0u};
+    const int64_t o = (t * m.C + c) * kSize<DT>;
+    if (m.base) base = *reinterpret_cast<const u32x4*>(m.base + o);
+    add_and_store<DT>(m.out + o, 0, base, acc);
+}
+
+// ---- outer: d[l] = sum over its pairs of u[p] v[row of p]^T -----------------------------
+//
+// The pairs are sorted by adapter and cut into tiles of 32 of one adapter.  lora_pieces
+// writes the R-vectors of a tile in the order that the products take them, u^T in pieces
+// of 16 bits: [tile][piece][16*RT][32].  A workgroup takes `run` tiles in a row and 512 bytes
+// of columns; where the adapter changes it writes its sums: to the result if all the
+// adapter's tiles are its own, else to part 2c (the adapter began before run c) or
+// 2c + 1, and lora_reduce adds an adapter's parts in their order.
+
+constexpr int kTile = 32;
+
+struct OuterTables {
+    const int32_t* tiles;      // [L + 2] first tile of each adapter; the last entry is their number
+    const int32_t* sorted;
+    const int4* tdesc;         // per tile {adapter (L: none), first slot, pairs, 0}
+};
+
+struct PiecesArgs {
+    const float* part;         // [splits][pairs][R]
+    const float* scale;        // [L] or null
+    float* sum;                // [pairs][R] or null: the sum of the parts
+    void* u;                   // [tiles][kPieces][16*RT][32]
+    float* back;               // [tiles]: 2^e of a tile's pieces (fp16)
+    int64_t pairs, max_tiles;
+    int32_t L, R, splits;
+};
+
+// One workgroup per tile (of either set of vectors): thread h has pair h%32 and every eighth group of four ranks from h/32 on.
+template <int DT, int RT>
+__global__ __launch_bounds__(kThreads) void lora_pieces_kernel(OuterTables tab, PiecesArgs a0, PiecesArgs a1)
+{
+    constexpr int kQuads = 4 * RT, kMine = (kQuads + 7) / 8;
+    __shared__ float wave_lds[kThreads / 64];
+    const bool second = (int64_t)blockIdx.x >= a0.max_tiles;
+    const PiecesArgs m = second ? a1 : a0;
+    const int64_t t = second ? blockIdx.x - a0.max_tiles : blockIdx.x;
+    if (t >= tab.tiles[m.L + 1]) return;
+    const int4 d = tab.tdesc[t];
+    const int s = threadIdx.x % kTile, q0 = threadIdx.x / kTile;
+    const bool have = s < d.z;
+    const int64_t p = have ? tab.sorted[d.y + s] : 0;
+    const bool none = d.x >= m.L;
+    const float scale = !none && m.scale ? m.scale[d.x] : 1.0f;
+    f32x4 z[kMine] = {};
+    float size = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+        const int r = (q0 + 8 * i) * 4;
+        if (have && r < m.R) {
+            if (!none) {
+                for (int k = 0; k < m.splits; ++k) z[i] += *reinterpret_cast<const f32x4*>(m.part + (k * m.pairs + p) * m.R + r);
+            }
+            z[i] *= scale;
+            if (m.sum) *reinterpret_cast<f32x4*>(m.sum + p * m.R + r) = z[i];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) size = fmaxf(size, __builtin_fabsf(z[i][e]));
+        }
+    }
+    if (none || !m.u) return;
+    if constexpr (DT == FTQ_F16) {
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) size = fmaxf(size, __shfl_xor(size, o));
+        if (threadIdx.x % 64 == 0) wave_lds[threadIdx.x / 64] = size;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kThreads / 64; ++w) size = fmaxf(size, wave_lds[w]);
+        const int e2 = middle_exponent(size);
+        const float f = __builtin_ldexpf(1.0f, -e2);
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) z[i] *= f;
+        if (threadIdx.x == 0) m.back[t] = __builtin_ldexpf(1.0f, e2);
+    }
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+        const int r = (q0 + 8 * i) * 4;
+        if (r >= 16 * RT) continue;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if constexpr (DT == FTQ_F32) {
+                static_cast<float*>(m.u)[(t * 16 * RT + r + e) * kTile + s] = z[i][e];
+            } else {
+                float v = z[i][e];
+#pragma unroll
+                for (int c = 0; c < kPieces<DT>; ++c) static_cast<uint16_t*>(m.u)[((t * kPieces<DT> + c) * 16 * RT + r + e) * kTile + s] = take_piece<DT>(v);
+            }
+        }
     }
 }
 
-constexpr int64_t kGrid = int64_t(1) << 20;
-int64_t grid_of(int64_t items) { return std::min((items + kThreads - 1) / kThreads, kGrid); }
+struct OuterArgs {
+    const uint8_t* u;          // as lora_pieces writes it
+    const float* back;
+    const uint8_t* v;          // rows
+    int64_t ldv;               // bytes
+    float* part;               // [2 * runs][16*RT * C] (or C * R, as the result)
+    float* d;                  // result: [L][R][C], or [L][C][R] with by_column
+    int64_t C, col_items, items;
+    int32_t div, L, R, by_column;
+    int32_t run;               // tiles of a workgroup
+};
 
-template <int DT, int OT>
-int forward(const LoraArgs& m, float* z, hipStream_t s)
+constexpr int kOuterDepth = 3, kBatch = 32;           // tiles in LDS, tiles listed there
+
+template <int DT, int RT>
+__global__ __launch_bounds__(kThreads) void lora_outer_kernel(OuterTables tab, OuterArgs a0, OuterArgs a1)
 {
-    const int64_t pairs = m.T * m.top_k;
-    int st = launch("lora_shrink_kernel", lora_shrink_kernel<DT>, std::min((pairs + 3) / 4, kGrid), kThreads, 0, s, m.x, m.ldx, m.act_div,
-                    m.a, m.R * m.K, m.K, int64_t(1), (const float*)nullptr, m.ids, z, m.L, m.R, m.K, pairs);
-    if (st != FTQ_OK) return st;
-    return launch("lora_expand_kernel", lora_expand_kernel<DT, OT>, grid_of(pairs * m.N), kThreads, 0, s, (const float*)z, m.b, m.N * m.R,
-                  int64_t(1), m.R, m.scale, m.ids, m.base, m.ld_base, m.out, m.ld_out, m.L, m.R, m.N, pairs, int64_t(1));
+    constexpr int kCols = 512 / kSize<DT>, kTiles = kCols / 64;    // columns of a workgroup, 16-column tiles of a wave
+    constexpr int kULine = kTile * kSize<DT>;                      // bytes of a rank's row of u
+    constexpr int kUBytes = kPieces<DT> * 16 * RT * kULine;        // of a tile, whole copies of 1024
+    constexpr int kU = kUBytes / 1024, kUShare = (kU + 3) / 4, kPer = 4 + kUShare;
+    static_assert(kUBytes % 1024 == 0);
+    __shared__ __attribute__((aligned(16))) uint8_t vs[kOuterDepth][kTile][512];
+    __shared__ __attribute__((aligned(16))) uint8_t us[kOuterDepth][kUBytes];
+    __shared__ int32_t row_lds[kBatch * kTile], id_lds[kBatch + 1];
+    __shared__ float back_lds[kBatch];
+    const bool second = (int64_t)blockIdx.x >= a0.items;
+    const OuterArgs m = second ? a1 : a0;
+    const int64_t item = second ? blockIdx.x - a0.items : blockIdx.x;
+    const int lane = threadIdx.x & 63, wave = uniform((int32_t)(threadIdx.x >> 6));
+    const int r16 = lane & 15, q = lane >> 4;
+    const int64_t chunk = item / m.col_items, col0 = (item - chunk * m.col_items) * kCols;
+    const int64_t t0 = chunk * m.run, t1 = min(t0 + m.run, (int64_t)uniform(tab.tiles[m.L]));   // (the pairs without adapter are last)
+    if (t0 >= t1) return;
+    // copies: instruction i of a wave brings rows 2*(4*i + wave), +1; a lane's position in its row holds another run (below)
+    const int cr = lane >> 5, pos = lane & 31;
+    const uint8_t* none = reinterpret_cast<const uint8_t*>(&kZeros);
+    const auto swizzle = [](int row) { return ((row & 3) | ((row >> 1) & 4)) << 1; };
+    f32x4 acc[kTiles][RT] = {};
+    // a batch of tiles at a time: its rows are listed in LDS, since a load in the loop below would wait for the copies too
+    for (int64_t b0 = t0; b0 < t1; b0 += kBatch) {
+    const int count = (int)min((int64_t)kBatch, t1 - b0);
+    block_barrier();                                               // the last batch's lists have been read
+    for (int i = threadIdx.x; i < count * kTile; i += kThreads) {
+        const int4 d = tab.tdesc[b0 + i / kTile];
+        const int s = i % kTile;
+        row_lds[i] = s < d.z ? tab.sorted[d.y + s] / m.div : -1;
+        if (s == 0) {
+            id_lds[i / kTile] = d.x;
+            if constexpr (DT == FTQ_F16) back_lds[i / kTile] = m.back[b0 + i / kTile];
+        }
+    }
+    if (threadIdx.x == 0) id_lds[count] = b0 + count < t1 ? tab.tdesc[b0 + count].x : -1;
+    block_barrier();
+    const auto copy_tile = [&](int i0) {
+        const int buf = i0 % kOuterDepth;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int at = 2 * (4 * i + wave) + cr;
+            const int32_t row = row_lds[i0 * kTile + at];
+            const int64_t c = col0 + (pos ^ swizzle(at)) * (16 / kSize<DT>);
+            copy16(lds_address(&vs[buf][2 * (4 * i + wave)][0]), row >= 0 && c < m.C ? m.v + (int64_t)row * m.ldv + c * kSize<DT> : none);
+        }
+#pragma unroll
+        for (int i = 0; i < kUShare; ++i) {
+            const int part = (wave + 4 * i) % kU;
+            copy16(lds_address(&us[buf][part * 1024]), m.u + (b0 + i0) * kUBytes + part * 1024 + lane * 16);
+        }
+    };
+    for (int i0 = 0; i0 < count && i0 < kOuterDepth - 1; ++i0) copy_tile(i0);
+    for (int i0 = 0; i0 < count; ++i0) {
+        const int buf = i0 % kOuterDepth;
+        if (count - 1 - i0 >= 1) wait_copies_but<kPer>();
+        else wait_copies();
+        block_barrier();                                           // all waves' copies of the tile are there, the last one has been read
+        const int32_t l = uniform(id_lds[i0]), after = uniform(id_lds[i0 + 1]);
+        const float f = DT == FTQ_F16 ? back_lds[i0] : 1.0f;
+        if (i0 + kOuterDepth - 1 < count) copy_tile(i0 + kOuterDepth - 1);
+        if constexpr (DT == FTQ_F32) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                float x[kTiles];
+#pragma unroll
+                for (int i = 0; i < kTiles; ++i) {
+                    const int row = 4 * k + q, c = wave * (kCols / 4) + 16 * i + r16;
+                    x[i] = *reinterpret_cast<const float*>(&vs[buf][row][((c >> 2) ^ swizzle(row)) * 16 + (c & 3) * 4]);
+                }
+#pragma unroll
+                for (int j = 0; j < RT; ++j) {
+                    const float u = *reinterpret_cast<const float*>(&us[buf][(16 * j + r16) * kULine + (4 * k + q) * 4]);
+#pragma unroll
+                    for (int i = 0; i < kTiles; ++i) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(x[i], u, acc[i][j], 0, 0, 0);
+                }
+            }
+        } else {
+            // columns as the left operand: a transposing read gives a lane four rows of its column
+            u32x4 x[kTiles];
+#pragma unroll
+            for (int i = 0; i < kTiles; ++i) {
+                u32x2 half[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int row = 8 * q + 4 * h + (r16 >> 2), c = wave * (kCols / 4) + 16 * i + (r16 & 3) * 4;
+                    const uint8_t* src = &vs[buf][row][((c >> 3) ^ swizzle(row)) * 16 + (c & 7) * 2];
+                    half[h] = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) i16x4*)src));
+                }
+                x[i] = u32x4{half[0][0], half[0][1], half[1][0], half[1][1]};
+            }
+#pragma unroll
+            for (int j = 0; j < RT; ++j) {
+                f32x4 p[kTiles];
+#pragma unroll
+                for (int i = 0; i < kTiles; ++i) p[i] = DT == FTQ_F16 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : acc[i][j];
+#pragma unroll
+                for (int c = 0; c < kPieces<DT>; ++c) {
+                    const u32x4 u = *reinterpret_cast<const u32x4*>(&us[buf][((c * RT + j) * 16 + r16) * kULine + q * 16]);
+#pragma unroll
+                    for (int i = 0; i < kTiles; ++i) p[i] = multiply<DT>(x[i], u, p[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < kTiles; ++i) {
+                    if constexpr (DT == FTQ_F16) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(p[i][e], f, acc[i][j][e]);
+                    } else {
+                        acc[i][j] = p[i];
+                    }
+                }
+            }
+        }
+        if (after == l) continue;
+        // the adapter's last tile here: its sums
+        const int64_t f0 = uniform(tab.tiles[l]), f1 = uniform(tab.tiles[l + 1]);
+        float* to = m.d + (int64_t)l * m.R * m.C;
+        if (f0 < t0 || f1 > t1) to = m.part + (2 * chunk + (f0 < t0 ? 0 : 1)) * m.R * m.C;
+#pragma unroll
+        for (int i = 0; i < kTiles; ++i) {
+            const int64_t c = col0 + wave * (kCols / 4) + 16 * i + 4 * q;   // this lane's four columns
+#pragma unroll
+            for (int j = 0; j < RT; ++j) {
+                const int r = 16 * j + r16;
+                if (c < m.C && r < m.R) {
+                    if (m.by_column) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) to[(c + e) * m.R + r] = acc[i][j][e];
+                    } else {
+                        *reinterpret_cast<f32x4*>(to + r * m.C + c) = acc[i][j];
+                    }
+                }
+                acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            }
+        }
+    }
+    }
 }
+
+// Adapters whose tiles lie in several runs: their parts added up; adapters without a pair: zeros.
+struct ReduceArgs {
+    const float* part;
+    float* d;
+    int64_t size;              // R * C
+    int32_t L, run;
+    int64_t blocks;            // workgroups of an adapter
+};
+
+__global__ __launch_bounds__(kThreads) void lora_reduce_kernel(const int32_t* tiles, ReduceArgs a0, ReduceArgs a1)
+{
+    const bool second = (int64_t)blockIdx.x >= a0.blocks * a0.L;
+    const ReduceArgs m = second ? a1 : a0;
+    const int64_t item = second ? blockIdx.x - a0.blocks * a0.L : blockIdx.x;
+    const int64_t l = item / m.blocks, i0 = (item - l * m.blocks) * kThreads + threadIdx.x;
+    const int64_t t0 = tiles ? tiles[l] : 0, t1 = tiles ? tiles[l + 1] : 0;
+    const int64_t c0 = t0 / m.run, c1 = t1 > t0 ? (t1 - 1) / m.run : c0;
+    if (t1 > t0 && c0 == c1) return;
+    for (int64_t i = i0; i < m.size / 4; i += m.blocks * kThreads) {
+        f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (t1 > t0) {
+            sum = *reinterpret_cast<const f32x4*>(m.part + (2 * c0 + 1) * m.size + 4 * i);
+            for (int64_t c = c0 + 1; c <= c1; ++c) sum += *reinterpret_cast<const f32x4*>(m.part + 2 * c * m.size + 4 * i);
+        }
+        *reinterpret_cast<f32x4*>(m.d + l * m.size + 4 * i) = sum;
+    }
+}
+
+// ---- transposed copies of the weights of adapters that have pairs ---------------------
+//
+// w [L][rows][cols] -> [L][cols][rows]; tiles of 64 x 64 through LDS.
+
+struct TransposeArgs {
+    const uint8_t* w;
+    uint8_t* to;
+    int64_t rows, cols, items, per;   // per: workgroups of an adapter
+};
 
 template <int DT>
-int backward(const LoraBackwardArgs& m, float* g, hipStream_t s)
+__global__ __launch_bounds__(kThreads) void lora_transpose_kernel(const int32_t* tiles, TransposeArgs a0, TransposeArgs a1)
 {
-    const int64_t pairs = m.T * m.top_k, rows = pairs / m.act_div;
-    int st = FTQ_OK;
-    if (pairs > 0 && (m.d_x || m.d_a)) {
-        st = launch("lora_shrink_kernel", lora_shrink_kernel<DT>, std::min((pairs + 3) / 4, kGrid), kThreads, 0, s, m.d_out, m.ld_d, int64_t(1),
-                    m.b, m.N * m.R, int64_t(1), m.R, m.scale, m.ids, g, m.L, m.R, m.N, pairs);
-        if (st != FTQ_OK) return st;
+    using Elem = std::conditional_t<DT == FTQ_F32, uint32_t, uint16_t>;
+    __shared__ Elem lds[64][65];
+    const bool second = (int64_t)blockIdx.x >= a0.items;
+    const TransposeArgs m = second ? a1 : a0;
+    const int64_t item = second ? blockIdx.x - a0.items : blockIdx.x, l = item / m.per;
+    if (tiles[l] == tiles[l + 1]) return;
+    const int64_t ct = (m.cols + 63) / 64, tile = item - l * m.per, r0 = tile / ct * 64, c0 = tile % ct * 64;
+    const Elem* w = reinterpret_cast<const Elem*>(m.w) + l * m.rows * m.cols;
+    Elem* to = reinterpret_cast<Elem*>(m.to) + l * m.rows * m.cols;
+    const int x = threadIdx.x % 64;
+    for (int y = threadIdx.x / 64; y < 64; y += kThreads / 64) {
+        if (r0 + y < m.rows && c0 + x < m.cols) lds[y][x] = w[(r0 + y) * m.cols + c0 + x];
     }
-    if (pairs > 0 && m.d_x) {
-        st = launch("lora_expand_kernel", lora_expand_kernel<DT, DT>, grid_of(rows * m.K), kThreads, 0, s, (const float*)g, m.a, m.R * m.K, m.K,
-                    int64_t(1), (const float*)nullptr, m.ids, m.base, m.K, m.d_x, m.K, m.L, m.R, m.K, rows, m.act_div);
-        if (st != FTQ_OK) return st;
+    __syncthreads();
+    for (int y = threadIdx.x / 64; y < 64; y += kThreads / 64) {
+        if (c0 + y < m.cols && r0 + x < m.rows) to[(c0 + y) * m.rows + r0 + x] = lds[x][y];
     }
-    if (m.d_a) {
-        st = launch("lora_outer_kernel", lora_outer_kernel<DT>, grid_of(m.L * m.R * m.K), kThreads, 0, s, (const float*)g, m.x, m.ldx, m.act_div,
-                    (const float*)nullptr, m.ids, m.d_a, m.R * m.K, m.K, int64_t(1), m.L, m.R, m.K, pairs);
-        if (st != FTQ_OK) return st;
+}
+
+// ---- host ---------------------------------------------------------------------------
+
+int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t size_of(int dtype) { return dtype == FTQ_F32 ? 4 : 2; }
+int rank_tiles(int64_t R) { return R <= 16 ? 1 : R <= 32 ? 2 : R <= 64 ? 4 : 8; }
+
+// Parts that a row's length is split into: by the sizes alone, so that a pair's bits do not go by the path.
+int64_t shrink_splits(int64_t pairs, int64_t C, int64_t R, int dtype)
+{
+    const int64_t steps = ceil_div(C * size_of(dtype), kLine), tiles = ceil_div(pairs, 64);
+    const int64_t want = tiles <= 16 ? 16 : std::max<int64_t>(1, 512 / tiles / std::max<int64_t>(1, R / 32));
+    return std::max<int64_t>(1, std::min({want, int64_t(16), steps / 2}));
+}
+
+// 16 rows a tile, or 64: few pairs, or few of an adapter side by side.
+bool small_tiles(int64_t pairs, int64_t L, bool sorted) { return pairs <= 256 || (sorted && pairs / L < 32); }
+
+// Calls f(type constant).
+template <typename F>
+int by_type(int dtype, F f)
+{
+    if (dtype == FTQ_F32) return f(std::integral_constant<int, FTQ_F32>{});
+    if (dtype == FTQ_F16) return f(std::integral_constant<int, FTQ_F16>{});
+    return f(std::integral_constant<int, FTQ_BF16>{});
+}
+
+template <int DT, int WAVES>
+int launch_shrink(const ShrinkArgs& m, int64_t grid, hipStream_t s)
+{
+    const auto go = [&](auto* kernel) { return launch("lora_shrink_kernel", kernel, grid, 64 * WAVES, 0, s, m); };
+    switch (rank_tiles(m.R)) {
+        case 1: return go(lora_shrink_kernel<DT, WAVES, 1>);
+        case 2: return go(lora_shrink_kernel<DT, WAVES, 2>);
+        case 4: return go(lora_shrink_kernel<DT, WAVES, 4>);
+        default: return go(lora_shrink_kernel<DT, WAVES, 8>);
     }
-    if (!m.d_b) return FTQ_OK;
-    return launch("lora_outer_kernel", lora_outer_kernel<DT>, grid_of(m.L * m.R * m.N), kThreads, 0, s, m.h, m.d_out, m.ld_d, int64_t(1),
-                  m.scale, m.ids, m.d_b, m.N * m.R, int64_t(1), m.R, m.L, m.R, m.N, pairs);
+}
+
+int run_shrink(int dtype, ShrinkArgs m, hipStream_t s)
+{
+    const bool small = small_tiles(m.pairs, m.L, m.sorted != nullptr);
+    const int64_t tiles = ceil_div(m.pairs, small ? 16 : 64);
+    m.groups = m.pairs <= 256 ? (int32_t)std::min<int64_t>(16, m.L) : 1;
+    m.steps = (int32_t)ceil_div(ceil_div(m.row_bytes, kLine), m.splits);
+    return by_type(dtype, [&](auto dt) {
+        constexpr int DT = decltype(dt)::value;
+        const int64_t grid = tiles * m.groups * m.splits;
+        return small ? launch_shrink<DT, 1>(m, grid, s) : launch_shrink<DT, 4>(m, grid, s);
+    });
+}
+
+template <int DT, int OT, int BT>
+int launch_expand(const ExpandArgs& m, int64_t grid, hipStream_t s)
+{
+    const auto go = [&](auto* kernel) { return launch("lora_expand_kernel", kernel, grid, kThreads, 0, s, m); };
+    const int rt = rank_tiles(m.R);
+    if constexpr (DT == FTQ_F32) {
+        if (rt == 1) return go(lora_expand_kernel<DT, OT, BT, 1>);
+        if (rt == 2) return go(lora_expand_kernel<DT, OT, BT, 2>);
+        if (rt == 4) return go(lora_expand_kernel<DT, OT, BT, 4>);
+        return go(lora_expand_kernel<DT, OT, BT, 8>);
+    } else {
+        if (rt <= 2) return go(lora_expand_kernel<DT, OT, BT, 1>);
+        if (rt == 4) return go(lora_expand_kernel<DT, OT, BT, 2>);
+        return go(lora_expand_kernel<DT, OT, BT, 4>);
+    }
+}
+
+int run_expand(int dtype, int out_dtype, ExpandArgs m, hipStream_t s)
+{
+    const bool small = small_tiles(m.pairs, m.L, m.sorted != nullptr);
+    const int64_t tiles = ceil_div(m.pairs, small ? 16 : 64);
+    m.groups = m.pairs <= 256 ? (int32_t)std::min<int64_t>(16, m.L) : 1;
+    const int64_t chunks = ceil_div(m.C, 256), per = std::max<int64_t>(1, std::min(chunks, tiles * m.groups * chunks / 1024));
+    m.cols = (int32_t)(per * 256);
+    m.col_items = ceil_div(m.C, m.cols);
+    const int64_t grid = tiles * m.groups * m.col_items;
+    return by_type(dtype, [&](auto dt) {
+        return by_type(out_dtype, [&](auto ot) {
+            constexpr int DT = decltype(dt)::value, OT = decltype(ot)::value;
+            return small ? launch_expand<DT, OT, 1>(m, grid, s) : launch_expand<DT, OT, 4>(m, grid, s);
+        });
+    });
+}
+
+struct ForwardPlan {
+    BucketPlan bucket;
+    int64_t splits, off_part, bytes;
+};
+
+ForwardPlan plan_forward(int64_t L, int64_t R, int64_t K, int64_t pairs, int dtype, int path)
+{
+    ForwardPlan p;
+    if (path == FTQ_PATH_GROUPED) p.bucket = make_bucket_plan(pairs, L, 0);
+    p.splits = shrink_splits(pairs, K, R, dtype);
+    p.off_part = p.bucket.bytes;
+    p.bytes = p.off_part + align256(p.splits * pairs * R * 4);
+    return p;
+}
+
+struct BackwardPlan {
+    BucketPlan bucket;
+    bool gather;               // d_x row by row (rows that several pairs share)
+    int64_t splits, run, runs_max;
+    int64_t off_part, off_g, off_ug, off_uh, off_backs, off_bt, off_at, off_pa, off_pb, bytes;
+};
+
+BackwardPlan plan_backward(int64_t L, int64_t R, int64_t K, int64_t N, int64_t pairs, int64_t div, int dtype)
+{
+    BackwardPlan p;
+    const int64_t es = size_of(dtype), rt = 16 * rank_tiles(R), pieces = dtype == FTQ_F32 ? 2 : dtype == FTQ_F16 ? 2 : 3;
+    p.bucket = make_bucket_plan(pairs, L, kTile);
+    p.gather = div > 1;
+    p.splits = shrink_splits(pairs, N, R, dtype);
+    // runs of tiles for about 512 workgroups an output, at most a part for every four tiles
+    const int64_t col_items = ceil_div(std::min(K, N) * es, 512), tiles = std::max<int64_t>(p.bucket.max_tiles, 1);
+    p.run = std::max<int64_t>(4, ceil_div(tiles * col_items, 512));
+    p.runs_max = ceil_div(tiles, p.run);
+    int64_t off = p.bucket.bytes;
+    const auto take = [&](int64_t bytes) {
+        const int64_t at = off;
+        off += align256(bytes);
+        return at;
+    };
+    p.off_part = take(p.splits * pairs * R * 4);
+    p.off_g = take(pairs * R * 4);
+    p.off_ug = take(tiles * rt * kTile * 2 * pieces);
+    p.off_uh = take(tiles * rt * kTile * 2 * pieces);
+    p.off_backs = take(2 * tiles * 4);
+    p.off_bt = take(L * R * N * es);
+    p.off_at = take(p.gather ? 0 : L * R * K * es);
+    p.off_pa = take(2 * p.runs_max * R * K * 4);
+    p.off_pb = take(2 * p.runs_max * R * N * 4);
+    p.bytes = off;
+    return p;
+}
+
+int launch_pieces(int dtype, int rt, const OuterTables& tab, const PiecesArgs& a, const PiecesArgs& b, hipStream_t s)
+{
+    return by_type(dtype, [&](auto dt) {
+        constexpr int DT = decltype(dt)::value;
+        const auto go = [&](auto* kernel) { return launch("lora_pieces_kernel", kernel, a.max_tiles + b.max_tiles, kThreads, 0, s, tab, a, b); };
+        if (rt == 1) return go(lora_pieces_kernel<DT, 1>);
+        if (rt == 2) return go(lora_pieces_kernel<DT, 2>);
+        if (rt == 4) return go(lora_pieces_kernel<DT, 4>);
+        return go(lora_pieces_kernel<DT, 8>);
+    });
+}
+
+int launch_outer(int dtype, int rt, const OuterTables& tab, const OuterArgs& a, const OuterArgs& b, hipStream_t s)
+{
+    return by_type(dtype, [&](auto dt) {
+        constexpr int DT = decltype(dt)::value;
+        const auto go = [&](auto* kernel) { return launch("lora_outer_kernel", kernel, a.items + b.items, kThreads, 0, s, tab, a, b); };
+        if (rt == 1) return go(lora_outer_kernel<DT, 1>);
+        if (rt == 2) return go(lora_outer_kernel<DT, 2>);
+        if (rt == 4) return go(lora_outer_kernel<DT, 4>);
+        return go(lora_outer_kernel<DT, 8>);
+    });
 }
 
 }  // namespace
 
-int64_t lora_workspace(int64_t, int64_t R, int64_t, int64_t, int64_t T, int64_t top_k, int, int) { return (T * top_k * R * 4 + 255) / 256 * 256; }
-int64_t lora_backward_workspace(int64_t, int64_t R, int64_t, int64_t, int64_t T, int64_t top_k, int) { return (T * top_k * R * 4 + 255) / 256 * 256; }
-int lora_select_path(int64_t, int64_t) { return FTQ_PATH_GEMV; }
-
-int run_lora(const LoraArgs& m, void* ws, int, hipStream_t s)
+int64_t lora_workspace(int64_t L, int64_t R, int64_t K, int64_t, int64_t T, int64_t top_k, int dtype, int path)
 {
-    float* z = m.h ? m.h : static_cast<float*>(ws);
-    const auto by_out = [&](auto dt) {
-        constexpr int DT = decltype(dt)::value;
-        if (m.out_dtype == FTQ_F32) return forward<DT, FTQ_F32>(m, z, s);
-        if (m.out_dtype == FTQ_F16) return forward<DT, FTQ_F16>(m, z, s);
-        return forward<DT, FTQ_BF16>(m, z, s);
-    };
-    if (m.dtype == FTQ_F32) return by_out(std::integral_constant<int, FTQ_F32>{});
-    if (m.dtype == FTQ_F16) return by_out(std::integral_constant<int, FTQ_F16>{});
-    return by_out(std::integral_constant<int, FTQ_BF16>{});
+    return plan_forward(L, R, K, T * top_k, dtype, path).bytes;
+}
+
+int64_t lora_backward_workspace(int64_t L, int64_t R, int64_t K, int64_t N, int64_t T, int64_t top_k, int dtype)
+{
+    // either layout of the rows: the larger of the two
+    return T == 0 ? 0 : plan_backward(L, R, K, N, T * top_k, 1, dtype).bytes;
+}
+
+int lora_select_path(int64_t T, int64_t top_k) { return top_k == 1 || T * top_k <= 256 ? FTQ_PATH_GEMV : FTQ_PATH_GROUPED; }
+
+int run_lora(const LoraArgs& m, void* ws, int path, hipStream_t s)
+{
+    const int64_t pairs = m.T * m.top_k;
+    uint8_t* mem = static_cast<uint8_t*>(ws);
+    const ForwardPlan plan = plan_forward(m.L, m.R, m.K, pairs, m.dtype, path);
+    const int32_t* sorted = nullptr;
+    if (path == FTQ_PATH_GROUPED) {
+        const int st = run_bucket(m.ids, m.L, plan.bucket, ws, s);
+        if (st != FTQ_OK) return st;
+        sorted = reinterpret_cast<const int32_t*>(mem + plan.bucket.off_sorted);
+    }
+    ShrinkArgs shrink{};
+    shrink.v = static_cast<const uint8_t*>(m.x);
+    shrink.ldv = m.ldx * size_of(m.dtype);
+    shrink.w = static_cast<const uint8_t*>(m.a);
+    shrink.ids = m.ids;
+    shrink.sorted = sorted;
+    shrink.part = reinterpret_cast<float*>(mem + plan.off_part);
+    shrink.pairs = pairs;
+    shrink.row_bytes = m.K * size_of(m.dtype);
+    shrink.div = (int32_t)m.act_div;
+    shrink.L = (int32_t)m.L;
+    shrink.R = (int32_t)m.R;
+    shrink.splits = (int32_t)plan.splits;
+    const int st = run_shrink(m.dtype, shrink, s);
+    if (st != FTQ_OK) return st;
+    ExpandArgs expand{};
+    expand.part = shrink.part;
+    expand.w = static_cast<const uint8_t*>(m.b);
+    expand.scale = m.scale;
+    expand.ids = m.ids;
+    expand.sorted = sorted;
+    expand.base = m.base;
+    expand.out = m.out;
+    expand.h = m.h;
+    expand.ld_base = m.ld_base;
+    expand.ld_out = m.ld_out;
+    expand.pairs = pairs;
+    expand.C = m.N;
+    expand.L = shrink.L;
+    expand.R = shrink.R;
+    expand.splits = shrink.splits;
+    return run_expand(m.dtype, m.out_dtype, expand, s);
 }
 
 int run_lora_backward(const LoraBackwardArgs& m, void* ws, hipStream_t s)
 {
-    float* g = static_cast<float*>(ws);
-    if (m.dtype == FTQ_F32) return backward<FTQ_F32>(m, g, s);
-    if (m.dtype == FTQ_F16) return backward<FTQ_F16>(m, g, s);
-    return backward<FTQ_BF16>(m, g, s);
+    const int64_t pairs = m.T * m.top_k, es = size_of(m.dtype);
+    const int rt = rank_tiles(m.R);
+    const auto reduce = [&](const int32_t* tiles, int64_t run, const float* pa, const float* pb) {
+        const auto args = [&](float* d, int64_t C, const float* part) {
+            return ReduceArgs{part, d, m.R * C, d ? (int32_t)m.L : 0, (int32_t)run, std::min<int64_t>(ceil_div(m.R * C / 4, kThreads), 64)};
+        };
+        const ReduceArgs a = args(m.d_a, m.K, pa), b = args(m.d_b, m.N, pb);
+        return launch("lora_reduce_kernel", lora_reduce_kernel, a.blocks * a.L + b.blocks * b.L, kThreads, 0, s, tiles, a, b);
+    };
+    if (pairs == 0) return reduce(nullptr, 1, nullptr, nullptr);
+    uint8_t* mem = static_cast<uint8_t*>(ws);
+    const BackwardPlan plan = plan_backward(m.L, m.R, m.K, m.N, pairs, m.act_div, m.dtype);
+    int st = run_bucket(m.ids, m.L, plan.bucket, ws, s);
+    if (st != FTQ_OK) return st;
+    const OuterTables tab{reinterpret_cast<const int32_t*>(mem + plan.bucket.off_tiles), reinterpret_cast<const int32_t*>(mem + plan.bucket.off_sorted),
+                          reinterpret_cast<const int4*>(mem + plan.bucket.off_tdesc)};
+    const auto floats = [&](int64_t off) { return reinterpret_cast<float*>(mem + off); };
+    const bool want_g = m.d_x || m.d_a, expand_x = m.d_x && !plan.gather;
+    if (want_g) {
+        const auto args = [&](const void* w, int64_t off, int64_t rows, int64_t cols, bool wanted) {
+            const int64_t per = ceil_div(rows, 64) * ceil_div(cols, 64);
+            return TransposeArgs{static_cast<const uint8_t*>(w), mem + off, rows, cols, wanted ? m.L * per : 0, per};
+        };
+        const TransposeArgs b = args(m.b, plan.off_bt, m.N, m.R, true), a = args(m.a, plan.off_at, m.R, m.K, expand_x);
+        st = by_type(m.dtype, [&](auto dt) {
+            return launch("lora_transpose_kernel", lora_transpose_kernel<decltype(dt)::value>, b.items + a.items, kThreads, 0, s, tab.tiles, b, a);
+        });
+        if (st != FTQ_OK) return st;
+        ShrinkArgs shrink{};
+        shrink.v = static_cast<const uint8_t*>(m.d_out);
+        shrink.ldv = m.ld_d * es;
+        shrink.w = mem + plan.off_bt;
+        shrink.ids = m.ids;
+        shrink.sorted = tab.sorted;
+        shrink.part = floats(plan.off_part);
+        shrink.pairs = pairs;
+        shrink.row_bytes = m.N * es;
+        shrink.div = 1;
+        shrink.L = (int32_t)m.L;
+        shrink.R = (int32_t)m.R;
+        shrink.splits = (int32_t)plan.splits;
+        st = run_shrink(m.dtype, shrink, s);
+        if (st != FTQ_OK) return st;
+    }
+    // the R-vectors of the outer products, and g itself
+    const int64_t tiles = plan.bucket.max_tiles;
+    const PiecesArgs pg{floats(plan.off_part), m.scale, m.d_x ? floats(plan.off_g) : nullptr, m.d_a ? mem + plan.off_ug : nullptr, floats(plan.off_backs),
+                        pairs, want_g ? tiles : 0, (int32_t)m.L, (int32_t)m.R, (int32_t)plan.splits};
+    const PiecesArgs ph{m.h, m.scale, nullptr, mem + plan.off_uh, floats(plan.off_backs) + tiles, pairs, m.d_b ? tiles : 0, (int32_t)m.L,
+                        (int32_t)m.R, 1};
+    st = launch_pieces(m.dtype, rt, tab, pg, ph, s);
+    if (st != FTQ_OK) return st;
+    if (expand_x) {
+        ExpandArgs expand{};
+        expand.part = floats(plan.off_g);
+        expand.w = mem + plan.off_at;
+        expand.ids = m.ids;
+        expand.sorted = tab.sorted;
+        expand.base = m.base;
+        expand.out = m.d_x;
+        expand.ld_base = expand.ld_out = expand.C = m.K;
+        expand.pairs = pairs;
+        expand.L = (int32_t)m.L;
+        expand.R = (int32_t)m.R;
+        expand.splits = 1;
+        st = run_expand(m.dtype, m.dtype, expand, s);
+        if (st != FTQ_OK) return st;
+    } else if (m.d_x) {
+        GatherArgs gather{floats(plan.off_g), static_cast<const uint8_t*>(m.a), m.ids, static_cast<const uint8_t*>(m.base), static_cast<uint8_t*>(m.d_x),
+                          m.T, m.K, ceil_div(m.K * es, 1024), ceil_div(m.T, kGatherTokens), (int32_t)m.L, (int32_t)m.R, (int32_t)m.top_k};
+        const int64_t grid = ceil_div(gather.slices * gather.groups, kXcds) * kXcds;
+        st = by_type(m.dtype, [&](auto dt) { return launch("lora_gather_kernel", lora_gather_kernel<decltype(dt)::value>, grid, kThreads, 0, s, gather); });
+        if (st != FTQ_OK) return st;
+    }
+    if (!m.d_a && !m.d_b) return FTQ_OK;
+    const auto outer = [&](int64_t off_u, int64_t backs, const void* v, int64_t ldv, int64_t off_part, float* d, int64_t C, int64_t div, bool by_column) {
+        const int64_t col_items = ceil_div(C * es, 512);
+        return OuterArgs{mem + off_u, floats(plan.off_backs) + backs, static_cast<const uint8_t*>(v), ldv * es, floats(off_part), d, C, col_items,
+                         d ? plan.runs_max * col_items : 0, (int32_t)div, (int32_t)m.L, (int32_t)m.R, by_column, (int32_t)plan.run};
+    };
+    st = launch_outer(m.dtype, rt, tab, outer(plan.off_ug, 0, m.x, m.ldx, plan.off_pa, m.d_a, m.K, m.act_div, false),
+                      outer(plan.off_uh, tiles, m.d_out, m.ld_d, plan.off_pb, m.d_b, m.N, 1, true), s);
+    if (st != FTQ_OK) return st;
+    return reduce(tab.tiles, plan.run, floats(plan.off_pa), floats(plan.off_pb));
 }
 
 }  // namespace ftq

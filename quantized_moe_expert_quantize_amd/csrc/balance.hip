@@ -6,191 +6,277 @@
 //
 //   loss = E / (top_k n^2) * sum_e c_e * sum_t p_te.
 //
-// A row (token) is worked on by LPR lanes, each with runs of V consecutive experts,
-// so that a wave takes 64/LPR rows.  The loss goes in two kernels: one workgroup per
+// A row (token) is worked on by LPR lanes, each with 16 experts in runs of V, so that
+// a wave takes 64/LPR rows.  (64 lanes a row, with four experts each, were bound by the
+// latency of the reductions: 32768 rows of 256 experts, loss 28 us, gradient 68 us.)
+// The loss goes in two kernels: one workgroup per
 // chunk of rows sums the probabilities and counts of each sequence that has rows in
 // it, and one per sequence adds up its chunks, in a fixed order and without
 // floating-point atomics.  Part (chunk c, sequence s) lies at index c + s: along the
-// rows either c or s grows, so that no two parts meet.
+// rows either c or s grows, so that no two parts meet.  A small batch is one
+// chunk, whose workgroup writes the losses itself.
+#include <algorithm>
+#include <type_traits>
+
 #include "ftq_internal.h"
+#include "row_lanes.h"
 
 namespace ftq {
 namespace {
 
-constexpr int kThreads = 256, kWaves = kThreads / 64;
+constexpr int kThreads = 256, kAloneThreads = 1024;
+constexpr int kPerLane = 16;                          // experts of a lane
 constexpr float kInf = __builtin_inff();
 
-template <int V> struct RunF { float v[V]; } __attribute__((packed, aligned(4)));
-template <int V> struct RunH { uint16_t v[V]; } __attribute__((packed, aligned(2)));
+// The lanes of a row talk through LDS within one wave, whose LDS accesses the hardware
+// keeps in order; the fence keeps the compiler from reordering them.
+__device__ __forceinline__ void wave_lds_fence() { __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront"); }
 
-// e^x for x <= 0: the base-2 product's rounding is carried along.
-__device__ __forceinline__ float exp_neg(float x)
+// N consecutive elements at any element address (the hardware takes unaligned accesses).
+template <int N> struct RunF { float v[N]; } __attribute__((packed, aligned(4)));
+template <int N> struct alignas(4 * N) LineF { float v[N]; };
+template <int N> struct RunH { uint16_t v[N]; } __attribute__((packed, aligned(2)));
+
+template <int DT> __device__ __forceinline__ float load_logit(const void* logits, int64_t i)
 {
-    constexpr float kLog2e = 1.4426950408889634f, kRest = 1.9259629911266175e-8f, kLn2 = 0.6931471805599453f;
-    const float t = x * kLog2e;
-    const float r = __builtin_fmaf(x, kRest, __builtin_fmaf(x, kLog2e, -t));
-    const float e = __builtin_amdgcn_exp2f(t);
-    return e == 0.0f ? e : __builtin_fmaf(e, r * kLn2, e);   // (-inf: its r is a NaN)
+    if constexpr (DT == FTQ_F32) return static_cast<const float*>(logits)[i];
+    const uint16_t h = static_cast<const uint16_t*>(logits)[i];
+    return DT == FTQ_F16 ? f32_of_f16(h) : f32_of_bf16(h);
 }
 
 // Experts of a lane: run i is (i*LPR + sub)*V .. + V-1; past the last one -inf.
-template <bool WIDE, int LPR, int G, int V>
-__device__ __forceinline__ void load_row(const void* logits, int dtype, int64_t at, int sub, int E, float (&l)[G][V])
+template <int DT, int LPR, int V>
+__device__ __forceinline__ void load_row(const void* logits, int64_t at, int sub, int E, float (&l)[kPerLane])
 {
 #pragma unroll
-    for (int i = 0; i < G; ++i) {
+    for (int i = 0; i < kPerLane / V; ++i) {
         const int e = (i * LPR + sub) * V;
         if (e < E) {                                   // E % V == 0: the whole run
-            if constexpr (WIDE) {
+            if constexpr (DT == FTQ_F32) {
                 const RunF<V> r = *reinterpret_cast<const RunF<V>*>(static_cast<const float*>(logits) + at + e);
 #pragma unroll
-                for (int v = 0; v < V; ++v) l[i][v] = r.v[v];
+                for (int v = 0; v < V; ++v) l[i * V + v] = r.v[v];
             } else {
                 const RunH<V> r = *reinterpret_cast<const RunH<V>*>(static_cast<const uint16_t*>(logits) + at + e);
 #pragma unroll
-                for (int v = 0; v < V; ++v) l[i][v] = dtype == FTQ_F16 ? f32_of_f16(r.v[v]) : f32_of_bf16(r.v[v]);
+                for (int v = 0; v < V; ++v) l[i * V + v] = DT == FTQ_F16 ? f32_of_f16(r.v[v]) : f32_of_bf16(r.v[v]);
             }
         } else {
 #pragma unroll
-            for (int v = 0; v < V; ++v) l[i][v] = -kInf;
+            for (int v = 0; v < V; ++v) l[i * V + v] = -kInf;
         }
     }
 }
 
-template <int LPR> __device__ __forceinline__ float row_max(float x)
+// e^x for x <= 0: within |x| + 2 units of 2^-24 of its size (the rounding of the base-2 exponent), so that what is
+// far off in its own size is small beside the row's largest.  -inf gives 0, a NaN itself.
+__device__ __forceinline__ float exp_neg(float x) { return __builtin_amdgcn_exp2f(x * 1.4426950408889634f); }
+
+// 1/(1 + e^-l), and 1 minus it, from one exponential of -|l| and one reciprocal (the hardware's, 1 unit off at most).
+__device__ __forceinline__ float sigmoid(float l, float& rest)
 {
-#pragma unroll
-    for (int o = 1; o < LPR; o <<= 1) x = fmaxf(x, __shfl_xor(x, o));
-    return x;
-}
-template <int LPR> __device__ __forceinline__ float row_sum(float x)
-{
-#pragma unroll
-    for (int o = 1; o < LPR; o <<= 1) x += __shfl_xor(x, o);
-    return x;
+    const float e = exp_neg(-__builtin_fabsf(l)), r = __builtin_amdgcn_rcpf(1.0f + e), er = e * r;
+    rest = l < 0.0f ? r : er;
+    return l < 0.0f ? er : r;
 }
 
-// Scores up to a factor of the row's own, from the logit `top` (the row's largest, or the largest chosen one)
-// on: softmax e^(l - top); sigmoid 1/(1 + e^-l) = e^min(l,0) / (1 + e^-|l|), divided by e^min(top,0).  No
-// logit is too small for them; a NaN stays one, and a row without a finite logit has zeros.
-__device__ __forceinline__ float weight_of(float l, float top, bool softmax)
+constexpr float kLow = -60.0f;                        // sigmoids from here down are e^l
+__device__ __forceinline__ float finite_top(float top) { return top == -kInf ? 0.0f : top; }
+
+// Scores of a row up to a factor of its own, and their sum: softmax e^(l - top) with the
+// row's largest logit; sigmoids as they are, or e^(l - top) where all lie so low that their
+// sum would lose bits.  A NaN stays one; a row without a finite logit has zeros.
+template <bool SOFT, int LPR>
+__device__ __forceinline__ void row_scores(const float (&l)[kPerLane], float (&w)[kPerLane], float (&rest)[kPerLane], float& top, float& sum)
 {
-    if (softmax) {
-        const float d = l - (top == -kInf ? 0.0f : top);
-        return exp_neg(d);
+    const auto relative = [&] {
+        top = -kInf;
+#pragma unroll
+        for (int i = 0; i < kPerLane; ++i) top = fmaxf(top, l[i]);
+        top = finite_top(row_max<LPR>(top));
+        sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kPerLane; ++i) sum += w[i] = exp_neg(l[i] - top);
+        sum = row_sum<LPR>(sum);
+    };
+    if constexpr (SOFT) {
+        relative();
+    } else {
+        sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kPerLane; ++i) sum += w[i] = sigmoid(l[i], rest[i]);
+        sum = row_sum<LPR>(sum);
+        if (sum < 1e-26f) relative();                 // every logit is below kLow
     }
-    const float t = top < 0.0f && top != -kInf ? top : 0.0f;
-    return exp_neg((l < 0.0f ? l : 0.0f) - t) / (1.0f + exp_neg(-__builtin_fabsf(l)));
 }
 
-// The sequence [begin, end) of rows that s is, within the T rows there are.
-__device__ __forceinline__ void sequence(const int32_t* offsets, int64_t s, int64_t T, int64_t& begin, int64_t& end)
-{
-    begin = 0;
-    end = T;
-    if (offsets) {
-        begin = max((int64_t)offsets[s], (int64_t)0);
-        end = min((int64_t)offsets[s + 1], T);
+// The packed sequences around a wave's rows: lane i holds where sequence s0 + i begins
+// (S: the end of the last one), so that finding a row's takes no further loads.
+struct Sequences {
+    const int32_t* offsets;    // or null: one sequence of all T rows
+    int64_t S, T, s0;
+    int32_t at;
+
+    // The one that `row` lies in comes first, or the whole array if it fits: 64 probes a load.
+    __device__ __forceinline__ void find(const int32_t* offsets_, int64_t S_, int64_t T_, int64_t row, int lane)
+    {
+        offsets = offsets_;
+        S = S_;
+        T = T_;
+        s0 = 0;
+        at = 0;
+        if (!offsets) return;
+        int64_t n = S;
+        while (n > 63) {                              // those in [s0, s0 + n) that end after `row` are its last ones
+            const int64_t step = (n + 63) / 64, s = s0 + (lane + 1) * step - 1;
+            const int64_t before = __popcll(__ballot(s < s0 + n && offsets[min(s + 1, S)] <= row)) * step;
+            s0 += before;
+            n = min(step, n - before);
+            if (step == 1) break;
+        }
+        at = offsets[min(s0 + lane, S)];
     }
-}
-
-// The first sequence that ends after `row`, found by all threads of the workgroup (one barrier).
-__device__ __forceinline__ int64_t first_sequence(const int32_t* offsets, int64_t S, int64_t row, int32_t* lds)
-{
-    if (!offsets) return 0;
-    int before = 0;
-    for (int64_t s = threadIdx.x; s < S; s += kThreads) before += offsets[s + 1] <= row;
+    // The first sequence from s0 on that ends after `row` (S if none does), and its rows within the T there are.
+    __device__ __forceinline__ int64_t of(int64_t row, int64_t& begin, int64_t& end) const
+    {
+        begin = 0;
+        end = T;
+        if (!offsets) return 0;
+        int i = 0;                                    // entries 1 .. i of `at` are <= row
 #pragma unroll
-    for (int o = 1; o < 64; o <<= 1) before += __shfl_xor(before, o);
-    if (threadIdx.x % 64 == 0) lds[threadIdx.x / 64] = before;
-    __syncthreads();
-    int64_t n = 0;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) n += lds[w];
-    return n;
-}
+        for (int o = 32; o > 0; o >>= 1) {
+            const int32_t v = __shfl(at, min(i + o, 63));
+            if (i + o < 64 && s0 + i + o <= S && v <= row) i += o;
+        }
+        begin = __shfl(at, i);
+        end = __shfl(at, min(i + 1, 63));
+        int64_t s = s0 + i;
+        if (i == 63 && s < S) {                       // more sequences than lanes
+            while (s < S && offsets[s + 1] <= row) ++s;
+            begin = offsets[min(s, S - 1)];
+            end = offsets[min(s + 1, S)];
+        }
+        if (s >= S) {
+            begin = end = T;
+            return S;
+        }
+        begin = max(begin, (int64_t)0);
+        end = min(end, T);
+        return s;
+    }
+};
 
 struct Part { float p; int32_t c; };
 
+__device__ __forceinline__ float loss_of(double sum, int32_t E, int32_t top_k, int32_t tokens)
+{
+    const double n = tokens;
+    return tokens == 0 ? 0.0f : (float)(sum * E / ((double)top_k * n * n));
+}
+
 // ---- loss: parts of a chunk of rows --------------------------------------------
 
-template <int LPR, int G, int V, bool WIDE>
-__global__ __launch_bounds__(kThreads) void balance_parts_kernel(BalanceArgs m, int64_t chunk, Part* __restrict__ parts,
-                                                                 int32_t* __restrict__ part_n)
+// ALONE: one workgroup takes all rows and writes the losses itself.
+template <int DT, bool SOFT, int LPR, int V, bool ALONE>
+__global__ __launch_bounds__(ALONE ? kAloneThreads : kThreads) void balance_parts_kernel(BalanceArgs m, int64_t chunk, Part* __restrict__ parts,
+                                                                                         int32_t* __restrict__ part_n)
 {
-    constexpr int kRows = kThreads / LPR;             // rows at a time
-    extern __shared__ int32_t lds[];                  // [E] counts, then [kRows][E] sums
-    __shared__ int32_t found[kWaves];
+    constexpr int THREADS = ALONE ? kAloneThreads : kThreads, kWaves = THREADS / 64;
+    constexpr int kRows = THREADS / LPR;              // rows at a time
+    extern __shared__ int32_t lds[];                  // [E] counts, then [kWaves][E] sums
+    __shared__ double sum_lds[kWaves];
     __shared__ int32_t rows_lds;
     int32_t* hist = lds;
     float* sums = reinterpret_cast<float*>(lds + m.E);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x / 64;
     const int sub = threadIdx.x % LPR, slot = threadIdx.x / LPR;
-    const bool softmax = m.score == FTQ_SCORE_SOFTMAX;
     const int64_t r0 = (int64_t)blockIdx.x * chunk, r1 = min(m.T, r0 + chunk);
-    for (int64_t s = first_sequence(m.offsets, m.S, r0, found); s < m.S; ++s) {
+    Sequences seq;
+    seq.find(m.offsets, m.S, m.T, ALONE ? -1 : r0, lane);
+    int64_t s = 0, row = r0;
+    for (int64_t next = 0;; ++next) {
         int64_t begin, end;
-        sequence(m.offsets, s, m.T, begin, end);
-        if (begin >= r1) break;
-        begin = max(begin, r0);
-        end = min(end, r1);
-        if (begin >= end) continue;
+        if constexpr (ALONE) {                        // every sequence (there are few)
+            if ((s = next) >= m.S) break;
+            begin = m.offsets ? max((int64_t)__shfl(seq.at, (int)s), (int64_t)0) : 0;
+            end = m.offsets ? min((int64_t)__shfl(seq.at, (int)s + 1), m.T) : m.T;
+        } else {                                      // those that have rows in this chunk
+            if (row >= r1 || (s = seq.of(row, begin, end)) >= m.S || begin >= r1) break;
+            if (begin > row) {                        // rows of no sequence
+                row = begin;
+                continue;
+            }
+            begin = row;
+            row = end = min(end, r1);
+        }
+        const int count = (int)max(end - begin, (int64_t)0);
+        float acc[kPerLane] = {}, ahead[kPerLane];
+        int32_t n = 0;
+        const auto load = [&](int t) {
+            t = min(t, count - 1);
+            load_row<DT, LPR, V>(m.logits, (begin + t) * m.ld, sub, m.E, ahead);
+        };
+        if (count > 0) load(slot);
+        const int32_t* ids = m.ids + begin * m.top_k;
+        const int pairs = count * m.top_k;            // (a chunk's fit 32 bits)
+        int32_t next_id = (int)threadIdx.x < pairs ? ids[threadIdx.x] : -1;
         __syncthreads();                              // the last part has been written
-        for (int e = threadIdx.x; e < m.E; e += kThreads) hist[e] = 0;
+        for (int e = threadIdx.x; e < m.E; e += THREADS) hist[e] = 0;
         if (threadIdx.x == 0) rows_lds = 0;
         __syncthreads();
-        float acc[G][V] = {};
-        int32_t n = 0;
-        for (int64_t t = begin + slot; t < end; t += kRows) {
-            if (m.valid && !m.valid[t]) continue;
-            ++n;
-            float l[G][V], top = -kInf, sum = 0.0f;
-            load_row<WIDE, LPR>(m.logits, m.dtype, t * m.ld, sub, m.E, l);
+        for (int i = threadIdx.x; i < pairs; i += THREADS) {
+            const int32_t id = next_id;
+            next_id = i + THREADS < pairs ? ids[i + THREADS] : -1;
+            if (id >= 0 && id < m.E && (!m.valid || m.valid[begin + (uint32_t)i / (uint32_t)m.top_k])) atomicAdd(&hist[id], 1);
+        }
+        for (int t0 = 0; t0 < count; t0 += kRows) {   // every lane goes round as often
+            const bool live = t0 + slot < count && (!m.valid || m.valid[begin + t0 + slot]);
+            float l[kPerLane], w[kPerLane], rest[kPerLane], top, sum;
 #pragma unroll
-            for (int i = 0; i < G; ++i) {
-#pragma unroll
-                for (int v = 0; v < V; ++v) top = fmaxf(top, l[i][v]);
-            }
-            top = row_max<LPR>(top);
-#pragma unroll
-            for (int i = 0; i < G; ++i) {
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    l[i][v] = weight_of(l[i][v], top, softmax);
-                    sum += l[i][v];
-                }
-            }
-            sum = row_sum<LPR>(sum);
+            for (int i = 0; i < kPerLane; ++i) l[i] = ahead[i];
+            if (t0 + kRows < count) load(t0 + kRows + slot);
+            row_scores<SOFT, LPR>(l, w, rest, top, sum);
             const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+            n += live;
 #pragma unroll
-            for (int i = 0; i < G; ++i) {
-#pragma unroll
-                for (int v = 0; v < V; ++v) acc[i][v] = __builtin_fmaf(l[i][v], inv, acc[i][v]);
-            }
+            for (int i = 0; i < kPerLane; ++i) acc[i] = live ? __builtin_fmaf(w[i], inv, acc[i]) : acc[i];
         }
 #pragma unroll
-        for (int i = 0; i < G; ++i) {
-            const int e = (i * LPR + sub) * V;
-            if (e < m.E) {
-#pragma unroll
-                for (int v = 0; v < V; ++v) sums[slot * m.E + e + v] = acc[i][v];
-            }
+        for (int i = 0; i < kPerLane; ++i) {
+            const int e = (i / V * LPR + sub) * V + i % V;
+            acc[i] = sum_over_rows<LPR>(acc[i]);
+            if (lane < LPR && e < m.E) sums[wave * m.E + e] = acc[i];
         }
         if (sub == 0 && n) atomicAdd(&rows_lds, n);
-        const int64_t ids = (end - begin) * m.top_k;
-        for (int64_t i = threadIdx.x; i < ids; i += kThreads) {
-            const int64_t t = begin + i / m.top_k;
-            if (m.valid && !m.valid[t]) continue;
-            const int32_t id = m.ids[begin * m.top_k + i];
-            if (id >= 0 && id < m.E) atomicAdd(&hist[id], 1);
-        }
         __syncthreads();
         const int64_t at = blockIdx.x + s;
-        for (int e = threadIdx.x; e < m.E; e += kThreads) {
+        double loss = 0.0;
+        for (int e = threadIdx.x; e < m.E; e += THREADS) {
             float p = 0.0f;
-            for (int q = 0; q < kRows; ++q) p += sums[q * m.E + e];
-            parts[at * m.E + e] = Part{p, hist[e]};
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) p += sums[w * m.E + e];
+            if constexpr (ALONE) {
+                m.counts[s * m.E + e] = hist[e];
+                loss += (double)p * hist[e];
+            } else {
+                parts[at * m.E + e] = Part{p, hist[e]};
+            }
         }
-        if (threadIdx.x == 0) part_n[at] = rows_lds;
+        if constexpr (ALONE) {
+#pragma unroll
+            for (int o = 1; o < 64; o <<= 1) loss += __shfl_xor(loss, o);
+            if (lane == 0) sum_lds[wave] = loss;
+            __syncthreads();
+            if (threadIdx.x == 0) {
+                loss = 0.0;
+#pragma unroll
+                for (int w = 0; w < kWaves; ++w) loss += sum_lds[w];
+                m.tokens[s] = rows_lds;
+                m.loss[s] = loss_of(loss, m.E, m.top_k, rows_lds);
+            }
+        } else {
+            if (threadIdx.x == 0) part_n[at] = rows_lds;
+        }
     }
 }
 
@@ -206,8 +292,7 @@ __global__ __launch_bounds__(kSumThreads) void balance_sum_kernel(BalanceArgs m,
     __shared__ double wave_lds[kSumThreads / 64];
     __shared__ int32_t n_lds;
     const int64_t s = blockIdx.x;
-    int64_t begin, end;
-    sequence(m.offsets, s, m.T, begin, end);
+    const int64_t begin = m.offsets ? max(m.offsets[s], 0) : 0, end = m.offsets ? min((int64_t)m.offsets[s + 1], m.T) : m.T;
     const int64_t c0 = begin / chunk, c1 = begin < end ? (end - 1) / chunk + 1 : c0;
     if (threadIdx.x == 0) n_lds = 0;
     __syncthreads();
@@ -219,6 +304,7 @@ __global__ __launch_bounds__(kSumThreads) void balance_sum_kernel(BalanceArgs m,
     double p = 0.0;
     int32_t c_sum = 0;
     if (way < ways) {
+#pragma unroll 8
         for (int64_t c = c0 + way; c < c1; c += ways) {
             const Part x = parts[(c + s) * m.E + e];
             p += (double)x.p;
@@ -235,7 +321,7 @@ __global__ __launch_bounds__(kSumThreads) void balance_sum_kernel(BalanceArgs m,
             c_sum += c_lds[w * m.E + e];
         }
         m.counts[s * m.E + e] = c_sum;
-        loss = c_sum == 0 ? 0.0 * p : p * c_sum;
+        loss = p * c_sum;
     }
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) loss += __shfl_xor(loss, o);
@@ -244,191 +330,260 @@ __global__ __launch_bounds__(kSumThreads) void balance_sum_kernel(BalanceArgs m,
     if (threadIdx.x == 0) {
         loss = 0.0;
         for (int w = 0; w < kSumThreads / 64; ++w) loss += wave_lds[w];
-        const double nd = n_lds;
         m.tokens[s] = n_lds;
-        m.loss[s] = n_lds == 0 ? 0.0f : (float)(loss * m.E / ((double)m.top_k * nd * nd));
+        m.loss[s] = loss_of(loss, m.E, m.top_k, n_lds);
     }
 }
 
 // ---- gradient of the logits ------------------------------------------------------
 //
-// With v_e = d_loss E/(top_k n^2) c_e, u_e the sum of scale * d_gates over the
-// choices that are e, and m_e their number:
+// With v_e = d_loss E/(top_k n^2) c_e, and for choice j of expert e_j, u_j = scale * d_gates_j:
 //   balance               dl_k += p_k (v_k - sum_e p_e v_e) [* (1 - s_k) for sigmoid scores]
-//   gates, renormalised   D = sum m s, W = sum u s / D:  dl_k += s_k/D (u_k - m_k W) [* (1 - s_k)]
-//   gates, softmax        dl_k += s_k (u_k - sum_e u_e s_e)
-//   gates, sigmoid        dl_k += s_k (1 - s_k) u_k
+//   gates, renormalised   D = sum_j s, W = sum_j u s / D: choice j gives s/D (u - W) [* (1 - s)] to its expert
+//   gates, softmax        choice j gives s u to its expert, and dl_k -= p_k sum_j s u
+//   gates, sigmoid        choice j gives s (1 - s) u to its expert
+// The first and third have a term for every expert, which the row's lanes form of their
+// experts; what the choices give goes through LDS to the lanes that hold their experts.
 // s/D is formed from scores relative to the largest chosen logit, so that choices far
 // below the row's largest (a bias can choose them) keep their gradients.
 
-template <int LPR, int G, int V, bool WIDE>
+template <int DT, bool SOFT, int LPR, int V>
 __global__ __launch_bounds__(kThreads) void topk_backward_kernel(TopkBackwardArgs m, int64_t chunk)
 {
     constexpr int kRows = kThreads / LPR;
-    __shared__ int32_t found[kWaves];
-    const int sub = threadIdx.x % LPR, slot = threadIdx.x / LPR;
-    const bool softmax = m.score == FTQ_SCORE_SOFTMAX, balance = m.d_loss != nullptr;
+    extern __shared__ __attribute__((aligned(16))) float row_lds[];                // [kRows][E + 4] gradients of the choices by expert, zero between
+                                                      // rows, then [kRows][top_k] of them by choice, and the choices
+    const int lane = threadIdx.x & 63, sub = threadIdx.x % LPR, slot = threadIdx.x / LPR;
+    const int wide_e = m.E + 4;                       // rows of 256 floats would meet the same banks
+    float* by_expert = row_lds + slot * wide_e;
+    float* by_choice = row_lds + kRows * wide_e + slot * m.top_k;
+    int32_t* id_of = reinterpret_cast<int32_t*>(row_lds + kRows * (wide_e + m.top_k)) + slot * m.top_k;
+    const bool balance = m.d_loss != nullptr, spreads = SOFT && m.d_gates && !m.renorm;
     const int64_t r0 = (int64_t)blockIdx.x * chunk, r1 = min(m.T, r0 + chunk);
-    int64_t s = balance ? first_sequence(m.offsets, m.S, r0, found) : 0;
-    for (int64_t t = r0 + slot; t < r1; t += kRows) {
-        float grad[G][V] = {};
-        if (!m.valid || m.valid[t]) {
-            float l[G][V];
-            load_row<WIDE, LPR>(m.logits, m.dtype, t * m.ld, sub, m.E, l);
-            float top = -kInf;
-#pragma unroll
-            for (int i = 0; i < G; ++i) {
-#pragma unroll
-                for (int v = 0; v < V; ++v) top = fmaxf(top, l[i][v]);
+    if (m.d_gates) {
+        for (int e = sub; e < m.E; e += LPR) by_expert[e] = 0.0f;
+    }
+    for (int64_t b = r0; b < r1; b += kRows) {        // every lane goes round as often
+        // what a row reads is asked for at once: its logits, the lane's first choice and that choice's logit
+        const int64_t t = min(b + slot, r1 - 1);
+        const bool there = b + slot < r1, live = !m.valid || m.valid[t];
+        float grad[kPerLane] = {}, l[kPerLane], c[kPerLane] = {};
+        if (balance || spreads) load_row<DT, LPR, V>(m.logits, t * m.ld, sub, m.E, l);
+        const int32_t* ids = m.ids + t * m.top_k;
+        const float* d_gates = m.d_gates + t * m.top_k;
+        int32_t id0 = -1;
+        float u0 = 0.0f, x0 = 0.0f;
+        const auto choice = [&](int j, int32_t& id, float& u, float& x) {   // its expert (or -1), scaled gradient and logit
+            id = ids[j];
+            u = m.scale * d_gates[j];
+            if (id < 0 || id >= m.E) id = -1;
+            x = id >= 0 ? load_logit<DT>(m.logits, t * m.ld + id) : -kInf;
+        };
+        if (m.d_gates && sub < m.top_k) choice(sub, id0, u0, x0);
+        const auto recall = [&](int j, int32_t& id, float& u, float& x) {
+            if (j == sub) {
+                id = id0;
+                u = u0;
+                x = x0;
+            } else {
+                choice(j, id, u, x);
             }
-            top = row_max<LPR>(top);
-            bool counted = false;
-            float factor = 0.0f;
-            if (balance) {
-                while (s < m.S && m.offsets && m.offsets[s + 1] <= t) ++s;
-                int64_t begin = 0, end = 0;
-                if (s < m.S) sequence(m.offsets, s, m.T, begin, end);
-                counted = t >= begin && t < end;
-                if (counted) {
-                    const double n = m.tokens[s];
-                    factor = n > 0.0 ? (float)((double)m.d_loss[s] * m.E / ((double)m.top_k * n * n)) : 0.0f;
+        };
+        bool counted = false;
+        if (balance) {
+            Sequences seq;
+            seq.find(m.offsets, m.S, m.T, uniform(b + threadIdx.x / 64 * (64 / LPR)), lane);
+            const int64_t mine = min(seq.s0 + lane, m.S - 1);   // lane i: n and d_loss of sequence s0 + i
+            const int32_t tokens_at = m.tokens[mine];
+            const float d_loss_at = m.d_loss[mine];
+            int64_t begin, end;
+            const int64_t s = seq.of(t, begin, end);
+            float n = (float)__shfl(tokens_at, (int)min(s - seq.s0, (int64_t)63)), d = __shfl(d_loss_at, (int)min(s - seq.s0, (int64_t)63));
+            counted = live && s < m.S && t >= begin && t < end;
+            if (counted) {
+                if (s - seq.s0 > 63) {
+                    n = (float)m.tokens[s];
+                    d = m.d_loss[s];
                 }
-            }
-            float u[G][V] = {}, times[G][V] = {};
-            if (m.d_gates) {
-                for (int j = 0; j < m.top_k; ++j) {
-                    const int32_t id = m.ids[t * m.top_k + j];
-                    const float d = m.scale * m.d_gates[t * m.top_k + j];
+                const float factor = n > 0.0f ? d * (float)m.E / (float)m.top_k / n / n : 0.0f;
 #pragma unroll
-                    for (int i = 0; i < G; ++i) {
-#pragma unroll
-                        for (int v = 0; v < V; ++v) {
-                            const bool is = id == (i * LPR + sub) * V + v && id < m.E;
-                            u[i][v] += is ? d : 0.0f;
-                            times[i][v] += is ? 1.0f : 0.0f;
-                        }
-                    }
-                }
-            }
-            if (counted || (m.d_gates && softmax && !m.renorm)) {   // sums over the whole row
-                float w[G][V], sum = 0.0f, pv = 0.0f, us = 0.0f, c[G][V] = {};
-#pragma unroll
-                for (int i = 0; i < G; ++i) {
+                for (int i = 0; i < kPerLane / V; ++i) {
                     const int e = (i * LPR + sub) * V;
+                    if (e < m.E) {
+                        const RunF<V> r = *reinterpret_cast<const RunF<V>*>(reinterpret_cast<const float*>(m.counts) + s * m.E + e);
 #pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        if (counted && e < m.E) c[i][v] = (float)m.counts[s * m.E + e + v] * factor;
-                        w[i][v] = weight_of(l[i][v], top, softmax);
-                        sum += w[i][v];
-                        pv = __builtin_fmaf(w[i][v], c[i][v], pv);
-                        us = __builtin_fmaf(w[i][v], u[i][v], us);
-                    }
-                }
-                sum = row_sum<LPR>(sum);
-                const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-                pv = row_sum<LPR>(pv) * inv;
-                us = row_sum<LPR>(us) * inv;
-#pragma unroll
-                for (int i = 0; i < G; ++i) {
-#pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        const float p = w[i][v] * inv;
-                        if (counted) grad[i][v] = p * (c[i][v] - pv) * (softmax ? 1.0f : weight_of(-l[i][v], 0.0f, false));
-                        if (m.d_gates && softmax && !m.renorm) grad[i][v] += p * (u[i][v] - us);
-                    }
-                }
-            }
-            if (m.d_gates && m.renorm) {
-                float first = -kInf, w[G][V], sum = 0.0f, us = 0.0f;
-#pragma unroll
-                for (int i = 0; i < G; ++i) {
-#pragma unroll
-                    for (int v = 0; v < V; ++v) first = times[i][v] > 0.0f ? fmaxf(first, l[i][v]) : first;
-                }
-                first = row_max<LPR>(first);
-#pragma unroll
-                for (int i = 0; i < G; ++i) {
-#pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        w[i][v] = times[i][v] > 0.0f ? weight_of(l[i][v], first, softmax) : 0.0f;
-                        sum = __builtin_fmaf(times[i][v], w[i][v], sum);
-                        us = __builtin_fmaf(u[i][v], w[i][v], us);
-                    }
-                }
-                sum = row_sum<LPR>(sum);
-                const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-                us = row_sum<LPR>(us) * inv;
-#pragma unroll
-                for (int i = 0; i < G; ++i) {
-#pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        const float d = w[i][v] * inv * (u[i][v] - times[i][v] * us);
-                        if (times[i][v] > 0.0f) grad[i][v] += d * (softmax ? 1.0f : weight_of(-l[i][v], 0.0f, false));
-                    }
-                }
-            } else if (m.d_gates && !softmax) {
-#pragma unroll
-                for (int i = 0; i < G; ++i) {
-#pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        if (times[i][v] > 0.0f) grad[i][v] += u[i][v] * weight_of(l[i][v], 0.0f, false) * weight_of(-l[i][v], 0.0f, false);
+                        for (int v = 0; v < V; ++v) c[i * V + v] = (float)__builtin_bit_cast(int32_t, r.v[v]) * factor;
                     }
                 }
             }
         }
+        const bool spread = live && spreads, whole = counted || spread;   // whole: a term for every expert
+        // the row's lanes over its experts
+        float top = 0.0f, inv = 0.0f, pv = 0.0f, rest[kPerLane];
+        if (whole) {
+            float sum;
+            row_scores<SOFT, LPR>(l, grad, rest, top, sum);
+            inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
-        for (int i = 0; i < G; ++i) {
+            for (int i = 0; i < kPerLane; ++i) pv = __builtin_fmaf(grad[i], c[i], pv);
+            pv = row_sum<LPR>(pv) * inv;
+        }
+        // the row's lanes over its choices
+        float shared = pv;                            // what every expert's term is reduced by
+        bool chose = false;
+        if (live && m.d_gates) {
+            float first = -kInf, sum = 0.0f, us = 0.0f;
+            int32_t id;
+            float u, x, tail = 1.0f;
+            const auto score = [&](float x, float first) {   // up to a factor; tail: 1 - s of a sigmoid
+                if constexpr (SOFT) return exp_neg(x - finite_top(first));
+                const float s = sigmoid(x, tail);
+                return first < kLow ? exp_neg(x - finite_top(first)) : s;
+            };
+            if (m.renorm) {
+                for (int j = sub; j < m.top_k; j += LPR) {
+                    recall(j, id, u, x);
+                    first = fmaxf(first, x);
+                }
+                first = row_max<LPR>(first);
+                for (int j = sub; j < m.top_k; j += LPR) {
+                    recall(j, id, u, x);
+                    const float w = score(x, first);       // (of -inf 0)
+                    sum += w;
+                    us = __builtin_fmaf(u, w, us);
+                }
+                sum = row_sum<LPR>(sum);
+                sum = sum == 0.0f ? 0.0f : 1.0f / sum;
+                us = row_sum<LPR>(us) * sum;
+            }
+            float given = 0.0f;
+            for (int j = sub; j < m.top_k; j += LPR) {
+                recall(j, id, u, x);
+                float g = 0.0f;
+                if (id >= 0) {
+                    chose = true;
+                    if (m.renorm) g = score(x, first) * sum * (u - us);
+                    else g = SOFT ? score(x, top) * inv * u : score(x, 0.0f) * u;
+                    g *= tail;
+                    given += g;
+                }
+                by_choice[j] = g;
+                id_of[j] = id;
+            }
+            if (spread) shared += row_sum<LPR>(given);
+            wave_lds_fence();
+            for (int j = sub; j < m.top_k; j += LPR) {   // an expert chosen more than once: the sum in the choices' order, by each
+                id = id_of[j];
+                if (id < 0) continue;
+                float total = 0.0f;
+                for (int i = 0; i < m.top_k; ++i) total += id_of[i] == id ? by_choice[i] : 0.0f;
+                by_expert[id] = total;
+            }
+            wave_lds_fence();
+        }
+        const bool any = row_max<LPR>(chose ? 1.0f : 0.0f) > 0.0f;
+        if (whole) {
+#pragma unroll
+            for (int i = 0; i < kPerLane; ++i) {
+                const float d = grad[i] * inv * (c[i] - shared) * (SOFT ? 1.0f : rest[i]);
+                grad[i] = counted || any ? d : 0.0f;
+            }
+        }
+        if (any) {
+#pragma unroll
+            for (int i = 0; i < kPerLane / V; ++i) {
+                const int e = (i * LPR + sub) * V;
+                if (e < m.E) {
+                    const LineF<V> r = *reinterpret_cast<const LineF<V>*>(by_expert + e);
+#pragma unroll
+                    for (int v = 0; v < V; ++v) grad[i * V + v] += r.v[v];
+                }
+            }
+            wave_lds_fence();
+            for (int j = sub; j < m.top_k; j += LPR) {
+                if (id_of[j] >= 0) by_expert[id_of[j]] = 0.0f;
+            }
+            wave_lds_fence();
+        }
+#pragma unroll
+        for (int i = 0; i < kPerLane / V; ++i) {
             const int e = (i * LPR + sub) * V;
-            if (e >= m.E) continue;
-            if constexpr (WIDE) {
+            if (!there || e >= m.E) continue;
+            if constexpr (DT == FTQ_F32) {
                 RunF<V> r;
 #pragma unroll
-                for (int v = 0; v < V; ++v) r.v[v] = grad[i][v];
+                for (int v = 0; v < V; ++v) r.v[v] = grad[i * V + v];
                 *reinterpret_cast<RunF<V>*>(static_cast<float*>(m.d_logits) + t * m.ld_d + e) = r;
             } else {
                 RunH<V> r;
 #pragma unroll
-                for (int v = 0; v < V; ++v) r.v[v] = m.dtype == FTQ_F16 ? f16_of_f32(grad[i][v]) : bf16_of_f32(grad[i][v]);
+                for (int v = 0; v < V; ++v) r.v[v] = DT == FTQ_F16 ? f16_of_f32(grad[i * V + v]) : bf16_of_f32(grad[i * V + v]);
                 *reinterpret_cast<RunH<V>*>(static_cast<uint16_t*>(m.d_logits) + t * m.ld_d + e) = r;
             }
         }
     }
 }
 
-constexpr int64_t kChunkRows = 64, kMaxChunks = 512;
+constexpr int64_t kMaxChunks = 2048;
 
-// Calls f<LPR, G, V>() for a row of E experts.
-template <typename F>
-int by_layout(int64_t E, F f)
+// Lanes of a row of E experts.  (Odd numbers of experts have two layouts, so that there are fewer kernels.)
+int lanes_of(int64_t E)
 {
-    if (E % 4 == 0) {
-        if (E <= 32) return f.template operator()<8, 1, 4>();
-        if (E <= 64) return f.template operator()<16, 1, 4>();
-        if (E <= 128) return f.template operator()<32, 1, 4>();
-        if (E <= 256) return f.template operator()<64, 1, 4>();
-        if (E <= 512) return f.template operator()<64, 2, 4>();
-        return f.template operator()<64, 4, 4>();
-    }
-    if (E <= 8) return f.template operator()<8, 1, 1>();
-    if (E <= 64) return f.template operator()<64, 1, 1>();
-    if (E <= 128) return f.template operator()<64, 2, 1>();
-    if (E <= 256) return f.template operator()<64, 4, 1>();
-    if (E <= 512) return f.template operator()<64, 8, 1>();
-    return f.template operator()<64, 16, 1>();
+    if (E % 4 != 0) return E <= 256 ? 16 : 64;
+    return E <= 32 ? 2 : E <= 64 ? 4 : E <= 128 ? 8 : E <= 256 ? 16 : E <= 512 ? 32 : 64;
+}
+
+// Calls f<DT, SOFT, LPR, V>() for such rows.
+template <typename F>
+int by_layout(int dtype, int score, int64_t E, F f)
+{
+    const auto with = [&](auto dt, auto soft) {
+        constexpr int DT = decltype(dt)::value;
+        constexpr bool SOFT = decltype(soft)::value;
+        const int lanes = lanes_of(E);
+        if (E % 4 != 0) return lanes == 16 ? f.template operator()<DT, SOFT, 16, 1>() : f.template operator()<DT, SOFT, 64, 1>();
+        if (lanes == 2) return f.template operator()<DT, SOFT, 2, 4>();
+        if (lanes == 4) return f.template operator()<DT, SOFT, 4, 4>();
+        if (lanes == 8) return f.template operator()<DT, SOFT, 8, 4>();
+        if (lanes == 16) return f.template operator()<DT, SOFT, 16, 4>();
+        if (lanes == 32) return f.template operator()<DT, SOFT, 32, 4>();
+        return f.template operator()<DT, SOFT, 64, 4>();
+    };
+    const auto typed = [&](auto dt) { return score == FTQ_SCORE_SOFTMAX ? with(dt, std::true_type{}) : with(dt, std::false_type{}); };
+    if (dtype == FTQ_F32) return typed(std::integral_constant<int, FTQ_F32>{});
+    if (dtype == FTQ_F16) return typed(std::integral_constant<int, FTQ_F16>{});
+    return typed(std::integral_constant<int, FTQ_BF16>{});
+}
+
+// Rows that a workgroup of so many threads works on at a time.
+int64_t rows_at_once(int64_t E, int64_t threads) { return threads / lanes_of(E); }
+
+struct BalancePlan { int64_t chunk, chunks, off_n, bytes; bool alone; };
+
+// One workgroup does a small batch by itself: at most two rounds over the rows, and few sequences, which it takes one by one.
+BalancePlan plan_balance(int64_t T, int64_t E, int64_t S)
+{
+    BalancePlan p;
+    p.alone = S <= 4 && T <= 2 * rows_at_once(E, kAloneThreads);
+    p.chunk = p.alone ? std::max<int64_t>(T, 1) : std::max(rows_at_once(E, kThreads), (T + kMaxChunks - 1) / kMaxChunks);
+    p.chunks = p.alone ? 1 : (T + p.chunk - 1) / p.chunk;
+    p.off_n = (p.chunks + S) * E * (int64_t)sizeof(Part);
+    p.bytes = (p.off_n + (p.chunks + S) * 4 + 255) / 256 * 256;
+    return p;
 }
 
 struct PartsCall {
     const BalanceArgs& m;
-    int64_t chunk, chunks;
+    const BalancePlan& p;
     Part* parts;
     int32_t* part_n;
     hipStream_t s;
-    template <int LPR, int G, int V> int operator()() const
+    template <int DT, bool SOFT, int LPR, int V> int operator()() const
     {
-        const size_t lds = sizeof(int32_t) * m.E * (1 + kThreads / LPR);
-        if (m.dtype == FTQ_F32)
-            return launch("balance_parts_kernel", balance_parts_kernel<LPR, G, V, true>, chunks, kThreads, lds, s, m, chunk, parts, part_n);
-        return launch("balance_parts_kernel", balance_parts_kernel<LPR, G, V, false>, chunks, kThreads, lds, s, m, chunk, parts, part_n);
+        const auto go = [&](auto* kernel, int threads) {
+            return launch("balance_parts_kernel", kernel, p.chunks, threads, sizeof(int32_t) * m.E * (1 + threads / 64), s, m, p.chunk, parts, part_n);
+        };
+        return p.alone ? go(balance_parts_kernel<DT, SOFT, LPR, V, true>, kAloneThreads) : go(balance_parts_kernel<DT, SOFT, LPR, V, false>, kThreads);
     }
 };
 
@@ -436,25 +591,12 @@ struct TopkBackwardCall {
     const TopkBackwardArgs& m;
     int64_t chunk, chunks;
     hipStream_t s;
-    template <int LPR, int G, int V> int operator()() const
+    template <int DT, bool SOFT, int LPR, int V> int operator()() const
     {
-        if (m.dtype == FTQ_F32)
-            return launch("topk_backward_kernel", topk_backward_kernel<LPR, G, V, true>, chunks, kThreads, 0, s, m, chunk);
-        return launch("topk_backward_kernel", topk_backward_kernel<LPR, G, V, false>, chunks, kThreads, 0, s, m, chunk);
+        const size_t lds = m.d_gates ? sizeof(float) * (kThreads / LPR) * (m.E + 4 + 2 * m.top_k) : 0;
+        return launch("topk_backward_kernel", topk_backward_kernel<DT, SOFT, LPR, V>, chunks, kThreads, lds, s, m, chunk);
     }
 };
-
-struct BalancePlan { int64_t chunk, chunks, off_n, bytes; };
-
-BalancePlan plan_balance(int64_t T, int64_t E, int64_t S)
-{
-    BalancePlan p;
-    p.chunk = std::max(kChunkRows, (T + kMaxChunks - 1) / kMaxChunks);
-    p.chunks = (T + p.chunk - 1) / p.chunk;
-    p.off_n = (p.chunks + S) * E * (int64_t)sizeof(Part);
-    p.bytes = (p.off_n + (p.chunks + S) * 4 + 255) / 256 * 256;
-    return p;
-}
 
 }  // namespace
 
@@ -466,8 +608,8 @@ int run_balance(const BalanceArgs& m, void* ws, hipStream_t s)
     Part* parts = static_cast<Part*>(ws);
     int32_t* part_n = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + p.off_n);
     if (p.chunks > 0) {
-        const int st = by_layout(m.E, PartsCall{m, p.chunk, p.chunks, parts, part_n, s});
-        if (st != FTQ_OK) return st;
+        const int st = by_layout(m.dtype, m.score, m.E, PartsCall{m, p, parts, part_n, s});
+        if (st != FTQ_OK || p.alone) return st;
     }
     return launch("balance_sum_kernel", balance_sum_kernel, m.S, kSumThreads, 0, s, m, p.chunk, static_cast<const Part*>(parts),
                   static_cast<const int32_t*>(part_n));
@@ -475,8 +617,9 @@ int run_balance(const BalanceArgs& m, void* ws, hipStream_t s)
 
 int run_topk_backward(const TopkBackwardArgs& m, hipStream_t s)
 {
-    const int64_t chunk = std::max<int64_t>(32, (m.T + (int64_t(1) << 20) - 1) >> 20);
-    return by_layout(m.E, TopkBackwardCall{m, chunk, (m.T + chunk - 1) / chunk, s});
+    const int64_t rows = rows_at_once(m.E, kThreads);   // a workgroup goes round once, unless there are more than a launch takes
+    const int64_t chunk = std::max(rows, (m.T + (int64_t(1) << 20) - 1) >> 20);
+    return by_layout(m.dtype, m.score, m.E, TopkBackwardCall{m, chunk, (m.T + chunk - 1) / chunk, s});
 }
 
 }  // namespace ftq

@@ -21,6 +21,7 @@
 // the 6.5 and 0.4 us that the logits take to read; a single row takes 3 to 7 us, the
 // length of its chain of reductions.
 #include "ftq_internal.h"
+#include "row_lanes.h"
 
 namespace ftq {
 namespace {
@@ -60,55 +61,8 @@ __device__ __forceinline__ void load_logits(const TopkArgs& m, int64_t i, float 
     }
 }
 
-// ---- reductions over the LPR lanes of a row; every lane gets the result ---------
+// ---- reductions over the LPR lanes of a row (row_lanes.h has the 32-bit ones) --------
 
-// The value of the lane across one halving step: lanes of a 2^(STEP+1) group hold
-// equal values within its halves when STEP is reached, so mirrored lanes do.
-template <int STEP>
-__device__ __forceinline__ uint32_t across(uint32_t v)
-{
-    if constexpr (STEP == 0) return __builtin_amdgcn_update_dpp(v, v, 0xB1, 0xF, 0xF, false);    // quad_perm 1 0 3 2
-    if constexpr (STEP == 1) return __builtin_amdgcn_update_dpp(v, v, 0x4E, 0xF, 0xF, false);    // quad_perm 2 3 0 1
-    if constexpr (STEP == 2) return __builtin_amdgcn_update_dpp(v, v, 0x141, 0xF, 0xF, false);   // row_half_mirror
-    return __builtin_amdgcn_update_dpp(v, v, 0x140, 0xF, 0xF, false);                            // row_mirror
-}
-
-template <int LPR, typename F>
-__device__ __forceinline__ uint32_t row_reduce(uint32_t v, F op)
-{
-    if constexpr (LPR > 1) v = op(v, across<0>(v));
-    if constexpr (LPR > 2) v = op(v, across<1>(v));
-    if constexpr (LPR > 4) v = op(v, across<2>(v));
-    if constexpr (LPR > 8) v = op(v, across<3>(v));
-    if constexpr (LPR > 16) {
-        const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
-        v = op(r[0], r[1]);
-    }
-    if constexpr (LPR > 32) {
-        const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
-        v = op(r[0], r[1]);
-    }
-    return v;
-}
-__device__ __forceinline__ float as_f(uint32_t u) { return __builtin_bit_cast(float, u); }
-__device__ __forceinline__ uint32_t as_u(float f) { return __builtin_bit_cast(uint32_t, f); }
-
-template <int LPR> __device__ __forceinline__ uint32_t row_max_u(uint32_t v)
-{
-    return row_reduce<LPR>(v, [](uint32_t a, uint32_t b) { return max(a, b); });
-}
-template <int LPR> __device__ __forceinline__ float row_max(float v)
-{
-    return as_f(row_reduce<LPR>(as_u(v), [](uint32_t a, uint32_t b) { return as_u(fmaxf(as_f(a), as_f(b))); }));
-}
-template <int LPR> __device__ __forceinline__ float row_min(float v)
-{
-    return as_f(row_reduce<LPR>(as_u(v), [](uint32_t a, uint32_t b) { return as_u(fminf(as_f(a), as_f(b))); }));
-}
-template <int LPR> __device__ __forceinline__ float row_sum(float v)
-{
-    return as_f(row_reduce<LPR>(as_u(v), [](uint32_t a, uint32_t b) { return as_u(as_f(a) + as_f(b)); }));
-}
 template <int LPR> __device__ __forceinline__ double row_sum(double v)
 {
 #pragma unroll

@@ -40,8 +40,9 @@ def _check_loss(logits, ids, score, offsets=None, valid=None):
     for s, r in enumerate(seqs):
         assert torch.equal(counts[s].cpu(), t.counts_of(ids, r, E).to(torch.int32)), f"sequence {s}"
     ref = t.losses(logits.double(), ids, E, k, seqs, SOFT[score])
-    # all terms are positive.  A share: two exponentials (4 roundings each), their quotient (2), the row's sum (16 + 6)
-    # and the division (2), 34; the sum over rows: 64 in fp32, then fp64 and one rounding
+    # all terms are positive.  A share: an exponential (|x| + 2 units of 2^-24, |x| <= 20 here, or the share is lost beside
+    # the row's others), the score's reciprocal and products (6), the row's sum (16 + 6) and the division (2), below 60; the
+    # sum over rows: 64 in fp32 and a tree, then fp64 and one rounding.  Together below 200 units, 100 steps
     off = (loss.double().cpu() - ref).abs()
     assert (off <= 2 * t.U * 100 * ref).all(), (off / ref).max()
     return loss, counts, tokens
@@ -72,6 +73,25 @@ def test_loss_of_packed_sequences(T, S, before, behind, padded, score):
         logits[T - behind:] = float("nan")
     offsets = _cuts(g, T, S, before, behind)
     _check_loss(logits, ids, score, offsets, valid)
+
+
+@pytest.mark.parametrize("T,S", [(5000, 5000), (300, 20000), (3000, 64), (3000, 63), (3000, 65), (9000, 130)])
+def test_many_sequences(T, S):
+    """Sequences of one row, long runs of empty ones, and numbers of them around a wave's lanes: loss and gradient."""
+    g, logits, ids = _inputs(T, 16, 2, "f32", seed=S)
+    offsets = torch.arange(S + 1, dtype=torch.int32) if T == S else _cuts(g, T, S, 2, 3)
+    loss, counts, tokens = _check_loss(logits, ids, ftq.SCORE_SIGMOID, offsets)
+    d_loss = torch.randn(S, generator=g)
+    got = ftq.moe_topk_backward(*_cuda(logits, ids), score=ftq.SCORE_SIGMOID, d_loss=d_loss.cuda(), counts=counts, tokens=tokens,
+                                offsets=offsets.cuda()).cpu()
+    row = torch.arange(T)
+    seq = torch.searchsorted(offsets[1:].contiguous(), row.to(torch.int32), right=True)
+    inside = (row >= offsets[0]) & (row < offsets[-1])
+    at = seq.clamp_max(S - 1)
+    n = tokens.cpu().double()[at].clamp_min(1)
+    v = counts.cpu().double()[at] * (d_loss.double()[at] * 16 / (2 * n * n))[:, None] * inside[:, None]
+    s, p = scores_and_shares(logits.double(), False)
+    t.close(got, p * (1 - s) * (v - (p * v).sum(1, keepdim=True)), p * (v.abs() + (p * v.abs()).sum(1, keepdim=True)), 144, "d_logits")
 
 
 def test_loss_of_strange_rows():
@@ -165,7 +185,8 @@ def _check_grad(logits, ids, score, renorm, scale=1.0, d_gates=None, d_loss=None
     got = ftq.moe_topk_backward(*_cuda(logits, ids), score=score, renorm=renorm, scale=scale, **dev)
     if check:
         ref, mag = _grad_ref(logits, ids, d_gates, score, renorm, scale, d_loss, offsets, valid)
-        # the shares' 34 roundings twice (p and the sum over the row), a sum over at most 64 choices, products and differences
+        # in steps of two units: the shares' 60 units twice (p and the sum over the row), a sum over at most 64 choices (64
+        # units), products and differences: below 144 steps
         t.close(got, ref, mag, 34 * 2 + 64 + 12, "d_logits")
     return got
 
@@ -203,6 +224,18 @@ def test_gradient_of_packed_sequences(renorm, score):
     a = _check_grad(dirty, ids, score, renorm, 0.7, d_gates, d_loss, offsets, valid, check=False)
     b = _check_grad(logits, ids, score, renorm, 0.7, d_gates, d_loss, offsets, valid, check=False)
     assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("E,k", [(2, 64), (31, 64), (8, 9), (100, 33)])
+def test_gradient_of_many_choices(E, k):
+    """More choices than lanes of a row, and than experts: every expert several times."""
+    g, logits, _ = _inputs(200, E, 1, "f32", seed=E)
+    ids = torch.randint(-1, E, (200, k), generator=g).to(torch.int32)
+    d_gates, d_loss = torch.randn(200, k, generator=g), torch.rand(1, generator=g)
+    for score in SOFT:
+        _check_loss(logits, ids, score)
+        for renorm in (True, False):
+            _check_grad(logits, ids, score, renorm, 1.0, d_gates, d_loss)
 
 
 @pytest.mark.parametrize("score", [ftq.SCORE_SOFTMAX, ftq.SCORE_SIGMOID])

@@ -524,7 +524,7 @@ __global__ __launch_bounds__(kThreads) void topk_backward_kernel(TopkBackwardArg
     }
 }
 
-constexpr int64_t kMaxChunks = 2048;
+constexpr int64_t kMaxChunks = 512;
 
 // Lanes of a row of E experts.  (Odd numbers of experts have two layouts, so that there are fewer kernels.)
 int lanes_of(int64_t E)

@@ -42,6 +42,10 @@ __device__ __forceinline__ void block_barrier()
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
+// All of the wave's global accesses so far have ended, and the compiler knows it: before a loop that copies, so
+// that it puts no wait of its own (which would wait for the copies too) into the loop.
+__device__ __forceinline__ void settle() { __builtin_amdgcn_s_waitcnt(0x0F70); }
+
 // At most N of the wave's global accesses are left in flight (they end in their order).
 template <int N> __device__ __forceinline__ void wait_copies_but() { __asm__ volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); }
 

@@ -71,6 +71,12 @@ __device__ __forceinline__ f32x4 multiply(u32x4 a, u32x4 b, f32x4 c)
     }
 }
 
+// Of 16 lanes, each naming 8 bytes (four 16-bit values), four lanes a row: lane l gets value l of the four rows.
+__device__ __forceinline__ u32x2 read_transposed(const uint8_t* lds)
+{
+    return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) i16x4*)lds));
+}
+
 // The next 16-bit piece of v; v becomes what is left of it.
 template <int DT>
 __device__ __forceinline__ uint16_t take_piece(float& v)
@@ -100,7 +106,7 @@ __device__ __forceinline__ int middle_exponent(float size)
 struct ShrinkArgs {
     const uint8_t* v;          // rows
     int64_t ldv;               // bytes from row to row
-    const uint8_t* w;          // [L][R][C]
+    const uint8_t* w;          // [L][R][C], or [L][C][R] (by_column)
     const int32_t* ids;        // [pairs]
     const int32_t* sorted;     // [pairs] or null: pairs in the order of tiles
     float* part;               // [splits][pairs][R]
@@ -113,9 +119,17 @@ struct ShrinkArgs {
 constexpr int kDepth = 4;      // pieces in LDS: one is multiplied while three are on their way
 
 // A workgroup takes 16 rows a wave.  LDS: run c (16 bytes) of row x sits at c ^ (x % 8).
-template <int DT, int WAVES, int RT>
+// COLS: the weights lie by column, [C][R].  A piece of them is then as many rows of R values
+// as it has columns (rows padded to 16*RT), and a lane collects its columns' values of one
+// rank, in 16 bits by transposing reads of four columns x 16 ranks.  The columns' places and
+// runs are permuted so that the 16 columns of such a read lie side by side and meet no bank twice.
+template <int DT, int WAVES, int RT, bool COLS>
 __global__ __launch_bounds__(64 * WAVES) void lora_shrink_kernel(ShrinkArgs m)
 {
+    constexpr int kRuns = RT * kSize<DT>;                          // 16-byte runs of a column's ranks
+    constexpr int kSpread = RT == 8 ? 0 : RT == 4 ? 1 : RT == 2 ? 2 : 3;
+    static_assert(kLine / kSize<DT> * kRuns == 128 * RT);
+    const auto run_at = [](int place, int run) { return DT == FTQ_F32 ? run : run ^ (((place >> kSpread) & (RT - 1)) << 1); };
     constexpr int BM = 16 * WAVES;
     constexpr int kW = 2 * RT, kShare = (kW + WAVES - 1) / WAVES;   // copies of the weights' rows: in all, and a wave's
     constexpr int kPer = 2 + kShare;                               // copies of a wave and step
@@ -139,7 +153,7 @@ __global__ __launch_bounds__(64 * WAVES) void lora_shrink_kernel(ShrinkArgs m)
     const uint8_t* xsrc[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) xsrc[i] = m.v + (int64_t)(__shfl(pair, min((wave * 2 + i) * 8 + cr, rows - 1)) / m.div) * m.ldv;
-    const int64_t total = (m.row_bytes + kLine - 1) / kLine, first = (int64_t)ks * m.steps;
+    const int64_t total = (m.row_bytes + kLine - 1) / kLine, first = (int64_t)ks * m.steps, columns = m.row_bytes / kSize<DT>;
     const int n = (int)max((int64_t)0, min((int64_t)m.steps, total - first));
     const int32_t my_pair = __shfl(pair, wave * 16 + r16);
     for (int index = 0; todo; ++index) {
@@ -148,8 +162,20 @@ __global__ __launch_bounds__(64 * WAVES) void lora_shrink_kernel(ShrinkArgs m)
         todo &= ~mine;
         if (index % m.groups != g) continue;
         const uint8_t* wsrc[kShare];
+        int col[kShare];                                           // COLS: the column of a step's that this lane copies a run of, or none (a large one)
 #pragma unroll
-        for (int i = 0; i < kShare; ++i) wsrc[i] = m.w + ((int64_t)l * m.R + min((wave + i * WAVES) % kW * 8 + cr, m.R - 1)) * m.row_bytes;
+        for (int i = 0; i < kShare; ++i) {
+            const int part = (wave + i * WAVES) % kW;
+            if constexpr (COLS) {
+                const int at = part * 64 + lane, place = at / kRuns, run_w = run_at(place, at % kRuns);
+                // place = 32h + 16a + 4b + c of 16-bit columns 32h + 8b + 4a + c, 16h + 4b + a of 32-bit ones 16h + 4a + b
+                col[i] = DT == FTQ_F32 ? (place & 16) + 4 * (place & 3) + ((place >> 2) & 3) : (place & 32) + 8 * ((place >> 2) & 3) + 4 * ((place >> 4) & 1) + (place & 3);
+                wsrc[i] = m.w + ((int64_t)l * columns + col[i]) * m.R * kSize<DT> + run_w * 16;
+                if (run_w * 16 >= m.R * kSize<DT>) col[i] = INT32_MAX;
+            } else {
+                wsrc[i] = m.w + ((int64_t)l * m.R + min(part * 8 + cr, m.R - 1)) * m.row_bytes;
+            }
+        }
         const auto copy_step = [&](int s) {
             const int64_t byte = (first + s) * kLine + run * 16;
             const bool in = byte < m.row_bytes;
@@ -158,10 +184,18 @@ __global__ __launch_bounds__(64 * WAVES) void lora_shrink_kernel(ShrinkArgs m)
 #pragma unroll
             for (int i = 0; i < 2; ++i) copy16(lds_address(&xs[buf][(wave * 2 + i) * 8][0]), in ? xsrc[i] + byte : none);
 #pragma unroll
-            for (int i = 0; i < kShare; ++i) copy16(lds_address(&ws[buf][(wave + i * WAVES) % kW * 8][0]), in ? wsrc[i] + byte : none);
+            for (int i = 0; i < kShare; ++i) {
+                const uint8_t* src = in ? wsrc[i] + byte : none;
+                if constexpr (COLS) {
+                    const int64_t c = (first + s) * (kLine / kSize<DT>);
+                    src = col[i] < columns - c ? wsrc[i] + c * m.R * kSize<DT> : none;
+                }
+                copy16(lds_address(&ws[buf][(wave + i * WAVES) % kW * 8][0]), src);
+            }
         };
         f32x4 acc[RT] = {};
         block_barrier();                                           // the last adapter's pieces have been read
+        settle();
         for (int s = 0; s < kDepth - 1 && s < n; ++s) copy_step(s);
         for (int s = 0; s < n; ++s) {
             if (n - 1 - s >= 2) wait_copies_but<2 * kPer>();
@@ -174,7 +208,27 @@ __global__ __launch_bounds__(64 * WAVES) void lora_shrink_kernel(ShrinkArgs m)
             for (int h = 0; h < 2; ++h) {
                 const u32x4 x = xs[buf][wave * 16 + r16][(4 * h + q) ^ (r16 & 7)];
 #pragma unroll
-                for (int i = 0; i < RT; ++i) acc[i] = multiply<DT>(ws[buf][16 * i + r16][(4 * h + q) ^ (r16 & 7)], x, acc[i]);
+                for (int i = 0; i < RT; ++i) {
+                    u32x4 w;
+                    if constexpr (!COLS) {
+                        w = ws[buf][16 * i + r16][(4 * h + q) ^ (r16 & 7)];
+                    } else {
+                        const uint8_t* base = reinterpret_cast<const uint8_t*>(&ws[buf][0][0]);
+                        if constexpr (DT == FTQ_F32) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) w[e] = *reinterpret_cast<const uint32_t*>(base + ((16 * h + 4 * e + q) * kRuns * 16 + (16 * i + r16) * 4));
+                        } else {
+#pragma unroll
+                            for (int a = 0; a < 2; ++a) {
+                                const int place = 32 * h + 16 * a + 4 * q + (r16 >> 2);
+                                const u32x2 t = read_transposed(base + (place * kRuns + run_at(place, 2 * i + ((r16 & 3) >> 1))) * 16 + (r16 & 1) * 8);
+                                w[2 * a] = t[0];
+                                w[2 * a + 1] = t[1];
+                            }
+                        }
+                    }
+                    acc[i] = multiply<DT>(w, x, acc[i]);
+                }
             }
         }
         if (mine >> (wave * 16 + r16) & 1) {
@@ -191,7 +245,7 @@ __global__ __launch_bounds__(64 * WAVES) void lora_shrink_kernel(ShrinkArgs m)
 
 struct ExpandArgs {
     const float* part;         // [splits][pairs][R]
-    const uint8_t* w;          // [L][C][R]
+    const uint8_t* w;          // [L][C][R], or [L][R][C] (by rank)
     const float* scale;        // [L] or null
     const int32_t* ids;
     const int32_t* sorted;     // or null
@@ -241,8 +295,9 @@ __device__ __forceinline__ void add_and_store(void* out, int64_t i, u32x4 base, 
 // which column is free and chosen so that a lane's results are whole 16-byte stores and
 // the four lanes of a row 64 bytes side by side: 32-bit results, row r of tile i is column
 // 16*i + r; 16-bit ones, column 32*(i/2) + 8*(r/4) + 4*(i%2) + r%4.
-// KST: 64-byte steps of an R-vector.
-template <int DT, int OT, int BT, int KST>
+// KST: 64-byte steps of an R-vector.  RANKS: the weights lie by rank, [R][C]; a lane then
+// loads its values one by one, 16 lanes neighbouring columns (they are few beside base and out).
+template <int DT, int OT, int BT, int KST, bool RANKS>
 __global__ __launch_bounds__(kThreads) void lora_expand_kernel(ExpandArgs m)
 {
     constexpr int BM = 16 * BT, kElems = 64 / kSize<DT>;           // elements of a step
@@ -328,10 +383,22 @@ __global__ __launch_bounds__(kThreads) void lora_expand_kernel(ExpandArgs m)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int c = kWide ? 16 * i + r16 : 32 * (i / 2) + 8 * (r16 / 4) + 4 * (i % 2) + r16 % 4;
-                    const uint8_t* src = m.w + (((int64_t)l * m.C + min(c0 + c, m.C - 1)) * m.R) * kSize<DT> + q * 16;
+                    const int64_t col = min(c0 + c, m.C - 1);
 #pragma unroll
                     for (int k = 0; k < KST; ++k) {
-                        if (k * kElems + q * (16 / kSize<DT>) < m.R) w[i][k] = *reinterpret_cast<const u32x4*>(src + k * 64);
+                        const int r = k * kElems + q * (16 / kSize<DT>);
+                        if (r >= m.R) continue;                    // (R is a multiple of 8: all of a lane's ranks are there or none)
+                        if constexpr (RANKS) {
+                            using Bits = std::conditional_t<DT == FTQ_F32, uint32_t, uint16_t>;
+                            const Bits* src = reinterpret_cast<const Bits*>(m.w) + ((int64_t)l * m.R + r) * m.C + col;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                if constexpr (DT == FTQ_F32) w[i][k][e] = src[e * m.C];
+                                else w[i][k][e] = src[2 * e * m.C] | (uint32_t)src[(2 * e + 1) * m.C] << 16;
+                            }
+                        } else {
+                            w[i][k] = *reinterpret_cast<const u32x4*>(m.w + (((int64_t)l * m.C + col) * m.R + r) * kSize<DT>);
+                        }
                     }
                 }
             }
@@ -530,7 +597,22 @@ struct OuterArgs {
     int32_t run;               // tiles of a workgroup
 };
 
-constexpr int kOuterDepth = 3, kBatch = 32;           // tiles in LDS, tiles listed there
+constexpr int kBatch = 32;                             // tiles listed in LDS
+// Tiles in LDS: as many as let two workgroups onto a CU, or one of the highest ranks.  (8192 rows of 4096 columns, rank
+// 64: 41 us with two tiles and two workgroups, 48 to 56 with four or five tiles and one.)
+template <int RT> constexpr int kOuterDepth = RT == 4 ? 2 : 3;
+
+// Waits until at most `left` (uniform, below D - 1) of the steps copied after the next one are in flight, PER copies each.
+template <int PER, int D>
+__device__ __forceinline__ void wait_step(int left)
+{
+    if constexpr (D > 0) {
+        if (left >= D) wait_copies_but<PER * D>();
+        else wait_step<PER, D - 1>(left);
+    } else {
+        wait_copies();
+    }
+}
 
 template <int DT, int RT>
 __global__ __launch_bounds__(kThreads) void lora_outer_kernel(OuterTables tab, OuterArgs a0, OuterArgs a1)
@@ -538,14 +620,19 @@ __global__ __launch_bounds__(kThreads) void lora_outer_kernel(OuterTables tab, O
     constexpr int kCols = 512 / kSize<DT>, kTiles = kCols / 64;    // columns of a workgroup, 16-column tiles of a wave
     constexpr int kULine = kTile * kSize<DT>;                      // bytes of a rank's row of u
     constexpr int kUBytes = kPieces<DT> * 16 * RT * kULine;        // of a tile, whole copies of 1024
+    constexpr int kDeep = kOuterDepth<RT>;
     constexpr int kU = kUBytes / 1024, kUShare = (kU + 3) / 4, kPer = 4 + kUShare;
     static_assert(kUBytes % 1024 == 0);
-    __shared__ __attribute__((aligned(16))) uint8_t vs[kOuterDepth][kTile][512];
-    __shared__ __attribute__((aligned(16))) uint8_t us[kOuterDepth][kUBytes];
+    __shared__ __attribute__((aligned(16))) uint8_t vs[kDeep][kTile][512];
+    __shared__ __attribute__((aligned(16))) uint8_t us[kDeep][kUBytes];
     __shared__ int32_t row_lds[kBatch * kTile], id_lds[kBatch + 1];
     __shared__ float back_lds[kBatch];
     const bool second = (int64_t)blockIdx.x >= a0.items;
-    const OuterArgs m = second ? a1 : a0;
+    // (field by field: a selected struct would be read from memory in the loop, and such a read waits for the copies)
+    const struct { const uint8_t *u, *v; const float* back; float *part, *d; int64_t ldv, C, col_items; int32_t div, L, R, by_column, run; } m = {
+        second ? a1.u : a0.u, second ? a1.v : a0.v, second ? a1.back : a0.back, second ? a1.part : a0.part, second ? a1.d : a0.d,
+        second ? a1.ldv : a0.ldv, second ? a1.C : a0.C, second ? a1.col_items : a0.col_items, second ? a1.div : a0.div, a0.L, a0.R,
+        second ? a1.by_column : a0.by_column, a0.run};
     const int64_t item = second ? blockIdx.x - a0.items : blockIdx.x;
     const int lane = threadIdx.x & 63, wave = uniform((int32_t)(threadIdx.x >> 6));
     const int r16 = lane & 15, q = lane >> 4;
@@ -573,7 +660,7 @@ __global__ __launch_bounds__(kThreads) void lora_outer_kernel(OuterTables tab, O
     if (threadIdx.x == 0) id_lds[count] = b0 + count < t1 ? tab.tdesc[b0 + count].x : -1;
     block_barrier();
     const auto copy_tile = [&](int i0) {
-        const int buf = i0 % kOuterDepth;
+        const int buf = i0 % kDeep;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int at = 2 * (4 * i + wave) + cr;
@@ -587,15 +674,15 @@ __global__ __launch_bounds__(kThreads) void lora_outer_kernel(OuterTables tab, O
             copy16(lds_address(&us[buf][part * 1024]), m.u + (b0 + i0) * kUBytes + part * 1024 + lane * 16);
         }
     };
-    for (int i0 = 0; i0 < count && i0 < kOuterDepth - 1; ++i0) copy_tile(i0);
+    settle();
+    for (int i0 = 0; i0 < count && i0 < kDeep - 1; ++i0) copy_tile(i0);
     for (int i0 = 0; i0 < count; ++i0) {
-        const int buf = i0 % kOuterDepth;
-        if (count - 1 - i0 >= 1) wait_copies_but<kPer>();
-        else wait_copies();
+        const int buf = i0 % kDeep;
+        wait_step<kPer, kDeep - 2>(count - 1 - i0);
         block_barrier();                                           // all waves' copies of the tile are there, the last one has been read
         const int32_t l = uniform(id_lds[i0]), after = uniform(id_lds[i0 + 1]);
         const float f = DT == FTQ_F16 ? back_lds[i0] : 1.0f;
-        if (i0 + kOuterDepth - 1 < count) copy_tile(i0 + kOuterDepth - 1);
+        if (i0 + kDeep - 1 < count) copy_tile(i0 + kDeep - 1);
         if constexpr (DT == FTQ_F32) {
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
@@ -622,7 +709,7 @@ __global__ __launch_bounds__(kThreads) void lora_outer_kernel(OuterTables tab, O
                 for (int h = 0; h < 2; ++h) {
                     const int row = 8 * q + 4 * h + (r16 >> 2), c = wave * (kCols / 4) + 16 * i + (r16 & 3) * 4;
                     const uint8_t* src = &vs[buf][row][((c >> 3) ^ swizzle(row)) * 16 + (c & 7) * 2];
-                    half[h] = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) i16x4*)src));
+                    half[h] = read_transposed(src);
                 }
                 x[i] = u32x4{half[0][0], half[0][1], half[1][0], half[1][1]};
             }
@@ -702,38 +789,6 @@ __global__ __launch_bounds__(kThreads) void lora_reduce_kernel(const int32_t* ti
     }
 }
 
-// ---- transposed copies of the weights of adapters that have pairs ---------------------
-//
-// w [L][rows][cols] -> [L][cols][rows]; tiles of 64 x 64 through LDS.
-
-struct TransposeArgs {
-    const uint8_t* w;
-    uint8_t* to;
-    int64_t rows, cols, items, per;   // per: workgroups of an adapter
-};
-
-template <int DT>
-__global__ __launch_bounds__(kThreads) void lora_transpose_kernel(const int32_t* tiles, TransposeArgs a0, TransposeArgs a1)
-{
-    using Elem = std::conditional_t<DT == FTQ_F32, uint32_t, uint16_t>;
-    __shared__ Elem lds[64][65];
-    const bool second = (int64_t)blockIdx.x >= a0.items;
-    const TransposeArgs m = second ? a1 : a0;
-    const int64_t item = second ? blockIdx.x - a0.items : blockIdx.x, l = item / m.per;
-    if (tiles[l] == tiles[l + 1]) return;
-    const int64_t ct = (m.cols + 63) / 64, tile = item - l * m.per, r0 = tile / ct * 64, c0 = tile % ct * 64;
-    const Elem* w = reinterpret_cast<const Elem*>(m.w) + l * m.rows * m.cols;
-    Elem* to = reinterpret_cast<Elem*>(m.to) + l * m.rows * m.cols;
-    const int x = threadIdx.x % 64;
-    for (int y = threadIdx.x / 64; y < 64; y += kThreads / 64) {
-        if (r0 + y < m.rows && c0 + x < m.cols) lds[y][x] = w[(r0 + y) * m.cols + c0 + x];
-    }
-    __syncthreads();
-    for (int y = threadIdx.x / 64; y < 64; y += kThreads / 64) {
-        if (c0 + y < m.cols && r0 + x < m.rows) to[(c0 + y) * m.rows + r0 + x] = lds[x][y];
-    }
-}
-
 // ---- host ---------------------------------------------------------------------------
 
 int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
@@ -761,18 +816,19 @@ int by_type(int dtype, F f)
     return f(std::integral_constant<int, FTQ_BF16>{});
 }
 
-template <int DT, int WAVES>
+template <int DT, int WAVES, bool COLS>
 int launch_shrink(const ShrinkArgs& m, int64_t grid, hipStream_t s)
 {
     const auto go = [&](auto* kernel) { return launch("lora_shrink_kernel", kernel, grid, 64 * WAVES, 0, s, m); };
     switch (rank_tiles(m.R)) {
-        case 1: return go(lora_shrink_kernel<DT, WAVES, 1>);
-        case 2: return go(lora_shrink_kernel<DT, WAVES, 2>);
-        case 4: return go(lora_shrink_kernel<DT, WAVES, 4>);
-        default: return go(lora_shrink_kernel<DT, WAVES, 8>);
+        case 1: return go(lora_shrink_kernel<DT, WAVES, 1, COLS>);
+        case 2: return go(lora_shrink_kernel<DT, WAVES, 2, COLS>);
+        case 4: return go(lora_shrink_kernel<DT, WAVES, 4, COLS>);
+        default: return go(lora_shrink_kernel<DT, WAVES, 8, COLS>);
     }
 }
 
+template <bool COLS>
 int run_shrink(int dtype, ShrinkArgs m, hipStream_t s)
 {
     const bool small = small_tiles(m.pairs, m.L, m.sorted != nullptr);
@@ -782,27 +838,28 @@ int run_shrink(int dtype, ShrinkArgs m, hipStream_t s)
     return by_type(dtype, [&](auto dt) {
         constexpr int DT = decltype(dt)::value;
         const int64_t grid = tiles * m.groups * m.splits;
-        return small ? launch_shrink<DT, 1>(m, grid, s) : launch_shrink<DT, 4>(m, grid, s);
+        return small ? launch_shrink<DT, 1, COLS>(m, grid, s) : launch_shrink<DT, 4, COLS>(m, grid, s);
     });
 }
 
-template <int DT, int OT, int BT>
+template <int DT, int OT, int BT, bool RANKS>
 int launch_expand(const ExpandArgs& m, int64_t grid, hipStream_t s)
 {
     const auto go = [&](auto* kernel) { return launch("lora_expand_kernel", kernel, grid, kThreads, 0, s, m); };
     const int rt = rank_tiles(m.R);
     if constexpr (DT == FTQ_F32) {
-        if (rt == 1) return go(lora_expand_kernel<DT, OT, BT, 1>);
-        if (rt == 2) return go(lora_expand_kernel<DT, OT, BT, 2>);
-        if (rt == 4) return go(lora_expand_kernel<DT, OT, BT, 4>);
-        return go(lora_expand_kernel<DT, OT, BT, 8>);
+        if (rt == 1) return go(lora_expand_kernel<DT, OT, BT, 1, RANKS>);
+        if (rt == 2) return go(lora_expand_kernel<DT, OT, BT, 2, RANKS>);
+        if (rt == 4) return go(lora_expand_kernel<DT, OT, BT, 4, RANKS>);
+        return go(lora_expand_kernel<DT, OT, BT, 8, RANKS>);
     } else {
-        if (rt <= 2) return go(lora_expand_kernel<DT, OT, BT, 1>);
-        if (rt == 4) return go(lora_expand_kernel<DT, OT, BT, 2>);
-        return go(lora_expand_kernel<DT, OT, BT, 4>);
+        if (rt <= 2) return go(lora_expand_kernel<DT, OT, BT, 1, RANKS>);
+        if (rt == 4) return go(lora_expand_kernel<DT, OT, BT, 2, RANKS>);
+        return go(lora_expand_kernel<DT, OT, BT, 4, RANKS>);
     }
 }
 
+template <bool RANKS>
 int run_expand(int dtype, int out_dtype, ExpandArgs m, hipStream_t s)
 {
     const bool small = small_tiles(m.pairs, m.L, m.sorted != nullptr);
@@ -813,10 +870,13 @@ int run_expand(int dtype, int out_dtype, ExpandArgs m, hipStream_t s)
     m.col_items = ceil_div(m.C, m.cols);
     const int64_t grid = tiles * m.groups * m.col_items;
     return by_type(dtype, [&](auto dt) {
-        return by_type(out_dtype, [&](auto ot) {
-            constexpr int DT = decltype(dt)::value, OT = decltype(ot)::value;
-            return small ? launch_expand<DT, OT, 1>(m, grid, s) : launch_expand<DT, OT, 4>(m, grid, s);
-        });
+        constexpr int DT = decltype(dt)::value;
+        const auto with = [&](auto ot) {
+            constexpr int OT = decltype(ot)::value;
+            return small ? launch_expand<DT, OT, 1, RANKS>(m, grid, s) : launch_expand<DT, OT, 4, RANKS>(m, grid, s);
+        };
+        if constexpr (RANKS) return with(dt);                      // d_x has the rows' type
+        else return by_type(out_dtype, with);
     });
 }
 
@@ -837,21 +897,20 @@ ForwardPlan plan_forward(int64_t L, int64_t R, int64_t K, int64_t pairs, int dty
 
 struct BackwardPlan {
     BucketPlan bucket;
-    bool gather;               // d_x row by row (rows that several pairs share)
     int64_t splits, run, runs_max;
-    int64_t off_part, off_g, off_ug, off_uh, off_backs, off_bt, off_at, off_pa, off_pb, bytes;
+    int64_t off_part, off_g, off_ug, off_uh, off_backs, off_pa, off_pb, bytes;
 };
 
-BackwardPlan plan_backward(int64_t L, int64_t R, int64_t K, int64_t N, int64_t pairs, int64_t div, int dtype)
+BackwardPlan plan_backward(int64_t L, int64_t R, int64_t K, int64_t N, int64_t pairs, int dtype)
 {
     BackwardPlan p;
     const int64_t es = size_of(dtype), rt = 16 * rank_tiles(R), pieces = dtype == FTQ_F32 ? 2 : dtype == FTQ_F16 ? 2 : 3;
     p.bucket = make_bucket_plan(pairs, L, kTile);
-    p.gather = div > 1;
     p.splits = shrink_splits(pairs, N, R, dtype);
-    // runs of tiles for about 512 workgroups an output, at most a part for every four tiles
-    const int64_t col_items = ceil_div(std::min(K, N) * es, 512), tiles = std::max<int64_t>(p.bucket.max_tiles, 1);
-    p.run = std::max<int64_t>(4, ceil_div(tiles * col_items, 512));
+    // runs of tiles for as many workgroups as fit the chip at once (by LDS two on a CU, one of high ranks), at most a part
+    // for every four tiles
+    const int64_t col_items = ceil_div(K * es, 512) + ceil_div(N * es, 512), tiles = std::max<int64_t>(p.bucket.max_tiles, 1);
+    p.run = std::max<int64_t>(4, ceil_div(tiles * col_items, R <= 64 ? 512 : 256));
     p.runs_max = ceil_div(tiles, p.run);
     int64_t off = p.bucket.bytes;
     const auto take = [&](int64_t bytes) {
@@ -864,8 +923,6 @@ BackwardPlan plan_backward(int64_t L, int64_t R, int64_t K, int64_t N, int64_t p
     p.off_ug = take(tiles * rt * kTile * 2 * pieces);
     p.off_uh = take(tiles * rt * kTile * 2 * pieces);
     p.off_backs = take(2 * tiles * 4);
-    p.off_bt = take(L * R * N * es);
-    p.off_at = take(p.gather ? 0 : L * R * K * es);
     p.off_pa = take(2 * p.runs_max * R * K * 4);
     p.off_pb = take(2 * p.runs_max * R * N * 4);
     p.bytes = off;
@@ -905,8 +962,7 @@ int64_t lora_workspace(int64_t L, int64_t R, int64_t K, int64_t, int64_t T, int6
 
 int64_t lora_backward_workspace(int64_t L, int64_t R, int64_t K, int64_t N, int64_t T, int64_t top_k, int dtype)
 {
-    // either layout of the rows: the larger of the two
-    return T == 0 ? 0 : plan_backward(L, R, K, N, T * top_k, 1, dtype).bytes;
+    return T == 0 ? 0 : plan_backward(L, R, K, N, T * top_k, dtype).bytes;
 }
 
 int lora_select_path(int64_t T, int64_t top_k) { return top_k == 1 || T * top_k <= 256 ? FTQ_PATH_GEMV : FTQ_PATH_GROUPED; }
@@ -935,7 +991,7 @@ int run_lora(const LoraArgs& m, void* ws, int path, hipStream_t s)
     shrink.L = (int32_t)m.L;
     shrink.R = (int32_t)m.R;
     shrink.splits = (int32_t)plan.splits;
-    const int st = run_shrink(m.dtype, shrink, s);
+    const int st = run_shrink<false>(m.dtype, shrink, s);
     if (st != FTQ_OK) return st;
     ExpandArgs expand{};
     expand.part = shrink.part;
@@ -953,7 +1009,7 @@ int run_lora(const LoraArgs& m, void* ws, int path, hipStream_t s)
     expand.L = shrink.L;
     expand.R = shrink.R;
     expand.splits = shrink.splits;
-    return run_expand(m.dtype, m.out_dtype, expand, s);
+    return run_expand<false>(m.dtype, m.out_dtype, expand, s);
 }
 
 int run_lora_backward(const LoraBackwardArgs& m, void* ws, hipStream_t s)
@@ -969,27 +1025,18 @@ int run_lora_backward(const LoraBackwardArgs& m, void* ws, hipStream_t s)
     };
     if (pairs == 0) return reduce(nullptr, 1, nullptr, nullptr);
     uint8_t* mem = static_cast<uint8_t*>(ws);
-    const BackwardPlan plan = plan_backward(m.L, m.R, m.K, m.N, pairs, m.act_div, m.dtype);
+    const BackwardPlan plan = plan_backward(m.L, m.R, m.K, m.N, pairs, m.dtype);
     int st = run_bucket(m.ids, m.L, plan.bucket, ws, s);
     if (st != FTQ_OK) return st;
     const OuterTables tab{reinterpret_cast<const int32_t*>(mem + plan.bucket.off_tiles), reinterpret_cast<const int32_t*>(mem + plan.bucket.off_sorted),
                           reinterpret_cast<const int4*>(mem + plan.bucket.off_tdesc)};
     const auto floats = [&](int64_t off) { return reinterpret_cast<float*>(mem + off); };
-    const bool want_g = m.d_x || m.d_a, expand_x = m.d_x && !plan.gather;
+    const bool want_g = m.d_x || m.d_a, expand_x = m.d_x && m.act_div == 1;   // else rows that several pairs share
     if (want_g) {
-        const auto args = [&](const void* w, int64_t off, int64_t rows, int64_t cols, bool wanted) {
-            const int64_t per = ceil_div(rows, 64) * ceil_div(cols, 64);
-            return TransposeArgs{static_cast<const uint8_t*>(w), mem + off, rows, cols, wanted ? m.L * per : 0, per};
-        };
-        const TransposeArgs b = args(m.b, plan.off_bt, m.N, m.R, true), a = args(m.a, plan.off_at, m.R, m.K, expand_x);
-        st = by_type(m.dtype, [&](auto dt) {
-            return launch("lora_transpose_kernel", lora_transpose_kernel<decltype(dt)::value>, b.items + a.items, kThreads, 0, s, tab.tiles, b, a);
-        });
-        if (st != FTQ_OK) return st;
         ShrinkArgs shrink{};
         shrink.v = static_cast<const uint8_t*>(m.d_out);
         shrink.ldv = m.ld_d * es;
-        shrink.w = mem + plan.off_bt;
+        shrink.w = static_cast<const uint8_t*>(m.b);
         shrink.ids = m.ids;
         shrink.sorted = tab.sorted;
         shrink.part = floats(plan.off_part);
@@ -999,7 +1046,7 @@ int run_lora_backward(const LoraBackwardArgs& m, void* ws, hipStream_t s)
         shrink.L = (int32_t)m.L;
         shrink.R = (int32_t)m.R;
         shrink.splits = (int32_t)plan.splits;
-        st = run_shrink(m.dtype, shrink, s);
+        st = run_shrink<true>(m.dtype, shrink, s);
         if (st != FTQ_OK) return st;
     }
     // the R-vectors of the outer products, and g itself
@@ -1013,7 +1060,7 @@ int run_lora_backward(const LoraBackwardArgs& m, void* ws, hipStream_t s)
     if (expand_x) {
         ExpandArgs expand{};
         expand.part = floats(plan.off_g);
-        expand.w = mem + plan.off_at;
+        expand.w = static_cast<const uint8_t*>(m.a);
         expand.ids = m.ids;
         expand.sorted = tab.sorted;
         expand.base = m.base;
@@ -1023,7 +1070,7 @@ int run_lora_backward(const LoraBackwardArgs& m, void* ws, hipStream_t s)
         expand.L = (int32_t)m.L;
         expand.R = (int32_t)m.R;
         expand.splits = 1;
-        st = run_expand(m.dtype, m.dtype, expand, s);
+        st = run_expand<true>(m.dtype, m.dtype, expand, s);
         if (st != FTQ_OK) return st;
     } else if (m.d_x) {
         GatherArgs gather{floats(plan.off_g), static_cast<const uint8_t*>(m.a), m.ids, static_cast<const uint8_t*>(m.base), static_cast<uint8_t*>(m.d_x),

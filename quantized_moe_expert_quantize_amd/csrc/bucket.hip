@@ -27,7 +27,6 @@ constexpr int kCountThreads = 256;
 constexpr int kScanThreads = 1024;
 constexpr int kScanPer = 8;                  // elements per thread and pass of the flat scan
 constexpr int kScatterWaves = 4;             // chunks per scatter workgroup (one wave each)
-constexpr int kKeyBits = 12;                 // bucket ids < 4096
 
 __device__ __forceinline__ int bucket_of(int32_t id, int32_t E) { return (id >= 0 && id < E) ? id : E; }
 
@@ -177,8 +176,27 @@ __device__ __forceinline__ void wave_lds_fence() { __builtin_amdgcn_fence(__ATOM
 constexpr int kScatterSteps = kBucketChunk / 64;
 static_assert(kBucketChunk % 64 == 0, "whole steps per chunk");
 
+// For each of STEPS steps of a wave, the lanes that hold the same bucket (-1: none) as this one: one ballot per key bit,
+// all steps at a time, so that none waits for another's.
+template <int STEPS>
+__device__ __forceinline__ void lanes_alike(const int32_t (&b)[STEPS], int bits, uint64_t (&same)[STEPS])
+{
+#pragma unroll
+    for (int st = 0; st < STEPS; ++st) same[st] = __ballot(b[st] >= 0);
+    for (int k = 0; k < bits; ++k) {
+#pragma unroll
+        for (int st = 0; st < STEPS; ++st) {
+            const int32_t bit = (b[st] << (31 - k)) >> 31;         // all ones if the bit is set
+            const uint64_t ones = __ballot(bit != 0);
+            const uint32_t lo = (uint32_t)same[st] & ~((uint32_t)ones ^ (uint32_t)bit);
+            const uint32_t hi = (uint32_t)(same[st] >> 32) & ~((uint32_t)(ones >> 32) ^ (uint32_t)bit);
+            same[st] = (uint64_t)hi << 32 | lo;
+        }
+    }
+}
+
 __global__ __launch_bounds__(64 * kScatterWaves) void bucket_scatter_kernel(
-    const int32_t* __restrict__ ids, int64_t pairs, int32_t E, int32_t nbuckets, int64_t nchunks,
+    const int32_t* __restrict__ ids, int64_t pairs, int32_t E, int32_t nbuckets, int64_t nchunks, int bits,
     const int32_t* __restrict__ bases, int32_t* __restrict__ sorted)
 {
     extern __shared__ int32_t lds_all[];         // [kScatterWaves][2][nbuckets]: counters, chunk bases
@@ -192,7 +210,7 @@ __global__ __launch_bounds__(64 * kScatterWaves) void bucket_scatter_kernel(
 #pragma unroll
     for (int st = 0; st < kScatterSteps; ++st) {
         const int64_t p = base + st * 64 + lane;
-        idv[st] = p < pairs ? ids[p] : 0;
+        idv[st] = p < pairs ? bucket_of(ids[p], E) : -1;
     }
     for (int b = lane; b < nbuckets; b += 64) {
         seen[b] = 0;
@@ -200,24 +218,17 @@ __global__ __launch_bounds__(64 * kScatterWaves) void bucket_scatter_kernel(
     }
     wave_lds_fence();
     const uint64_t below = (lane == 0) ? 0ull : (~0ull >> (64 - lane));
+    uint64_t same[kScatterSteps];
+    lanes_alike(idv, bits, same);
 #pragma unroll
     for (int st = 0; st < kScatterSteps; ++st) {
-        const int64_t p = base + st * 64 + lane;
-        const bool live = p < pairs;
-        const int32_t b = live ? bucket_of(idv[st], E) : -1;
-        // lanes holding the same bucket: agree on every key bit (and are live)
-        uint64_t same = __ballot(live);
-#pragma unroll
-        for (int k = 0; k < kKeyBits; ++k) {
-            const uint64_t ones = __ballot(live && ((b >> k) & 1));
-            same &= ((b >> k) & 1) ? ones : ~ones;
-        }
-        if (live) {
-            const int rank = __popcll(same & below);
+        const int32_t b = idv[st];
+        if (b >= 0) {
+            const int rank = __popcll(same[st] & below);
             const int32_t prev = seen[b];
-            sorted[cbase[b] + prev + rank] = (int32_t)p;
+            sorted[cbase[b] + prev + rank] = (int32_t)(base + st * 64 + lane);
             wave_lds_fence();   // every lane has read seen[] before the leaders update it
-            if (rank == 0) seen[b] = prev + __popcll(same);
+            if (rank == 0) seen[b] = prev + __popcll(same[st]);
         }
         wave_lds_fence();
     }
@@ -227,51 +238,56 @@ __global__ __launch_bounds__(64 * kScatterWaves) void bucket_scatter_kernel(
 // chunks whose counts fit in LDS: the same bucket-major counts, the same flat
 // scan and the same in-order scatter, so the same tables bit for bit, without
 // the two kernel boundaries (and their launch and memory round trips) between
-// the passes.  Wave w counts and scatters chunk w, whose ids it keeps in
-// registers; the scanned counts in LDS serve as the scatter's running bases.
-// Up to 8 chunks (8192 pairs) it measures 3-4 us faster than the three
-// kernels (10-15 us); from about 12 chunks on, the serial walk of each wave's
-// chunk makes it slower.
-constexpr int kSmallChunks = 8;
-constexpr int kSmallCounts = kScanThreads * kScanPer;   // buckets x chunks: one scan pass
+// the passes.  Wave w counts and scatters chunk w, whose buckets it keeps in
+// registers, with each pair's rank among its step's equal ones: those are found
+// once, for the counts (one LDS addition for each bucket and step, where an
+// addition for each pair would meet itself 64-fold when neighbours share a
+// bucket) and for the scatter.  The scanned counts in LDS serve as the scatter's
+// running bases.  A chunk is 64*STEPS pairs here, so that a small batch spreads over the waves too.
+constexpr int kSmallChunks = kScanThreads / 64;
+constexpr int kSmallCounts = 12288;
 constexpr int kSmallBuckets = 2048;
-constexpr int kSmallSteps = kBucketChunk / 64;
 
+template <int STEPS>
 __global__ __launch_bounds__(kScanThreads) void bucket_small_kernel(
-    const int32_t* __restrict__ ids, int64_t pairs, int32_t E, int32_t nbuckets, int32_t nchunks, int32_t tile_m,
+    const int32_t* __restrict__ ids, int64_t pairs, int32_t E, int32_t nbuckets, int32_t nchunks, int32_t tile_m, int bits,
     int32_t* __restrict__ offsets, int32_t* __restrict__ tiles, int32_t* __restrict__ sorted,
     int4* __restrict__ tdesc)
 {
-    // [nbuckets][nchunks] counts (then bases), [nbuckets + 1] offsets, [nbuckets + 1] tile offsets
+    // [nbuckets][nchunks] counts (then bases), [nbuckets + 1] offsets, [nbuckets + 1] tile offsets, [pairs] sorted pairs
     extern __shared__ int32_t lds_small[];
     int32_t* cnt = lds_small;
     int32_t* off_lds = cnt + nbuckets * nchunks;
     int32_t* tiles_lds = off_lds + nbuckets + 1;
+    uint16_t* sorted_lds = reinterpret_cast<uint16_t*>(tiles_lds + nbuckets + 1);
     __shared__ int32_t wsum[kScanWaves + 1];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int len = nbuckets * nchunks;
+    const bool mine = wave < nchunks;
+    const int64_t base = (int64_t)wave * (64 * STEPS);
+    int32_t bucket[STEPS], rank[STEPS];   // rank: lanes below with the same bucket, and their number in all << 8
+#pragma unroll
+    for (int st = 0; st < STEPS; ++st) {
+        const int64_t p = base + st * 64 + lane;
+        bucket[st] = (mine && p < pairs) ? bucket_of(ids[p], E) : -1;
+    }
     for (int i = threadIdx.x; i < len; i += kScanThreads) cnt[i] = 0;
     __syncthreads();
-    const bool mine = wave < nchunks;
-    const int64_t base = (int64_t)wave * kBucketChunk;
-    int32_t idv[kSmallSteps];
-#pragma unroll
-    for (int st = 0; st < kSmallSteps; ++st) {
-        const int64_t p = base + st * 64 + lane;
-        idv[st] = (mine && p < pairs) ? ids[p] : 0;
-    }
     if (mine) {
+        const uint64_t below = (lane == 0) ? 0ull : (~0ull >> (64 - lane));
+        uint64_t same[STEPS];
+        lanes_alike(bucket, bits, same);
 #pragma unroll
-        for (int st = 0; st < kSmallSteps; ++st) {
-            const int64_t p = base + st * 64 + lane;
-            if (p < pairs) atomicAdd(&cnt[bucket_of(idv[st], E) * nchunks + wave], 1);
+        for (int st = 0; st < STEPS; ++st) {
+            rank[st] = __popcll(same[st] & below) | __popcll(same[st]) << 8;
+            if (bucket[st] >= 0 && (rank[st] & 255) == 0) atomicAdd(&cnt[bucket[st] * nchunks + wave], rank[st] >> 8);
         }
     }
     __syncthreads();
-    // flat exclusive scan of the counts in place (len <= kSmallCounts: one pass)
+    // flat exclusive scan of the counts in place
     int32_t carry = 0;
-    {
-        const int i0 = threadIdx.x * kScanPer;
+    for (int b0 = 0; b0 < len; b0 += kScanThreads * kScanPer) {
+        const int i0 = b0 + threadIdx.x * kScanPer;
         int32_t v[kScanPer];
         int32_t local = 0;
 #pragma unroll
@@ -298,30 +314,21 @@ __global__ __launch_bounds__(kScanThreads) void bucket_small_kernel(
     __syncthreads();
     write_tables(nbuckets, tile_m, off_lds, tiles_lds, wsum, offsets, tiles, tdesc);
     // scatter: chunk `wave` in pair order, 64 pairs per step (as bucket_scatter_kernel);
-    // cnt[b][wave] is bucket b's next slot for this chunk
-    if (!mine) return;   // no barrier follows
-    const uint64_t below = (lane == 0) ? 0ull : (~0ull >> (64 - lane));
+    // cnt[b][wave] is bucket b's next slot for this chunk.  Into LDS, and from there in order:
+    // one CU makes a scattered store of a wave no faster than a lane a cycle.
 #pragma unroll
-    for (int st = 0; st < kSmallSteps; ++st) {
-        const int64_t p = base + st * 64 + lane;
-        const bool live = p < pairs;
-        const int32_t b = live ? bucket_of(idv[st], E) : -1;
-        uint64_t same = __ballot(live);
-#pragma unroll
-        for (int k = 0; k < kKeyBits; ++k) {
-            const uint64_t ones = __ballot(live && ((b >> k) & 1));
-            same &= ((b >> k) & 1) ? ones : ~ones;
-        }
-        if (live) {
-            const int rank = __popcll(same & below);
-            int32_t* next = &cnt[b * nchunks + wave];
+    for (int st = 0; st < STEPS; ++st) {
+        if (bucket[st] >= 0) {
+            int32_t* next = &cnt[bucket[st] * nchunks + wave];
             const int32_t at = *next;
-            sorted[at + rank] = (int32_t)p;
             wave_lds_fence();   // every lane has read its counter before the leaders update it
-            if (rank == 0) *next = at + __popcll(same);
+            if ((rank[st] & 255) == 0) *next = at + (rank[st] >> 8);
+            sorted_lds[at + (rank[st] & 255)] = (uint16_t)(base + st * 64 + lane);
         }
         wave_lds_fence();
     }
+    __syncthreads();
+    for (int i = threadIdx.x; i < pairs; i += kScanThreads) sorted[i] = sorted_lds[i];
 }
 
 }  // namespace
@@ -356,11 +363,23 @@ int run_bucket(const int32_t* ids, int64_t E, const BucketPlan& plan, void* ws, 
     int32_t* sorted = reinterpret_cast<int32_t*>(base + plan.off_sorted);
     int4* tdesc = reinterpret_cast<int4*>(base + plan.off_tdesc);
     const int32_t nb = (int32_t)plan.buckets;
-    if (plan.chunks <= kSmallChunks && (int64_t)nb * plan.chunks <= kSmallCounts && nb <= kSmallBuckets &&
-        !route_split_forced()) {
-        const size_t lds = sizeof(int32_t) * ((size_t)nb * plan.chunks + 2 * ((size_t)nb + 1));
-        return launch("bucket_small_kernel", bucket_small_kernel, 1, kScanThreads, lds, s, ids, plan.pairs, (int32_t)E,
-                      nb, (int32_t)plan.chunks, (int32_t)plan.tile_m, offsets, tiles, sorted, tdesc);
+    int bits = 0;
+    while ((plan.buckets - 1) >> bits) ++bits;
+    if (plan.pairs <= kSmallChunks * kBucketChunk && nb <= kSmallBuckets && !route_split_forced()) {
+        // the shortest chunks that the waves and the counts in LDS allow
+        int64_t steps = 1;
+        while ((plan.pairs + 64 * steps - 1) / (64 * steps) > std::min<int64_t>(kSmallChunks, std::max(1, kSmallCounts / nb))) steps *= 2;
+        const int32_t chunks = (int32_t)((plan.pairs + 64 * steps - 1) / (64 * steps));
+        const size_t lds = sizeof(int32_t) * ((size_t)nb * chunks + 2 * ((size_t)nb + 1)) + sizeof(uint16_t) * (size_t)plan.pairs;
+        const auto go = [&](auto* kernel) {
+            return launch("bucket_small_kernel", kernel, 1, kScanThreads, lds, s, ids, plan.pairs, (int32_t)E, nb, chunks,
+                          (int32_t)plan.tile_m, bits, offsets, tiles, sorted, tdesc);
+        };
+        if (steps == 1) return go(bucket_small_kernel<1>);
+        if (steps == 2) return go(bucket_small_kernel<2>);
+        if (steps == 4) return go(bucket_small_kernel<4>);
+        if (steps == 8) return go(bucket_small_kernel<8>);
+        if (steps == 16) return go(bucket_small_kernel<16>);
     }
     int st = launch("bucket_count_kernel", bucket_count_kernel, plan.chunks, kCountThreads,
                     sizeof(int32_t) * nb, s, ids, plan.pairs, (int32_t)E, nb, plan.chunks, counts);
@@ -370,7 +389,7 @@ int run_bucket(const int32_t* ids, int64_t E, const BucketPlan& plan, void* ws, 
     if (st != FTQ_OK) return st;
     return launch("bucket_scatter_kernel", bucket_scatter_kernel, (plan.chunks + kScatterWaves - 1) / kScatterWaves,
                   64 * kScatterWaves, sizeof(int32_t) * 2 * kScatterWaves * nb, s, ids, plan.pairs, (int32_t)E, nb,
-                  plan.chunks, static_cast<const int32_t*>(counts), sorted);
+                  plan.chunks, bits, static_cast<const int32_t*>(counts), sorted);
 }
 
 }  // namespace ftq

@@ -101,6 +101,38 @@ __device__ __forceinline__ int middle_exponent(float size)
     return min(max(e, -110), 110);
 }
 
+// ---- tiles of pairs --------------------------------------------------------------
+//
+// Without tables a tile is BM pairs in their order, of whatever adapters.  With the tables of
+// pairs sorted by adapter (bucket.hip) it is `span` table tiles in a row, each of one adapter.
+
+struct TileList {
+    const int32_t* sorted;     // or null: no tables
+    const int4* tdesc;         // per table tile {adapter (L: none), first slot, pairs, 0}
+    const int32_t* count;      // number of table tiles
+    int32_t span;
+    int32_t rows;              // pairs of a tile at most
+    int64_t most;              // tiles at most
+};
+
+// First slot and pairs of tile i (no pairs behind the last tile).
+template <int BM>
+__device__ __forceinline__ void find_tile(const TileList& t, int64_t i, int64_t pairs, int64_t& slot0, int& rows)
+{
+    if (!t.sorted) {
+        slot0 = i * BM;
+        rows = (int)min((int64_t)BM, pairs - slot0);
+        return;
+    }
+    const int64_t n = uniform(*t.count), t0 = i * t.span;
+    slot0 = 0;
+    rows = 0;
+    if (t0 >= n) return;
+    const int4 d0 = t.tdesc[t0], d1 = t.tdesc[min(t0 + t.span, n) - 1];
+    slot0 = uniform(d0.y);
+    rows = uniform(d1.y) + uniform(d1.z) - uniform(d0.y);
+}
+
 // ---- shrink: z[p] = W_l v[row of p] ---------------------------------------------
 
 struct ShrinkArgs {
@@ -108,7 +140,7 @@ struct ShrinkArgs {
     int64_t ldv;               // bytes from row to row
     const uint8_t* w;          // [L][R][C], or [L][C][R] (by_column)
     const int32_t* ids;        // [pairs]
-    const int32_t* sorted;     // [pairs] or null: pairs in the order of tiles
+    TileList tiles;
     float* part;               // [splits][pairs][R]
     int64_t pairs, row_bytes;  // bytes of C elements
     int32_t div, L, R;
@@ -139,12 +171,14 @@ __global__ __launch_bounds__(64 * WAVES) void lora_shrink_kernel(ShrinkArgs m)
     const int r16 = lane & 15, q = lane >> 4;
     const int64_t item = blockIdx.x, at = item / m.splits;
     const int ks = (int)(item - at * m.splits), g = (int)(at % m.groups);
-    const int64_t slot0 = at / m.groups * BM;
-    const int rows = (int)min((int64_t)BM, m.pairs - slot0);
+    int64_t slot0;
+    int rows;
+    find_tile<BM>(m.tiles, at / m.groups, m.pairs, slot0, rows);
+    if (rows == 0) return;
     // lane i: row i of the tile
     int32_t pair = 0, id = -1;
     if (lane < rows) {
-        pair = m.sorted ? m.sorted[slot0 + lane] : (int32_t)(slot0 + lane);
+        pair = m.tiles.sorted ? m.tiles.sorted[slot0 + lane] : (int32_t)(slot0 + lane);
         id = m.ids[pair];
         if (!adapter_ok(id, m.L)) id = -1;
     }
@@ -152,7 +186,11 @@ __global__ __launch_bounds__(64 * WAVES) void lora_shrink_kernel(ShrinkArgs m)
     const int cr = lane >> 3, run = (lane & 7) ^ cr;               // row of eight and 16-byte run that this lane copies
     const uint8_t* xsrc[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) xsrc[i] = m.v + (int64_t)(__shfl(pair, min((wave * 2 + i) * 8 + cr, rows - 1)) / m.div) * m.ldv;
+    for (int i = 0; i < 2; ++i) {
+        const int row = (wave * 2 + i) * 8 + cr;
+        xsrc[i] = m.v + (int64_t)(__shfl(pair, min(row, rows - 1)) / m.div) * m.ldv;
+        if (row >= rows) xsrc[i] = nullptr;
+    }
     const int64_t total = (m.row_bytes + kLine - 1) / kLine, first = (int64_t)ks * m.steps, columns = m.row_bytes / kSize<DT>;
     const int n = (int)max((int64_t)0, min((int64_t)m.steps, total - first));
     const int32_t my_pair = __shfl(pair, wave * 16 + r16);
@@ -182,7 +220,7 @@ __global__ __launch_bounds__(64 * WAVES) void lora_shrink_kernel(ShrinkArgs m)
             const uint8_t* none = reinterpret_cast<const uint8_t*>(&kZeros);
             const int buf = s % kDepth;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) copy16(lds_address(&xs[buf][(wave * 2 + i) * 8][0]), in ? xsrc[i] + byte : none);
+            for (int i = 0; i < 2; ++i) copy16(lds_address(&xs[buf][(wave * 2 + i) * 8][0]), in && xsrc[i] ? xsrc[i] + byte : none);
 #pragma unroll
             for (int i = 0; i < kShare; ++i) {
                 const uint8_t* src = in ? wsrc[i] + byte : none;
@@ -248,14 +286,14 @@ struct ExpandArgs {
     const uint8_t* w;          // [L][C][R], or [L][R][C] (by rank)
     const float* scale;        // [L] or null
     const int32_t* ids;
-    const int32_t* sorted;     // or null
+    TileList tiles;
     const void* base;          // or null
     void* out;
     float* h;                  // [pairs][R] or null: the sum of the parts
     int64_t ld_base, ld_out, pairs, C;
     int32_t L, R, splits, groups;
     int64_t col_items;         // workgroups along the columns
-    int32_t cols;              // columns of a workgroup, a multiple of 256
+    int32_t cols;              // columns of a workgroup, whole steps
 };
 
 template <int DT> __device__ __forceinline__ float load1(const void* p, int64_t i)
@@ -290,152 +328,262 @@ __device__ __forceinline__ void add_and_store(void* out, int64_t i, u32x4 base, 
     }
 }
 
-// A workgroup takes 16*BT rows and m.cols columns, a wave 64 of every 256.  W is the left
-// operand, so that a lane holds four columns of one row; which row of a 16-row tile is
-// which column is free and chosen so that a lane's results are whole 16-byte stores and
-// the four lanes of a row 64 bytes side by side: 32-bit results, row r of tile i is column
-// 16*i + r; 16-bit ones, column 32*(i/2) + 8*(r/4) + 4*(i%2) + r%4.
-// KST: 64-byte steps of an R-vector.  RANKS: the weights lie by rank, [R][C]; a lane then
-// loads its values one by one, 16 lanes neighbouring columns (they are few beside base and out).
-template <int DT, int OT, int BT, int KST, bool RANKS>
+// The value of the lane beside this one (0 and 1, 2 and 3, ...).
+__device__ __forceinline__ float swap_pair(float v)
+{
+    const int i = __builtin_bit_cast(int, v);
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(i, i, 0xB1, 0xF, 0xF, false));   // quad_perm 1 0 3 2
+}
+
+// A wave takes 16 pairs, whose R-vectors it holds in registers as operands, and streams 64
+// columns at a time: base (the next columns' is on its way), results, and the weights.  WR == 4:
+// the waves of a workgroup have 16 pairs each and the same columns, whose weights they bring
+// into LDS in the order they lie, a step ahead in registers.  WR == 1: the same 16 pairs and 64
+// columns of 256 each, and every wave loads its weights as operands: for few pairs, which
+// cost time by the length of their chain of loads.  (Weights loaded so by each wave of many, a column a lane, took as many
+// address cycles as base and results together: 34 to 46 us where a copy of the same rows takes 21.)
+// W is the left operand, so that a lane holds four columns of one row; which row of a 16-row tile is
+// which column is free and chosen so that a lane's results are whole 16-byte runs and
+// the four lanes of a row have 64 bytes side by side: 32-bit results, row r of tile i is column
+// 16*i + r; 16-bit ones, column 32*(i/2) + 8*(r/4) + 4*(i%2) + r%4.  Lanes of neighbouring
+// rows then trade a run each, so that eight lanes read and write the 128 bytes of a line of one row.
+// KST: 64-byte steps of an R-vector.  RANKS: the weights lie by rank, [R][C], also in LDS, and
+// 16-bit ones are read by transposing reads of four ranks x 16 columns.
+template <int DT, int OT, int KST, bool RANKS, int WR>
 __global__ __launch_bounds__(kThreads) void lora_expand_kernel(ExpandArgs m)
 {
-    constexpr int BM = 16 * BT, kElems = 64 / kSize<DT>;           // elements of a step
-    constexpr int kRank = KST * kElems, kQuads = kRank / 4;        // R rounded up
-    constexpr int kPad = KST > 1 ? 16 / kSize<DT> : 0;             // rows of 64 bytes meet no bank twice, longer ones are set apart
+    constexpr int kElems = 64 / kSize<DT>, kOwn = 16 / kSize<DT>;  // ranks of a step, and a lane's of them
     constexpr bool kWide = OT == FTQ_F32;
-    constexpr int kRun = kWide ? 4 : 8, kLoads = 64 / (4 * kRun);  // columns of a lane's store, stores of a row and wave
-    static_assert((kQuads & (kQuads - 1)) == 0 && kQuads <= 64);
-    using Elem = std::conditional_t<DT == FTQ_F32, float, uint16_t>;
-    __shared__ __attribute__((aligned(16))) Elem zs[kPieces<DT>][BM][kRank + kPad];
-    __shared__ float back[BM];                                     // 2^e of a row's pieces
-    __shared__ int32_t pair_lds[BM], id_lds[BM];
-    const int lane = threadIdx.x & 63, wave = uniform((int32_t)(threadIdx.x >> 6));
-    const int r16 = lane & 15, q = lane >> 4;
+    constexpr int kRun = kWide ? 4 : 8, kLines = 64 / (8 * kRun);  // columns of a lane's store, 128-byte lines of a row and wave
+    constexpr int BM = 16 * WR, kCols = 256 / WR;                  // pairs of a workgroup, columns of its step
+    // LDS rows: a column's ranks or a rank's columns, set apart by 16 bytes where they would meet the same banks
+    constexpr int kRow = RANKS ? kCols * kSize<DT> : 64 * KST, kPitch = kRow + (RANKS || KST > 1 ? 16 : 0);
+    constexpr int kRowsLds = RANKS ? kElems * KST : kCols;
+    constexpr int kUnits = kRow / 16 * kRowsLds / kThreads;        // 16-byte runs of a thread
+    static_assert(kRow / 16 * kRowsLds % kThreads == 0);
+    constexpr bool kLds = WR == 4;
+    __shared__ __attribute__((aligned(16))) uint8_t wl[kLds ? kRowsLds * kPitch : 16];
+    const int lane = threadIdx.x & 63, wave = uniform((int32_t)(threadIdx.x >> 6)), r16 = lane & 15, q = lane >> 4;
+    const bool odd = r16 & 1;
     const int64_t item = blockIdx.x, at = item / m.col_items;
-    const int64_t c_first = (item - at * m.col_items) * m.cols;
+    const int64_t c_first = (item - at * m.col_items) * m.cols, c_end = min(c_first + m.cols, m.C);
     const int g = (int)(at % m.groups);
-    const int64_t slot0 = at / m.groups * BM;
-    const int rows = (int)min((int64_t)BM, m.pairs - slot0);
-    int32_t pair = 0, id = INT32_MIN;                              // rows that are not there
+    int64_t slot0;
+    int rows;
+    find_tile<BM>(m.tiles, at / m.groups, m.pairs, slot0, rows);
+    if (rows == 0) return;
+    // lane i: row i of the tile
+    int32_t tile_pair = 0, tile_id = INT32_MIN;                    // rows that are not there
     if (lane < rows) {
-        pair = m.sorted ? m.sorted[slot0 + lane] : (int32_t)(slot0 + lane);
-        id = m.ids[pair];
-        if (!adapter_ok(id, m.L)) id = -1;
+        tile_pair = m.tiles.sorted ? m.tiles.sorted[slot0 + lane] : (int32_t)(slot0 + lane);
+        tile_id = m.ids[tile_pair];
+        if (!adapter_ok(tile_id, m.L)) tile_id = -1;
     }
-    if (wave == 0 && lane < BM) {
-        pair_lds[lane] = pair;
-        id_lds[lane] = id;
-    }
-    uint64_t todo = __ballot(id != INT32_MIN);
-    int32_t pair_of[BT];
+    const int row0 = WR == 1 ? 0 : 16 * wave, col0 = WR == 1 ? 64 * wave : 0;   // of this wave
+    const int32_t pair = __shfl(tile_pair, row0 + r16);
+    // this lane's row and its neighbour's, the even one first
+    const uint8_t* from[2];
+    uint8_t* to[2];
 #pragma unroll
-    for (int b = 0; b < BT; ++b) pair_of[b] = __shfl(pair, 16 * b + r16);
+    for (int z = 0; z < 2; ++z) {
+        const int64_t p = __shfl(tile_pair, row0 + (r16 & 14) + z);
+        from[z] = static_cast<const uint8_t*>(m.base) + (p * m.ld_base + col0 + odd * 4 * kRun + q * kRun) * kSize<OT>;
+        to[z] = static_cast<uint8_t*>(m.out) + (p * m.ld_out + col0 + odd * 4 * kRun + q * kRun) * kSize<OT>;
+    }
+    // runs of the weights that this thread brings: of rank or column `row` the run `part`; ranks from R on stay zero
+    const int per_row = RANKS ? kRow / 16 : m.R * kSize<DT> / 16, have = RANKS ? m.R * per_row : kCols * per_row;
+    int row_of[kUnits], part_of[kUnits];
+#pragma unroll
+    for (int i = 0; i < kUnits && kLds; ++i) {
+        const int u = i * kThreads + threadIdx.x;
+        row_of[i] = u < have ? u / per_row : INT32_MAX;
+        part_of[i] = u % per_row;
+    }
+    if (kLds && have < kUnits * kThreads) {
+        for (int i = threadIdx.x; i < kRowsLds * kPitch / 16; i += kThreads) *reinterpret_cast<u32x4*>(wl + 16 * i) = u32x4{0u, 0u, 0u, 0u};
+    }
+    uint64_t todo = __ballot(tile_id != INT32_MIN);
     for (int index = 0; todo; ++index) {
-        const int32_t l = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
-        const uint64_t mine = __ballot(id == l);
-        todo &= ~mine;
+        const int32_t l = __builtin_amdgcn_readlane(tile_id, __builtin_ctzll(todo));
+        const uint64_t all = __ballot(tile_id == l);
+        todo &= ~all;
         if (index % m.groups != g) continue;
-        block_barrier();                                           // pair_lds is written, the last adapter's zs read
-        const float scale = l >= 0 && m.scale ? m.scale[l] : 1.0f;
-        for (int i = threadIdx.x; i < BM * kQuads; i += kThreads) {
-            const int row = i / kQuads, r = i % kQuads * 4;
-            const bool own = id_lds[row] == l && r < m.R;
-            f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};
-            if (own) {
-                const int64_t o = (int64_t)pair_lds[row] * m.R + r;
-                if (l >= 0) {
-                    for (int k = 0; k < m.splits; ++k) z += *reinterpret_cast<const f32x4*>(m.part + k * m.pairs * m.R + o);
-                }
-                if (m.h && c_first == 0) *reinterpret_cast<f32x4*>(m.h + o) = z;
-                z *= scale;
-            }
-            if constexpr (DT == FTQ_F32) {
-                *reinterpret_cast<f32x4*>(&zs[0][row][r]) = z;
-            } else {
-                if constexpr (DT == FTQ_F16) {
-                    float size = 0.0f;
+        const uint32_t mine = (uint32_t)(all >> row0) & 0xffff;    // of this wave's rows
+        const bool own[2] = {(mine >> (r16 & 14) & 1) != 0, (mine >> (r16 | 1) & 1) != 0};
+        // line t: the even lanes of a pair take its first half, the odd ones its second, of the even row, then the odd one
+        const auto there = [&](int64_t c0, int t) { return c0 + col0 + (2 * t + odd) * 4 * kRun + q * kRun < c_end; };
+        const auto load_base = [&](int64_t c0, u32x4 (&b)[kLines][2]) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) size = fmaxf(size, __builtin_fabsf(z[e]));
+            for (int t = 0; t < kLines; ++t) {
 #pragma unroll
-                    for (int o = 1; o < kQuads; o <<= 1) size = fmaxf(size, __shfl_xor(size, o));
-                    const int e2 = middle_exponent(size);
-                    z *= __builtin_ldexpf(1.0f, -e2);
-                    if (r == 0) back[row] = __builtin_ldexpf(1.0f, e2);
-                }
-#pragma unroll
-                for (int c = 0; c < kPieces<DT>; ++c) {
-                    u16x4 p;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float v = z[e];
-                        p[e] = take_piece<DT>(v);
-                        z[e] = v;
-                    }
-                    *reinterpret_cast<u16x4*>(&zs[c][row][r]) = p;
+                for (int z = 0; z < 2; ++z) {
+                    if (m.base && own[z] && there(c0, t)) b[t][z] = *reinterpret_cast<const u32x4*>(from[z] + (c0 + t * 8 * kRun) * kSize<OT>);
                 }
             }
-        }
-        block_barrier();
-        for (int64_t c0 = c_first + wave * 64; c0 < min(c_first + m.cols, m.C); c0 += 256) {
-            u32x4 w[4][KST] = {}, base[BT][kLoads] = {};
-            if (l >= 0) {
+        };
+        const auto column = [&](int i) { return col0 + (kWide ? 16 * i + r16 : 32 * (i / 2) + 8 * (r16 / 4) + 4 * (i % 2) + r16 % 4); };   // of a weight tile's row
+        u32x4 ahead[kLds ? kUnits : 4 * KST] = {};
+        const auto load_weights = [&](int64_t c0) {
+            if (l < 0) return;
+            if constexpr (!kLds) {                                 // each lane its own operand
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int c = kWide ? 16 * i + r16 : 32 * (i / 2) + 8 * (r16 / 4) + 4 * (i % 2) + r16 % 4;
-                    const int64_t col = min(c0 + c, m.C - 1);
+                    const int64_t c = min(c0 + column(i), m.C - 1);
 #pragma unroll
                     for (int k = 0; k < KST; ++k) {
-                        const int r = k * kElems + q * (16 / kSize<DT>);
+                        const int r = k * kElems + q * kOwn;
                         if (r >= m.R) continue;                    // (R is a multiple of 8: all of a lane's ranks are there or none)
                         if constexpr (RANKS) {
                             using Bits = std::conditional_t<DT == FTQ_F32, uint32_t, uint16_t>;
-                            const Bits* src = reinterpret_cast<const Bits*>(m.w) + ((int64_t)l * m.R + r) * m.C + col;
+                            const Bits* src = reinterpret_cast<const Bits*>(m.w) + ((int64_t)l * m.R + r) * m.C + c;
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
-                                if constexpr (DT == FTQ_F32) w[i][k][e] = src[e * m.C];
-                                else w[i][k][e] = src[2 * e * m.C] | (uint32_t)src[(2 * e + 1) * m.C] << 16;
+                                if constexpr (DT == FTQ_F32) ahead[i * KST + k][e] = src[e * m.C];
+                                else ahead[i * KST + k][e] = src[2 * e * m.C] | (uint32_t)src[(2 * e + 1) * m.C] << 16;
                             }
                         } else {
-                            w[i][k] = *reinterpret_cast<const u32x4*>(m.w + (((int64_t)l * m.C + col) * m.R + r) * kSize<DT>);
+                            ahead[i * KST + k] = *reinterpret_cast<const u32x4*>(m.w + (((int64_t)l * m.C + c) * m.R + r) * kSize<DT>);
+                        }
+                    }
+                }
+                return;
+            }
+#pragma unroll
+            for (int i = 0; i < (kLds ? kUnits : 0); ++i) {
+                if constexpr (RANKS) {
+                    if (row_of[i] < m.R && c0 + part_of[i] * kOwn < m.C)
+                        ahead[i] = *reinterpret_cast<const u32x4*>(m.w + (((int64_t)l * m.R + row_of[i]) * m.C + c0) * kSize<DT> + part_of[i] * 16);
+                } else {
+                    if (row_of[i] < m.C - c0) ahead[i] = *reinterpret_cast<const u32x4*>(m.w + (((int64_t)l * m.C + c0 + row_of[i]) * m.R) * kSize<DT> + part_of[i] * 16);
+                }
+            }
+        };
+        u32x4 base[kLines][2] = {}, base_next[kLines][2] = {};
+        load_weights(c_first);
+        load_base(c_first, base);
+        // the R-vectors of this adapter's rows (zeros for others) as operands
+        u32x4 z[KST][kPieces<DT>];
+        float f = 1.0f;                                            // 2^e of this row's pieces
+        {
+            const float scale = l >= 0 && m.scale ? m.scale[l] : 1.0f;
+            const bool take = mine >> r16 & 1;
+            f32x4 v[KST][kOwn / 4];
+            float size = 0.0f;
+#pragma unroll
+            for (int k = 0; k < KST; ++k) {
+#pragma unroll
+                for (int h = 0; h < kOwn / 4; ++h) {
+                    const int r = k * kElems + q * kOwn + 4 * h;
+                    v[k][h] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                    if (take && r < m.R) {
+                        const int64_t o = (int64_t)pair * m.R + r;
+                        if (l >= 0) {
+#pragma unroll(WR == 1 ? 8 : 1)
+                            for (int i = 0; i < m.splits; ++i) v[k][h] += *reinterpret_cast<const f32x4*>(m.part + i * m.pairs * m.R + o);
+                        }
+                        if (m.h && c_first == 0 && (WR == 4 || wave == 0)) *reinterpret_cast<f32x4*>(m.h + o) = v[k][h];
+                        v[k][h] *= scale;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) size = fmaxf(size, __builtin_fabsf(v[k][h][e]));
+                }
+            }
+            if constexpr (DT == FTQ_F16) {
+                size = fmaxf(size, __shfl_xor(size, 16));
+                size = fmaxf(size, __shfl_xor(size, 32));
+                const int e2 = middle_exponent(size);
+                const float to_middle = __builtin_ldexpf(1.0f, -e2);
+                f = __builtin_ldexpf(1.0f, e2);
+#pragma unroll
+                for (int k = 0; k < KST; ++k) {
+#pragma unroll
+                    for (int h = 0; h < kOwn / 4; ++h) v[k][h] *= to_middle;
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < KST; ++k) {
+                if constexpr (DT == FTQ_F32) {
+                    z[k][0] = __builtin_bit_cast(u32x4, v[k][0]);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < kPieces<DT>; ++c) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            float lo = v[k][e / 2][e % 2 * 2], hi = v[k][e / 2][e % 2 * 2 + 1];
+                            const uint32_t piece = take_piece<DT>(lo);
+                            z[k][c][e] = piece | (uint32_t)take_piece<DT>(hi) << 16;
+                            v[k][e / 2][e % 2 * 2] = lo;
+                            v[k][e / 2][e % 2 * 2 + 1] = hi;
                         }
                     }
                 }
             }
-            if (m.base) {
+        }
+        for (int64_t c0 = c_first; c0 < c_end; c0 += kCols) {
+            if constexpr (kLds) {
+                block_barrier();                                   // the last step's weights have been read
 #pragma unroll
-                for (int b = 0; b < BT; ++b) {
-                    const bool own = mine >> (16 * b + r16) & 1;
-#pragma unroll
-                    for (int t = 0; t < kLoads; ++t) {
-                        const int64_t c = c0 + t * 4 * kRun + q * kRun;
-                        if (own && c < m.C) base[b][t] = *reinterpret_cast<const u32x4*>(static_cast<const uint8_t*>(m.base) + (pair_of[b] * m.ld_base + c) * kSize<OT>);
-                    }
+                for (int i = 0; i < kUnits; ++i) {
+                    if (row_of[i] != INT32_MAX) *reinterpret_cast<u32x4*>(wl + row_of[i] * kPitch + part_of[i] * 16) = ahead[i];
                 }
+                if (c0 + kCols < c_end) load_weights(c0 + kCols);
             }
-#pragma unroll
-            for (int b = 0; b < BT; ++b) {
+            if (c0 + kCols < c_end) load_base(c0 + kCols, base_next);
+            if constexpr (kLds) block_barrier();
+            if (mine && c0 + col0 < c_end && (l >= 0 || m.base != m.out)) {   // (in place, rows without an adapter stay as they are)
                 f32x4 acc[4] = {};
 #pragma unroll
                 for (int k = 0; k < KST; ++k) {
+                    if (l < 0) continue;                           // no adapter, no weights: what LDS holds may be anything
 #pragma unroll
-                    for (int c = 0; c < kPieces<DT>; ++c) {
-                        const u32x4 z = *reinterpret_cast<const u32x4*>(&zs[c][16 * b + r16][k * kElems + q * (16 / kSize<DT>)]);
+                    for (int i = 0; i < 4; ++i) {
+                        u32x4 w;
+                        if constexpr (!kLds) {
+                            w = ahead[i * KST + k];
+                        } else if constexpr (!RANKS || DT == FTQ_F32) {
+                            const int c = column(i);
+                            if constexpr (!RANKS) {
+                                w = *reinterpret_cast<const u32x4*>(wl + c * kPitch + k * 64 + q * 16);
+                            } else {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) acc[i] = multiply<DT>(w[i][k], z, acc[i]);
+                                for (int e = 0; e < 4; ++e) w[e] = *reinterpret_cast<const uint32_t*>(wl + (k * kElems + 4 * q + e) * kPitch + c * 4);
+                            }
+                        } else {
+                            // columns four by four, as lanes 4j .. 4j+3 of a result hold them
+                            const int c = col0 + (kWide ? 16 * i + 4 * (r16 & 3) : 32 * (i / 2) + 8 * (r16 & 3) + 4 * (i % 2));
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const u32x2 t = read_transposed(wl + (k * kElems + 8 * q + 4 * h + (r16 >> 2)) * kPitch + c * 2);
+                                w[2 * h] = t[0];
+                                w[2 * h + 1] = t[1];
+                            }
+                        }
+#pragma unroll
+                        for (int c = 0; c < kPieces<DT>; ++c) acc[i] = multiply<DT>(w, z[k][c], acc[i]);
                     }
                 }
-                if (!(mine >> (16 * b + r16) & 1)) continue;
-                if (l < 0 && m.base == m.out) continue;            // in place: rows without an adapter stay as they are
-                const float f = DT == FTQ_F16 ? back[16 * b + r16] : 1.0f;
 #pragma unroll
-                for (int t = 0; t < kLoads; ++t) {
-                    const int64_t c = c0 + t * 4 * kRun + q * kRun;
-                    float v[kRun];
+                for (int t = 0; t < kLines; ++t) {
+                    float v[2][kRun];                              // of the even row, of the odd one
 #pragma unroll
-                    for (int e = 0; e < kRun; ++e) v[e] = kWide ? acc[t][e % 4] * f : acc[(2 * t + e / 4) & 3][e % 4] * f;
-                    if (c < m.C) add_and_store<OT>(m.out, pair_of[b] * m.ld_out + c, base[b][t], v);
+                    for (int e = 0; e < kRun; ++e) {
+                        const float first = (kWide ? acc[2 * t][e % 4] : acc[e / 4][e % 4]) * f;
+                        const float second = (kWide ? acc[2 * t + 1][e % 4] : acc[2 + e / 4][e % 4]) * f;
+                        const float got = swap_pair(odd ? first : second);
+                        v[0][e] = odd ? got : first;
+                        v[1][e] = odd ? second : got;
+                    }
+#pragma unroll
+                    for (int z2 = 0; z2 < 2; ++z2) {
+                        if (own[z2] && there(c0, t)) add_and_store<OT>(to[z2] + (c0 + t * 8 * kRun) * kSize<OT>, 0, base[t][z2], v[z2]);
+                    }
                 }
+            }
+            if (!kLds && c0 + kCols < c_end) load_weights(c0 + kCols);
+#pragma unroll
+            for (int t = 0; t < kLines; ++t) {
+#pragma unroll
+                for (int z2 = 0; z2 < 2; ++z2) base[t][z2] = base_next[t][z2];
             }
         }
     }
@@ -546,6 +694,7 @@ __global__ __launch_bounds__(kThreads) void lora_pieces_kernel(OuterTables tab, 
         const int r = (q0 + 8 * i) * 4;
         if (have && r < m.R) {
             if (!none) {
+#pragma unroll 4
                 for (int k = 0; k < m.splits; ++k) z[i] += *reinterpret_cast<const f32x4*>(m.part + (k * m.pairs + p) * m.R + r);
             }
             z[i] *= scale;
@@ -804,8 +953,24 @@ int64_t shrink_splits(int64_t pairs, int64_t C, int64_t R, int dtype)
     return std::max<int64_t>(1, std::min({want, int64_t(16), steps / 2}));
 }
 
-// 16 rows a tile, or 64: few pairs, or few of an adapter side by side.
-bool small_tiles(int64_t pairs, int64_t L, bool sorted) { return pairs <= 256 || (sorted && pairs / L < 32); }
+// Pairs of an adapter side by side that a table tile takes, by the average.
+int64_t table_tile(int64_t pairs, int64_t L) { return pairs / L >= 48 ? 64 : pairs / L >= 12 ? 32 : 16; }
+
+// Few pairs in their order: tiles of 16, whose adapters several workgroups share.
+bool few(int64_t pairs) { return pairs <= 256; }
+
+TileList in_order(int64_t pairs)
+{
+    const int32_t rows = few(pairs) ? 16 : 64;
+    return TileList{nullptr, nullptr, nullptr, 1, rows, ceil_div(pairs, rows)};
+}
+
+TileList from_tables(const BucketPlan& plan, const uint8_t* mem, int64_t L, int64_t span)
+{
+    return TileList{reinterpret_cast<const int32_t*>(mem + plan.off_sorted), reinterpret_cast<const int4*>(mem + plan.off_tdesc),
+                    reinterpret_cast<const int32_t*>(mem + plan.off_tiles) + L + 1, (int32_t)span, (int32_t)(plan.tile_m * span),
+                    ceil_div(plan.max_tiles, span)};
+}
 
 // Calls f(type constant).
 template <typename F>
@@ -831,9 +996,9 @@ int launch_shrink(const ShrinkArgs& m, int64_t grid, hipStream_t s)
 template <bool COLS>
 int run_shrink(int dtype, ShrinkArgs m, hipStream_t s)
 {
-    const bool small = small_tiles(m.pairs, m.L, m.sorted != nullptr);
-    const int64_t tiles = ceil_div(m.pairs, small ? 16 : 64);
-    m.groups = m.pairs <= 256 ? (int32_t)std::min<int64_t>(16, m.L) : 1;
+    const bool small = m.tiles.rows <= 16;
+    const int64_t tiles = m.tiles.most;
+    m.groups = !m.tiles.sorted && small ? (int32_t)std::min<int64_t>(16, m.L) : 1;
     m.steps = (int32_t)ceil_div(ceil_div(m.row_bytes, kLine), m.splits);
     return by_type(dtype, [&](auto dt) {
         constexpr int DT = decltype(dt)::value;
@@ -842,38 +1007,40 @@ int run_shrink(int dtype, ShrinkArgs m, hipStream_t s)
     });
 }
 
-template <int DT, int OT, int BT, bool RANKS>
+template <int DT, int OT, bool RANKS, int WR>
 int launch_expand(const ExpandArgs& m, int64_t grid, hipStream_t s)
 {
     const auto go = [&](auto* kernel) { return launch("lora_expand_kernel", kernel, grid, kThreads, 0, s, m); };
     const int rt = rank_tiles(m.R);
     if constexpr (DT == FTQ_F32) {
-        if (rt == 1) return go(lora_expand_kernel<DT, OT, BT, 1, RANKS>);
-        if (rt == 2) return go(lora_expand_kernel<DT, OT, BT, 2, RANKS>);
-        if (rt == 4) return go(lora_expand_kernel<DT, OT, BT, 4, RANKS>);
-        return go(lora_expand_kernel<DT, OT, BT, 8, RANKS>);
+        if (rt == 1) return go(lora_expand_kernel<DT, OT, 1, RANKS, WR>);
+        if (rt == 2) return go(lora_expand_kernel<DT, OT, 2, RANKS, WR>);
+        if (rt == 4) return go(lora_expand_kernel<DT, OT, 4, RANKS, WR>);
+        return go(lora_expand_kernel<DT, OT, 8, RANKS, WR>);
     } else {
-        if (rt <= 2) return go(lora_expand_kernel<DT, OT, BT, 1, RANKS>);
-        if (rt == 4) return go(lora_expand_kernel<DT, OT, BT, 2, RANKS>);
-        return go(lora_expand_kernel<DT, OT, BT, 4, RANKS>);
+        if (rt <= 2) return go(lora_expand_kernel<DT, OT, 1, RANKS, WR>);
+        if (rt == 4) return go(lora_expand_kernel<DT, OT, 2, RANKS, WR>);
+        return go(lora_expand_kernel<DT, OT, 4, RANKS, WR>);
     }
 }
 
 template <bool RANKS>
 int run_expand(int dtype, int out_dtype, ExpandArgs m, hipStream_t s)
 {
-    const bool small = small_tiles(m.pairs, m.L, m.sorted != nullptr);
-    const int64_t tiles = ceil_div(m.pairs, small ? 16 : 64);
-    m.groups = m.pairs <= 256 ? (int32_t)std::min<int64_t>(16, m.L) : 1;
-    const int64_t chunks = ceil_div(m.C, 256), per = std::max<int64_t>(1, std::min(chunks, tiles * m.groups * chunks / 1024));
-    m.cols = (int32_t)(per * 256);
+    const bool small = m.tiles.rows <= 16;
+    m.groups = !m.tiles.sorted && small ? (int32_t)std::min<int64_t>(16, m.L) : 1;
+    // the columns in even shares of whole steps, for about four workgroups a CU; many tiles are not shared (1009 tiles of up
+    // to 32 pairs, 2816 columns: 90 us, 98 in two shares)
+    const int64_t step = small ? 256 : 64, lots = ceil_div(m.C, step), tiles = m.tiles.most * m.groups;
+    const int64_t shares = tiles >= 512 ? 1 : std::min(lots, ceil_div(1024, tiles));
+    m.cols = (int32_t)(ceil_div(lots, shares) * step);
     m.col_items = ceil_div(m.C, m.cols);
-    const int64_t grid = tiles * m.groups * m.col_items;
+    const int64_t grid = tiles * m.col_items;
     return by_type(dtype, [&](auto dt) {
         constexpr int DT = decltype(dt)::value;
         const auto with = [&](auto ot) {
             constexpr int OT = decltype(ot)::value;
-            return small ? launch_expand<DT, OT, 1, RANKS>(m, grid, s) : launch_expand<DT, OT, 4, RANKS>(m, grid, s);
+            return small ? launch_expand<DT, OT, RANKS, 1>(m, grid, s) : launch_expand<DT, OT, RANKS, 4>(m, grid, s);
         };
         if constexpr (RANKS) return with(dt);                      // d_x has the rows' type
         else return by_type(out_dtype, with);
@@ -888,7 +1055,7 @@ struct ForwardPlan {
 ForwardPlan plan_forward(int64_t L, int64_t R, int64_t K, int64_t pairs, int dtype, int path)
 {
     ForwardPlan p;
-    if (path == FTQ_PATH_GROUPED) p.bucket = make_bucket_plan(pairs, L, 0);
+    if (path == FTQ_PATH_GROUPED) p.bucket = make_bucket_plan(pairs, L, table_tile(pairs, L));
     p.splits = shrink_splits(pairs, K, R, dtype);
     p.off_part = p.bucket.bytes;
     p.bytes = p.off_part + align256(p.splits * pairs * R * 4);
@@ -972,18 +1139,18 @@ int run_lora(const LoraArgs& m, void* ws, int path, hipStream_t s)
     const int64_t pairs = m.T * m.top_k;
     uint8_t* mem = static_cast<uint8_t*>(ws);
     const ForwardPlan plan = plan_forward(m.L, m.R, m.K, pairs, m.dtype, path);
-    const int32_t* sorted = nullptr;
+    TileList tiles = in_order(pairs);
     if (path == FTQ_PATH_GROUPED) {
         const int st = run_bucket(m.ids, m.L, plan.bucket, ws, s);
         if (st != FTQ_OK) return st;
-        sorted = reinterpret_cast<const int32_t*>(mem + plan.bucket.off_sorted);
+        tiles = from_tables(plan.bucket, mem, m.L, 1);
     }
     ShrinkArgs shrink{};
     shrink.v = static_cast<const uint8_t*>(m.x);
     shrink.ldv = m.ldx * size_of(m.dtype);
     shrink.w = static_cast<const uint8_t*>(m.a);
     shrink.ids = m.ids;
-    shrink.sorted = sorted;
+    shrink.tiles = tiles;
     shrink.part = reinterpret_cast<float*>(mem + plan.off_part);
     shrink.pairs = pairs;
     shrink.row_bytes = m.K * size_of(m.dtype);
@@ -998,7 +1165,7 @@ int run_lora(const LoraArgs& m, void* ws, int path, hipStream_t s)
     expand.w = static_cast<const uint8_t*>(m.b);
     expand.scale = m.scale;
     expand.ids = m.ids;
-    expand.sorted = sorted;
+    expand.tiles = tiles;
     expand.base = m.base;
     expand.out = m.out;
     expand.h = m.h;
@@ -1030,6 +1197,7 @@ int run_lora_backward(const LoraBackwardArgs& m, void* ws, hipStream_t s)
     if (st != FTQ_OK) return st;
     const OuterTables tab{reinterpret_cast<const int32_t*>(mem + plan.bucket.off_tiles), reinterpret_cast<const int32_t*>(mem + plan.bucket.off_sorted),
                           reinterpret_cast<const int4*>(mem + plan.bucket.off_tdesc)};
+    const TileList rows_of = from_tables(plan.bucket, mem, m.L, table_tile(pairs, m.L) == 64 ? 2 : 1);
     const auto floats = [&](int64_t off) { return reinterpret_cast<float*>(mem + off); };
     const bool want_g = m.d_x || m.d_a, expand_x = m.d_x && m.act_div == 1;   // else rows that several pairs share
     if (want_g) {
@@ -1038,7 +1206,7 @@ int run_lora_backward(const LoraBackwardArgs& m, void* ws, hipStream_t s)
         shrink.ldv = m.ld_d * es;
         shrink.w = static_cast<const uint8_t*>(m.b);
         shrink.ids = m.ids;
-        shrink.sorted = tab.sorted;
+        shrink.tiles = rows_of;
         shrink.part = floats(plan.off_part);
         shrink.pairs = pairs;
         shrink.row_bytes = m.N * es;
@@ -1062,7 +1230,7 @@ int run_lora_backward(const LoraBackwardArgs& m, void* ws, hipStream_t s)
         expand.part = floats(plan.off_g);
         expand.w = static_cast<const uint8_t*>(m.a);
         expand.ids = m.ids;
-        expand.sorted = tab.sorted;
+        expand.tiles = rows_of;
         expand.base = m.base;
         expand.out = m.d_x;
         expand.ld_base = expand.ld_out = expand.C = m.K;

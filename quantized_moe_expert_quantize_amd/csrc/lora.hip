@@ -949,7 +949,7 @@ int rank_tiles(int64_t R) { return R <= 16 ? 1 : R <= 32 ? 2 : R <= 64 ? 4 : 8; 
 int64_t shrink_splits(int64_t pairs, int64_t C, int64_t R, int dtype)
 {
     const int64_t steps = ceil_div(C * size_of(dtype), kLine), tiles = ceil_div(pairs, 64);
-    const int64_t want = tiles <= 16 ? 16 : std::max<int64_t>(1, 512 / tiles / std::max<int64_t>(1, R / 32));
+    const int64_t want = tiles <= 16 ? 16 : std::max<int64_t>(1, 512 / tiles);
     return std::max<int64_t>(1, std::min({want, int64_t(16), steps / 2}));
 }
 
@@ -1185,7 +1185,7 @@ int run_lora_backward(const LoraBackwardArgs& m, void* ws, hipStream_t s)
     const int rt = rank_tiles(m.R);
     const auto reduce = [&](const int32_t* tiles, int64_t run, const float* pa, const float* pb) {
         const auto args = [&](float* d, int64_t C, const float* part) {
-            return ReduceArgs{part, d, m.R * C, d ? (int32_t)m.L : 0, (int32_t)run, std::min<int64_t>(ceil_div(m.R * C / 4, kThreads), 64)};
+            return ReduceArgs{part, d, m.R * C, d ? (int32_t)m.L : 0, (int32_t)run, std::min<int64_t>(ceil_div(m.R * C / 4, kThreads), std::max<int64_t>(8, 2048 / m.L))};
         };
         const ReduceArgs a = args(m.d_a, m.K, pa), b = args(m.d_b, m.N, pb);
         return launch("lora_reduce_kernel", lora_reduce_kernel, a.blocks * a.L + b.blocks * b.L, kThreads, 0, s, tiles, a, b);

@@ -298,3 +298,22 @@ def test_offsets_past_32_bits():
     assert not out[1:].any()
     ref, _, mag, _ = t.lora_forward(x[:1], a[-1:], b[-1:], torch.zeros(1, 1, dtype=torch.int32), None, None, False)
     t.close(out[:1], ref, mag, K + R + 8)
+
+
+def test_wide_rows_past_32_bits():
+    """Results, their base and gradients of more than 2^31 elements and 2^32 bytes."""
+    L, R, K, N, T = 2, 8, 8, 65536, 33000
+    x, a, b = torch.randn(T, K, device="cuda").bfloat16(), torch.randn(L, R, K, device="cuda").bfloat16(), torch.randn(L, N, R, device="cuda").bfloat16()
+    ids = (torch.arange(T, device="cuda") % L).to(torch.int32).view(T, 1)
+    for path in PATHS:
+        out = torch.ones(T, N, dtype=torch.bfloat16, device="cuda")
+        h = torch.empty(T, R, device="cuda")
+        ftq.lora(x, a, b, ids, base=out, out=out, h=h, path=path)
+        few = ftq.lora(x[-40:], a, b, ids[-40:], base=torch.ones(40, N, dtype=torch.bfloat16, device="cuda"), path=path)
+        assert torch.equal(out[-40:], few)
+    out.zero_()
+    out[-40:] = torch.randn(40, N, device="cuda")              # now the gradient
+    _, d_a, d_b = ftq.lora_backward(out, x, a, b, ids, h)
+    ref = t.lora_backward(out[-40:], x[-40:], a, b, ids[-40:], h[-40:], None, None, False)
+    t.close(d_a, *ref["d_a"], N + T + 10, "d_a")
+    t.close(d_b, *ref["d_b"], T + 10, "d_b")

@@ -341,3 +341,36 @@ def test_combine_gradient_against_differences():
         want = (value(y0 + vy, g0) - value(y0 - vy, g0)) / 2 + (value(y0, g0 + vg) - value(y0, g0 - vg)) / 2
         got = float((d_y.cpu().double() * vy).sum() + (d_gates.cpu().double() * vg).sum())
         assert abs(want - got) <= 1e-5 * (1 + abs(want))
+
+
+# ---- offsets past 32 bits -------------------------------------------------------------
+
+def test_router_offsets_past_32_bits():
+    T, E, k = (1 << 21) + 300, 1024, 2                         # 2.1e9 logits
+    logits = torch.empty(T, E, dtype=torch.bfloat16, device="cuda").normal_()
+    ids = torch.randint(0, E, (T, k), dtype=torch.int32, device="cuda")
+    offsets = torch.tensor([0, T - 77, T], dtype=torch.int32, device="cuda")
+    loss, counts, tokens = ftq.moe_balance(logits, ids, offsets=offsets)
+    assert tokens.tolist() == [T - 77, 77]
+    assert torch.equal(counts[0], torch.bincount(ids[:-77].reshape(-1).long(), minlength=E).to(torch.int32))
+    tail = [logits[-77:].clone(), ids[-77:].clone()]
+    few = ftq.moe_balance(*tail)
+    assert torch.equal(counts[1], few[1][0]) and abs(float(loss[1]) / float(few[0][0]) - 1) <= 2 * t.U * 100
+    # evenly spread pairs: the loss is 1 but for the spread of counts and probabilities over 2e6 rows
+    assert abs(float(loss[0]) - 1) < 1e-3
+    d_gates, d_loss = torch.randn(T, k, device="cuda"), torch.rand(2, device="cuda")
+    got = ftq.moe_topk_backward(logits, ids, d_gates, d_loss=d_loss, counts=counts, tokens=tokens, offsets=offsets)
+    want = ftq.moe_topk_backward(*tail, d_gates[-77:].clone(), d_loss=d_loss[1:].clone(), counts=counts[1:].clone(), tokens=tokens[1:].clone())
+    assert torch.equal(got[-77:], want)
+
+
+def test_combine_offsets_past_32_bits():
+    T, k, N = 33000, 2, 33000                                  # 2.2e9 values of y
+    y = torch.zeros(T * k, N, device="cuda")
+    y[-6:] = torch.randn(6, N, device="cuda")
+    d_out, gates = torch.zeros(T, N, device="cuda"), torch.rand(T, k, device="cuda")
+    d_out[-3:] = torch.randn(3, N, device="cuda")
+    d_y, d_gates = ftq.combine_topk_backward(d_out, y, gates, d_y_dtype=torch.bfloat16)
+    few = ftq.combine_topk_backward(d_out[-3:].clone(), y[-6:].clone(), gates[-3:].clone(), d_y_dtype=torch.bfloat16)
+    assert torch.equal(d_y[-6:], few[0]) and torch.equal(d_gates[-3:], few[1])
+    assert not d_y[:-6].any() and not d_gates[:-3].any()

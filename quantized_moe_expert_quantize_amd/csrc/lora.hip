@@ -302,8 +302,10 @@ template <int DT> __device__ __forceinline__ float load1(const void* p, int64_t 
     else return DT == FTQ_F16 ? f32_of_f16(static_cast<const uint16_t*>(p)[i]) : f32_of_bf16(static_cast<const uint16_t*>(p)[i]);
 }
 
-// N consecutive results v added to 16 bytes of base, rounded to OT and stored.
-template <int OT, int N>
+// N consecutive results v added to 16 bytes of base, rounded to OT and stored; PAST: past the caches, as long results
+// are that would drive out the rows other workgroups are about to read (8191 rows of 4096 in bf16, their shrink and expand
+// 62 us, 60 so).
+template <int OT, bool PAST, int N>
 __device__ __forceinline__ void add_and_store(void* out, int64_t i, u32x4 base, const float (&v)[N])
 {
     if constexpr (OT == FTQ_F32) {
@@ -311,7 +313,9 @@ __device__ __forceinline__ void add_and_store(void* out, int64_t i, u32x4 base, 
         f32x4 b = __builtin_bit_cast(f32x4, base);
 #pragma unroll
         for (int e = 0; e < 4; ++e) b[e] += v[e];
-        *reinterpret_cast<f32x4*>(static_cast<float*>(out) + i) = b;
+        f32x4* to = reinterpret_cast<f32x4*>(static_cast<float*>(out) + i);
+        if constexpr (PAST) __builtin_nontemporal_store(b, to);
+        else *to = b;
     } else {
         static_assert(N == 8);
         u32x4 r;
@@ -324,7 +328,9 @@ __device__ __forceinline__ void add_and_store(void* out, int64_t i, u32x4 base, 
                 r[e] = bf16_of_f32(f32_of_bf16(lo) + v[2 * e]) | (uint32_t)bf16_of_f32(f32_of_bf16(hi) + v[2 * e + 1]) << 16;
             }
         }
-        *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(out) + i) = r;
+        u32x4* to = reinterpret_cast<u32x4*>(static_cast<uint16_t*>(out) + i);
+        if constexpr (PAST) __builtin_nontemporal_store(r, to);
+        else *to = r;
     }
 }
 
@@ -575,7 +581,7 @@ __global__ __launch_bounds__(kThreads) void lora_expand_kernel(ExpandArgs m)
                     }
 #pragma unroll
                     for (int z2 = 0; z2 < 2; ++z2) {
-                        if (own[z2] && there(c0, t)) add_and_store<OT>(to[z2] + (c0 + t * 8 * kRun) * kSize<OT>, 0, base[t][z2], v[z2]);
+                        if (own[z2] && there(c0, t)) add_and_store<OT, WR == 4>(to[z2] + (c0 + t * 8 * kRun) * kSize<OT>, 0, base[t][z2], v[z2]);
                     }
                 }
             }
@@ -641,7 +647,7 @@ __global__ __launch_bounds__(kThreads) void lora_gather_kernel(GatherArgs m)
     u32x4 base = {0u, 0u, 0u, 0u};
     const int64_t o = (t * m.C + c) * kSize<DT>;
     if (m.base) base = *reinterpret_cast<const u32x4*>(m.base + o);
-    add_and_store<DT>(m.out + o, 0, base, acc);
+    add_and_store<DT, false>(m.out + o, 0, base, acc);
 }
 
 // ---- outer: d[l] = sum over its pairs of u[p] v[row of p]^T -----------------------------

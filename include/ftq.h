@@ -565,7 +565,7 @@ int ftq_moe_balance(const void* logits, int dtype, int64_t ld, const int32_t* to
  * one expert.  Experts whose logit is -inf have gradient 0.  A row whose logits hold a NaN
  * has NaN from the balance loss, and nothing from gates if its ids name no expert.
  * Renormalised gates have their gradient relative to the largest chosen logit, so that
- * choices far below the row's largest keep theirs.  At least one of d_gates
+ * choices far below the row's largest keep theirs.  d_logits must not overlap the inputs.  At least one of d_gates
  * and d_loss; other limits as ftq_moe_balance.  T == 0: no-op.
  */
 int ftq_moe_topk_backward(const void* logits, int dtype, int64_t ld, const int32_t* topk_ids, const float* d_gates,

@@ -201,7 +201,7 @@ __global__ __launch_bounds__(ALONE ? kAloneThreads : kThreads) void balance_part
             begin = m.offsets ? max((int64_t)__shfl(seq.at, (int)s), (int64_t)0) : 0;
             end = m.offsets ? min((int64_t)__shfl(seq.at, (int)s + 1), m.T) : m.T;
         } else {                                      // those that have rows in this chunk
-            if (row >= r1 || (s = seq.of(row, begin, end)) >= m.S || begin >= r1) break;
+            if (row >= r1 || (s = seq.of(row, begin, end)) >= m.S || begin >= r1 || end <= row) break;   // (end <= row: offsets that descend)
             if (begin > row) {                        // rows of no sequence
                 row = begin;
                 continue;

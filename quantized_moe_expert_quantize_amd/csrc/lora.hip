@@ -368,6 +368,7 @@ __global__ __launch_bounds__(kThreads) void lora_expand_kernel(ExpandArgs m)
     constexpr int kUnits = kRow / 16 * kRowsLds / kThreads;        // 16-byte runs of a thread
     static_assert(kRow / 16 * kRowsLds % kThreads == 0);
     constexpr bool kLds = WR == 4;
+    static_assert(kLds || !RANKS);
     __shared__ __attribute__((aligned(16))) uint8_t wl[kLds ? kRowsLds * kPitch : 16];
     const int lane = threadIdx.x & 63, wave = uniform((int32_t)(threadIdx.x >> 6)), r16 = lane & 15, q = lane >> 4;
     const bool odd = r16 & 1;
@@ -439,17 +440,7 @@ __global__ __launch_bounds__(kThreads) void lora_expand_kernel(ExpandArgs m)
                     for (int k = 0; k < KST; ++k) {
                         const int r = k * kElems + q * kOwn;
                         if (r >= m.R) continue;                    // (R is a multiple of 8: all of a lane's ranks are there or none)
-                        if constexpr (RANKS) {
-                            using Bits = std::conditional_t<DT == FTQ_F32, uint32_t, uint16_t>;
-                            const Bits* src = reinterpret_cast<const Bits*>(m.w) + ((int64_t)l * m.R + r) * m.C + c;
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                if constexpr (DT == FTQ_F32) ahead[i * KST + k][e] = src[e * m.C];
-                                else ahead[i * KST + k][e] = src[2 * e * m.C] | (uint32_t)src[(2 * e + 1) * m.C] << 16;
-                            }
-                        } else {
-                            ahead[i * KST + k] = *reinterpret_cast<const u32x4*>(m.w + (((int64_t)l * m.C + c) * m.R + r) * kSize<DT>);
-                        }
+                        ahead[i * KST + k] = *reinterpret_cast<const u32x4*>(m.w + (((int64_t)l * m.C + c) * m.R + r) * kSize<DT>);
                     }
                 }
                 return;
@@ -1009,7 +1000,10 @@ int run_shrink(int dtype, ShrinkArgs m, hipStream_t s)
     return by_type(dtype, [&](auto dt) {
         constexpr int DT = decltype(dt)::value;
         const int64_t grid = tiles * m.groups * m.splits;
-        return small ? launch_shrink<DT, 1, COLS>(m, grid, s) : launch_shrink<DT, 4, COLS>(m, grid, s);
+        if constexpr (!COLS) {                                     // (the gradients' tiles are of 32 pairs and more)
+            if (small) return launch_shrink<DT, 1, COLS>(m, grid, s);
+        }
+        return launch_shrink<DT, 4, COLS>(m, grid, s);
     });
 }
 
@@ -1046,7 +1040,10 @@ int run_expand(int dtype, int out_dtype, ExpandArgs m, hipStream_t s)
         constexpr int DT = decltype(dt)::value;
         const auto with = [&](auto ot) {
             constexpr int OT = decltype(ot)::value;
-            return small ? launch_expand<DT, OT, RANKS, 1>(m, grid, s) : launch_expand<DT, OT, RANKS, 4>(m, grid, s);
+            if constexpr (!RANKS) {
+                if (small) return launch_expand<DT, OT, RANKS, 1>(m, grid, s);
+            }
+            return launch_expand<DT, OT, RANKS, 4>(m, grid, s);
         };
         if constexpr (RANKS) return with(dt);                      // d_x has the rows' type
         else return by_type(out_dtype, with);

@@ -94,6 +94,18 @@ def test_many_sequences(T, S):
     t.close(got, p * (1 - s) * (v - (p * v).sum(1, keepdim=True)), p * (v.abs() + (p * v.abs()).sum(1, keepdim=True)), 144, "d_logits")
 
 
+def test_offsets_that_descend_end():
+    """Offsets that are not ascending have no defined losses, but the call ends and leaves the next one right."""
+    g, logits, ids = _inputs(9000, 16, 2, "f32", seed=2)
+    for cuts in ([0, 9000, 4000, 100, 9000], [9000, 0, 9000, 0, 5], [-5, 20000, -7, 3, 20000], [7, 7, 5, 7, 6]):
+        for more in (0, 200):
+            offsets = torch.tensor(cuts + cuts[1:] * (more // 4), dtype=torch.int32).cuda()
+            _, counts, tokens = ftq.moe_balance(*_cuda(logits, ids), offsets=offsets)
+            ftq.moe_topk_backward(*_cuda(logits, ids), d_loss=torch.ones(len(offsets) - 1).cuda(), counts=counts, tokens=tokens, offsets=offsets)
+    torch.cuda.synchronize()
+    _check_loss(logits, ids, ftq.SCORE_SOFTMAX, _cuts(g, 9000, 5))
+
+
 def test_loss_of_strange_rows():
     _, logits, ids = _inputs(300, 64, 4, "f32", seed=1)
     logits[5, :60] = -INF                                      # few experts left

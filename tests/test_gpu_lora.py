@@ -93,6 +93,17 @@ def test_forward_in_place_without_base_and_strided(path):
     assert not y.any() and not h.any()
 
 
+def test_in_place_with_another_stride_is_refused():
+    """out at base's address with a stride of its own would be another tensor than base."""
+    x, a, b, ids = torch.ones(4, 8).cuda(), torch.ones(1, 8, 8).cuda(), torch.ones(1, 8, 8).cuda(), torch.zeros(4, 1, dtype=torch.int32).cuda()
+    buf = torch.full((4, 16), 2.0).cuda()
+    with pytest.raises(ftq.FtqError):
+        ftq.lora(x, a, b, ids, base=buf[:, :8], out=buf.view(8, 8)[:4])
+    assert (buf == 2.0).all()
+    ftq.lora(x[:1], a, b, ids[:1], base=buf[:1, :8], out=buf.view(8, 8)[:1])   # one row: the same tensor
+    assert (buf[0, :8] == 66.0).all() and (buf[0, 8:] == 2.0).all()
+
+
 @pytest.mark.parametrize("path", PATHS)
 def test_rows_depend_on_their_own_inputs_alone(path):
     """NaN and infinities of one adapter or row stay with the pairs that use them; a pair alone has the same bits."""

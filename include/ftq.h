@@ -608,9 +608,9 @@ int ftq_moe_combine_topk_backward(const float* d_out, const float* y, const floa
  *            adapter lie together, as a request's do, or are few.  FTQ_PATH_GROUPED
  *            sorts them by adapter first.  FTQ_PATH_AUTO: ftq_lora_select_path,
  *            in order for top_k == 1 or few pairs, else sorted.
- * Products and sums are fp32 (h too), out is rounded once.  A row's bits depend neither on other rows
- * nor on the path, but for h's sums the number of parts they are split into goes by the sizes.  NaN and infinities of an
- * adapter or a row reach only the pairs that use them.
+ * Products are exact to fp32's 24 bits and sums fp32 (h too), in all types; out is rounded once.  A row's bits depend neither on
+ * other rows nor on the path, but for h's sums the number of parts they are split into goes by the sizes.  NaN and infinities of an
+ * adapter or a row reach only the pairs that use them; what an infinity is a factor of is infinite or NaN.
  * x, a, b, base, out and h are 16-byte aligned, their row strides whole 16-byte units.
  * Limits: K, N and R multiples of 8; R <= 128 (FTQ_ERR_UNSUPPORTED above); L, K, N, R >= 1;
  * L <= 4095 on the grouped path; T*top_k < 2^31; L, K and N < 2^31.  T == 0: no-op.
@@ -640,7 +640,8 @@ int ftq_lora(const void* x, int64_t ldx, const void* a, const void* b, const flo
  *   d_a, d_b fp32 [L][R][K] and [L][N][R], or NULL: not wanted.  Written: adapters without a
  *            pair get zeros.
  *   workspace: ftq_lora_backward_workspace_bytes(...) bytes, 256-byte aligned.
- * Sums are fp32 in a fixed order: the same call gives the same bits.  Alignment and limits as ftq_lora;
+ * Products are exact to fp32's 24 bits and sums fp32, in all types and a fixed order: the same call gives the same bits.
+ * NaN and infinities reach only the values that they are a term of.  Alignment and limits as ftq_lora;
  * L <= 4095, top_k <= 64 (FTQ_ERR_UNSUPPORTED above); at least one output.  T == 0 writes zeros to d_a and d_b.
  */
 int64_t ftq_lora_backward_workspace_bytes(int64_t L, int64_t R, int64_t K, int64_t N, int64_t T, int64_t top_k, int dtype);

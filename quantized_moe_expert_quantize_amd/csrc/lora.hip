@@ -22,9 +22,13 @@
 // A tile of rows may hold several adapters: shrink and expand go through them one by
 // one, each time for the whole tile, and keep each row's results of its own adapter
 // alone, so that no row ever sees another's weights.  An adapter's R-vectors are fp32.
-// As operands beside 16-bit weights or rows they are split into a sum of 16-bit
-// pieces, three in bf16 (24 bits) or two in fp16 (22 bits, scaled by a power of two to
-// the middle of its range), and every piece is multiplied: products are as exact as fp32's.
+// As operands beside 16-bit weights or rows they are the sum of three bf16 pieces of 8 bits
+// each, which have fp32's range and, together, its 24 bits whatever else lies in the
+// vector.  bf16 weights and rows are multiplied by every piece; fp16 ones are the sum of two bf16
+// operands (8 bits and the remaining 3), six products in all.  Each product is exact and
+// summed in fp32.  (fp16 with two fp16 pieces under one power of two: gradients of 8192 rows at rank 64 in 128 us,
+// 151 so, 8191 rows at rank 32 in 58, 60 so; but ranks or pairs at 2^-24 of the largest beside
+// them were 1e-4 of their size off, and an infinity took the bits of the others.)
 #include <type_traits>
 
 #include "ftq_internal.h"
@@ -37,16 +41,17 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short i16x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kThreads = 256;
 constexpr int kLine = 128;                             // bytes of a row in one piece
-constexpr float kInf = __builtin_inff();
 
 template <int DT> constexpr int kSize = DT == FTQ_F32 ? 4 : 2;
-template <int DT> constexpr int kPieces = DT == FTQ_F32 ? 1 : DT == FTQ_F16 ? 2 : 3;
+template <int DT> constexpr int kPieces = DT == FTQ_F32 ? 1 : 3;   // of an R-vector's value
+template <int DT> constexpr int kParts = DT == FTQ_F16 ? 2 : 1;     // of a weight or a row's value beside them
 
 __device__ const u32x4 kZeros = {0u, 0u, 0u, 0u};      // what a copy reads in place of what is not there
 
@@ -77,28 +82,44 @@ __device__ __forceinline__ u32x2 read_transposed(const uint8_t* lds)
     return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) i16x4*)lds));
 }
 
-// The next 16-bit piece of v; v becomes what is left of it.
-template <int DT>
-__device__ __forceinline__ uint16_t take_piece(float& v)
+// The next bf16 piece of v: its first 8 significant bits; v becomes what is left of it.
+__device__ __forceinline__ uint32_t take_piece(float& v)
 {
-    if constexpr (DT == FTQ_F16) {
-        const uint16_t h = f16_of_f32(v);
-        v -= f32_of_f16(h);
-        return h;
+    const uint32_t top = __builtin_bit_cast(uint32_t, v) & 0xffff0000u;
+    v -= __builtin_bit_cast(float, top);
+    return top >> 16;
+}
+
+// An operand of weights or rows as those that the pieces are multiplied by: itself, or, of fp16, two of bf16 whose
+// sum it is.  (Of an infinity the second is a NaN.)
+template <int DT>
+__device__ __forceinline__ void split_operand(u32x4 w, u32x4 (&part)[kParts<DT>])
+{
+    if constexpr (DT != FTQ_F16) {
+        part[0] = w;
     } else {
-        const uint16_t h = bf16_of_f32(v);
-        v -= f32_of_bf16(h);
-        return h;
+        const auto two = [](f16x2 h) {                 // values of at most 8 significant bits: the upper halves of their floats
+            return __builtin_bit_cast(uint32_t, (float)h[0]) >> 16 | (__builtin_bit_cast(uint32_t, (float)h[1]) & 0xffff0000u);
+        };
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const f16x2 top = __builtin_bit_cast(f16x2, w[i] & 0xfff8fff8u);
+            part[0][i] = two(top);
+            part[1][i] = two(__builtin_bit_cast(f16x2, (uint32_t)w[i]) - top);
+        }
     }
 }
 
-// The exponent e for which size * 2^-e lies in [2^12, 2^13), in the middle of fp16's range
-// (0 for sizes that have none; bounded, so that 2^e and 2^-e are normal numbers).
-__device__ __forceinline__ int middle_exponent(float size)
+// 16 rows x 16 columns += weights or rows (their parts) times 64 bytes of R-vectors (their pieces).
+template <int DT>
+__device__ __forceinline__ f32x4 multiply_pieces(const u32x4 (&part)[kParts<DT>], const u32x4 (&piece)[kPieces<DT>], f32x4 c)
 {
-    if (!(size > 0.0f && size < kInf)) return 0;
-    const int e = __builtin_amdgcn_frexp_expf(size) - 13;
-    return min(max(e, -110), 110);
+#pragma unroll
+    for (int i = 0; i < kPieces<DT>; ++i) {
+#pragma unroll
+        for (int h = 0; h < kParts<DT>; ++h) c = multiply<DT == FTQ_F16 ? FTQ_BF16 : DT>(part[h], piece[i], c);
+    }
+    return c;
 }
 
 // ---- tiles of pairs --------------------------------------------------------------
@@ -364,12 +385,12 @@ __global__ __launch_bounds__(kThreads) void lora_expand_kernel(ExpandArgs m)
     constexpr int BM = 16 * WR, kCols = 256 / WR;                  // pairs of a workgroup, columns of its step
     // LDS rows: a column's ranks or a rank's columns, set apart by 16 bytes where they would meet the same banks
     constexpr int kRow = RANKS ? kCols * kSize<DT> : 64 * KST, kPitch = kRow + (RANKS || KST > 1 ? 16 : 0);
-    constexpr int kRowsLds = RANKS ? kElems * KST : kCols;
+    constexpr int kRowsLds = RANKS ? kElems * KST : kCols, kPlane = kRowsLds * kPitch;   // a part's bytes
     constexpr int kUnits = kRow / 16 * kRowsLds / kThreads;        // 16-byte runs of a thread
     static_assert(kRow / 16 * kRowsLds % kThreads == 0);
     constexpr bool kLds = WR == 4;
     static_assert(kLds || !RANKS);
-    __shared__ __attribute__((aligned(16))) uint8_t wl[kLds ? kRowsLds * kPitch : 16];
+    __shared__ __attribute__((aligned(16))) uint8_t wl[kLds ? kParts<DT> * kPlane : 16];
     const int lane = threadIdx.x & 63, wave = uniform((int32_t)(threadIdx.x >> 6)), r16 = lane & 15, q = lane >> 4;
     const bool odd = r16 & 1;
     const int64_t item = blockIdx.x, at = item / m.col_items;
@@ -407,7 +428,7 @@ __global__ __launch_bounds__(kThreads) void lora_expand_kernel(ExpandArgs m)
         part_of[i] = u % per_row;
     }
     if (kLds && have < kUnits * kThreads) {
-        for (int i = threadIdx.x; i < kRowsLds * kPitch / 16; i += kThreads) *reinterpret_cast<u32x4*>(wl + 16 * i) = u32x4{0u, 0u, 0u, 0u};
+        for (int i = threadIdx.x; i < kParts<DT> * kPlane / 16; i += kThreads) *reinterpret_cast<u32x4*>(wl + 16 * i) = u32x4{0u, 0u, 0u, 0u};
     }
     uint64_t todo = __ballot(tile_id != INT32_MIN);
     for (int index = 0; todo; ++index) {
@@ -460,12 +481,10 @@ __global__ __launch_bounds__(kThreads) void lora_expand_kernel(ExpandArgs m)
         load_base(c_first, base);
         // the R-vectors of this adapter's rows (zeros for others) as operands
         u32x4 z[KST][kPieces<DT>];
-        float f = 1.0f;                                            // 2^e of this row's pieces
         {
             const float scale = l >= 0 && m.scale ? m.scale[l] : 1.0f;
             const bool take = mine >> r16 & 1;
             f32x4 v[KST][kOwn / 4];
-            float size = 0.0f;
 #pragma unroll
             for (int k = 0; k < KST; ++k) {
 #pragma unroll
@@ -481,20 +500,6 @@ __global__ __launch_bounds__(kThreads) void lora_expand_kernel(ExpandArgs m)
                         if (m.h && c_first == 0 && (WR == 4 || wave == 0)) *reinterpret_cast<f32x4*>(m.h + o) = v[k][h];
                         v[k][h] *= scale;
                     }
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) size = fmaxf(size, __builtin_fabsf(v[k][h][e]));
-                }
-            }
-            if constexpr (DT == FTQ_F16) {
-                size = fmaxf(size, __shfl_xor(size, 16));
-                size = fmaxf(size, __shfl_xor(size, 32));
-                const int e2 = middle_exponent(size);
-                const float to_middle = __builtin_ldexpf(1.0f, -e2);
-                f = __builtin_ldexpf(1.0f, e2);
-#pragma unroll
-                for (int k = 0; k < KST; ++k) {
-#pragma unroll
-                    for (int h = 0; h < kOwn / 4; ++h) v[k][h] *= to_middle;
                 }
             }
 #pragma unroll
@@ -507,8 +512,8 @@ __global__ __launch_bounds__(kThreads) void lora_expand_kernel(ExpandArgs m)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             float lo = v[k][e / 2][e % 2 * 2], hi = v[k][e / 2][e % 2 * 2 + 1];
-                            const uint32_t piece = take_piece<DT>(lo);
-                            z[k][c][e] = piece | (uint32_t)take_piece<DT>(hi) << 16;
+                            const uint32_t piece = take_piece(lo);
+                            z[k][c][e] = piece | take_piece(hi) << 16;
                             v[k][e / 2][e % 2 * 2] = lo;
                             v[k][e / 2][e % 2 * 2 + 1] = hi;
                         }
@@ -521,7 +526,11 @@ __global__ __launch_bounds__(kThreads) void lora_expand_kernel(ExpandArgs m)
                 block_barrier();                                   // the last step's weights have been read
 #pragma unroll
                 for (int i = 0; i < kUnits; ++i) {
-                    if (row_of[i] != INT32_MAX) *reinterpret_cast<u32x4*>(wl + row_of[i] * kPitch + part_of[i] * 16) = ahead[i];
+                    if (row_of[i] == INT32_MAX) continue;
+                    u32x4 w[kParts<DT>];
+                    split_operand<DT>(ahead[i], w);                // once for the workgroup (by each wave: 8192 rows, rank 64, 4096 columns 58 us, 46 so)
+#pragma unroll
+                    for (int h = 0; h < kParts<DT>; ++h) *reinterpret_cast<u32x4*>(wl + h * kPlane + row_of[i] * kPitch + part_of[i] * 16) = w[h];
                 }
                 if (c0 + kCols < c_end) load_weights(c0 + kCols);
             }
@@ -534,29 +543,31 @@ __global__ __launch_bounds__(kThreads) void lora_expand_kernel(ExpandArgs m)
                     if (l < 0) continue;                           // no adapter, no weights: what LDS holds may be anything
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        u32x4 w;
-                        if constexpr (!kLds) {
-                            w = ahead[i * KST + k];
-                        } else if constexpr (!RANKS || DT == FTQ_F32) {
-                            const int c = column(i);
-                            if constexpr (!RANKS) {
-                                w = *reinterpret_cast<const u32x4*>(wl + c * kPitch + k * 64 + q * 16);
+                        u32x4 w[kParts<DT>];
+                        if constexpr (!kLds) split_operand<DT>(ahead[i * KST + k], w);
+#pragma unroll
+                        for (int p = 0; p < (kLds ? kParts<DT> : 0); ++p) {
+                            const uint8_t* plane = wl + p * kPlane;
+                            if constexpr (!RANKS || DT == FTQ_F32) {
+                                const int c = column(i);
+                                if constexpr (!RANKS) {
+                                    w[p] = *reinterpret_cast<const u32x4*>(plane + c * kPitch + k * 64 + q * 16);
+                                } else {
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) w[p][e] = *reinterpret_cast<const uint32_t*>(plane + (k * kElems + 4 * q + e) * kPitch + c * 4);
+                                }
                             } else {
+                                // columns four by four, as lanes 4j .. 4j+3 of a result hold them
+                                const int c = col0 + (kWide ? 16 * i + 4 * (r16 & 3) : 32 * (i / 2) + 8 * (r16 & 3) + 4 * (i % 2));
 #pragma unroll
-                                for (int e = 0; e < 4; ++e) w[e] = *reinterpret_cast<const uint32_t*>(wl + (k * kElems + 4 * q + e) * kPitch + c * 4);
-                            }
-                        } else {
-                            // columns four by four, as lanes 4j .. 4j+3 of a result hold them
-                            const int c = col0 + (kWide ? 16 * i + 4 * (r16 & 3) : 32 * (i / 2) + 8 * (r16 & 3) + 4 * (i % 2));
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                const u32x2 t = read_transposed(wl + (k * kElems + 8 * q + 4 * h + (r16 >> 2)) * kPitch + c * 2);
-                                w[2 * h] = t[0];
-                                w[2 * h + 1] = t[1];
+                                for (int h = 0; h < 2; ++h) {
+                                    const u32x2 t = read_transposed(plane + (k * kElems + 8 * q + 4 * h + (r16 >> 2)) * kPitch + c * 2);
+                                    w[p][2 * h] = t[0];
+                                    w[p][2 * h + 1] = t[1];
+                                }
                             }
                         }
-#pragma unroll
-                        for (int c = 0; c < kPieces<DT>; ++c) acc[i] = multiply<DT>(w, z[k][c], acc[i]);
+                        acc[i] = multiply_pieces<DT>(w, z[k], acc[i]);
                     }
                 }
 #pragma unroll
@@ -564,8 +575,8 @@ __global__ __launch_bounds__(kThreads) void lora_expand_kernel(ExpandArgs m)
                     float v[2][kRun];                              // of the even row, of the odd one
 #pragma unroll
                     for (int e = 0; e < kRun; ++e) {
-                        const float first = (kWide ? acc[2 * t][e % 4] : acc[e / 4][e % 4]) * f;
-                        const float second = (kWide ? acc[2 * t + 1][e % 4] : acc[2 + e / 4][e % 4]) * f;
+                        const float first = kWide ? acc[2 * t][e % 4] : acc[e / 4][e % 4];
+                        const float second = kWide ? acc[2 * t + 1][e % 4] : acc[2 + e / 4][e % 4];
                         const float got = swap_pair(odd ? first : second);
                         v[0][e] = odd ? got : first;
                         v[1][e] = odd ? second : got;
@@ -644,8 +655,8 @@ __global__ __launch_bounds__(kThreads) void lora_gather_kernel(GatherArgs m)
 // ---- outer: d[l] = sum over its pairs of u[p] v[row of p]^T -----------------------------
 //
 // The pairs are sorted by adapter and cut into tiles of 32 of one adapter.  lora_pieces
-// writes the R-vectors of a tile in the order that the products take them, u^T in pieces
-// of 16 bits: [tile][piece][16*RT][32].  A workgroup takes `run` tiles in a row and 512 bytes
+// writes the R-vectors of a tile in the order that the products take them, u^T in its
+// pieces: [tile][piece][16*RT][32].  A workgroup takes `run` tiles in a row and 512 bytes
 // of columns; where the adapter changes it writes its sums: to the result if all the
 // adapter's tiles are its own, else to part 2c (the adapter began before run c) or
 // 2c + 1, and lora_reduce adds an adapter's parts in their order.
@@ -663,7 +674,6 @@ struct PiecesArgs {
     const float* scale;        // [L] or null
     float* sum;                // [pairs][R] or null: the sum of the parts
     void* u;                   // [tiles][kPieces][16*RT][32]
-    float* back;               // [tiles]: 2^e of a tile's pieces (fp16)
     int64_t pairs, max_tiles;
     int32_t L, R, splits;
 };
@@ -673,7 +683,6 @@ template <int DT, int RT>
 __global__ __launch_bounds__(kThreads) void lora_pieces_kernel(OuterTables tab, PiecesArgs a0, PiecesArgs a1)
 {
     constexpr int kQuads = 4 * RT, kMine = (kQuads + 7) / 8;
-    __shared__ float wave_lds[kThreads / 64];
     const bool second = (int64_t)blockIdx.x >= a0.max_tiles;
     const PiecesArgs m = second ? a1 : a0;
     const int64_t t = second ? blockIdx.x - a0.max_tiles : blockIdx.x;
@@ -685,7 +694,6 @@ __global__ __launch_bounds__(kThreads) void lora_pieces_kernel(OuterTables tab, 
     const bool none = d.x >= m.L;
     const float scale = !none && m.scale ? m.scale[d.x] : 1.0f;
     f32x4 z[kMine] = {};
-    float size = 0.0f;
 #pragma unroll
     for (int i = 0; i < kMine; ++i) {
         const int r = (q0 + 8 * i) * 4;
@@ -696,24 +704,9 @@ __global__ __launch_bounds__(kThreads) void lora_pieces_kernel(OuterTables tab, 
             }
             z[i] *= scale;
             if (m.sum) *reinterpret_cast<f32x4*>(m.sum + p * m.R + r) = z[i];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) size = fmaxf(size, __builtin_fabsf(z[i][e]));
         }
     }
     if (none || !m.u) return;
-    if constexpr (DT == FTQ_F16) {
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) size = fmaxf(size, __shfl_xor(size, o));
-        if (threadIdx.x % 64 == 0) wave_lds[threadIdx.x / 64] = size;
-        __syncthreads();
-#pragma unroll
-        for (int w = 0; w < kThreads / 64; ++w) size = fmaxf(size, wave_lds[w]);
-        const int e2 = middle_exponent(size);
-        const float f = __builtin_ldexpf(1.0f, -e2);
-#pragma unroll
-        for (int i = 0; i < kMine; ++i) z[i] *= f;
-        if (threadIdx.x == 0) m.back[t] = __builtin_ldexpf(1.0f, e2);
-    }
 #pragma unroll
     for (int i = 0; i < kMine; ++i) {
         const int r = (q0 + 8 * i) * 4;
@@ -725,7 +718,7 @@ __global__ __launch_bounds__(kThreads) void lora_pieces_kernel(OuterTables tab, 
             } else {
                 float v = z[i][e];
 #pragma unroll
-                for (int c = 0; c < kPieces<DT>; ++c) static_cast<uint16_t*>(m.u)[((t * kPieces<DT> + c) * 16 * RT + r + e) * kTile + s] = take_piece<DT>(v);
+                for (int c = 0; c < kPieces<DT>; ++c) static_cast<uint16_t*>(m.u)[((t * kPieces<DT> + c) * 16 * RT + r + e) * kTile + s] = (uint16_t)take_piece(v);
             }
         }
     }
@@ -733,7 +726,6 @@ __global__ __launch_bounds__(kThreads) void lora_pieces_kernel(OuterTables tab, 
 
 struct OuterArgs {
     const uint8_t* u;          // as lora_pieces writes it
-    const float* back;
     const uint8_t* v;          // rows
     int64_t ldv;               // bytes
     float* part;               // [2 * runs][16*RT * C] (or C * R, as the result)
@@ -772,11 +764,10 @@ __global__ __launch_bounds__(kThreads) void lora_outer_kernel(OuterTables tab, O
     __shared__ __attribute__((aligned(16))) uint8_t vs[kDeep][kTile][512];
     __shared__ __attribute__((aligned(16))) uint8_t us[kDeep][kUBytes];
     __shared__ int32_t row_lds[kBatch * kTile], id_lds[kBatch + 1];
-    __shared__ float back_lds[kBatch];
     const bool second = (int64_t)blockIdx.x >= a0.items;
     // (field by field: a selected struct would be read from memory in the loop, and such a read waits for the copies)
-    const struct { const uint8_t *u, *v; const float* back; float *part, *d; int64_t ldv, C, col_items; int32_t div, L, R, by_column, run; } m = {
-        second ? a1.u : a0.u, second ? a1.v : a0.v, second ? a1.back : a0.back, second ? a1.part : a0.part, second ? a1.d : a0.d,
+    const struct { const uint8_t *u, *v; float *part, *d; int64_t ldv, C, col_items; int32_t div, L, R, by_column, run; } m = {
+        second ? a1.u : a0.u, second ? a1.v : a0.v, second ? a1.part : a0.part, second ? a1.d : a0.d,
         second ? a1.ldv : a0.ldv, second ? a1.C : a0.C, second ? a1.col_items : a0.col_items, second ? a1.div : a0.div, a0.L, a0.R,
         second ? a1.by_column : a0.by_column, a0.run};
     const int64_t item = second ? blockIdx.x - a0.items : blockIdx.x;
@@ -798,10 +789,7 @@ __global__ __launch_bounds__(kThreads) void lora_outer_kernel(OuterTables tab, O
         const int4 d = tab.tdesc[b0 + i / kTile];
         const int s = i % kTile;
         row_lds[i] = s < d.z ? tab.sorted[d.y + s] / m.div : -1;
-        if (s == 0) {
-            id_lds[i / kTile] = d.x;
-            if constexpr (DT == FTQ_F16) back_lds[i / kTile] = m.back[b0 + i / kTile];
-        }
+        if (s == 0) id_lds[i / kTile] = d.x;
     }
     if (threadIdx.x == 0) id_lds[count] = b0 + count < t1 ? tab.tdesc[b0 + count].x : -1;
     block_barrier();
@@ -827,7 +815,6 @@ __global__ __launch_bounds__(kThreads) void lora_outer_kernel(OuterTables tab, O
         wait_step<kPer, kDeep - 2>(count - 1 - i0);
         block_barrier();                                           // all waves' copies of the tile are there, the last one has been read
         const int32_t l = uniform(id_lds[i0]), after = uniform(id_lds[i0 + 1]);
-        const float f = DT == FTQ_F16 ? back_lds[i0] : 1.0f;
         if (i0 + kDeep - 1 < count) copy_tile(i0 + kDeep - 1);
         if constexpr (DT == FTQ_F32) {
 #pragma unroll
@@ -847,7 +834,7 @@ __global__ __launch_bounds__(kThreads) void lora_outer_kernel(OuterTables tab, O
             }
         } else {
             // columns as the left operand: a transposing read gives a lane four rows of its column
-            u32x4 x[kTiles];
+            u32x4 x[kTiles][kParts<DT>];
 #pragma unroll
             for (int i = 0; i < kTiles; ++i) {
                 u32x2 half[2];
@@ -857,26 +844,17 @@ __global__ __launch_bounds__(kThreads) void lora_outer_kernel(OuterTables tab, O
                     const uint8_t* src = &vs[buf][row][((c >> 3) ^ swizzle(row)) * 16 + (c & 7) * 2];
                     half[h] = read_transposed(src);
                 }
-                x[i] = u32x4{half[0][0], half[0][1], half[1][0], half[1][1]};
+                split_operand<DT>(u32x4{half[0][0], half[0][1], half[1][0], half[1][1]}, x[i]);
             }
 #pragma unroll
             for (int j = 0; j < RT; ++j) {
-                f32x4 p[kTiles];
-#pragma unroll
-                for (int i = 0; i < kTiles; ++i) p[i] = DT == FTQ_F16 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : acc[i][j];
 #pragma unroll
                 for (int c = 0; c < kPieces<DT>; ++c) {
                     const u32x4 u = *reinterpret_cast<const u32x4*>(&us[buf][((c * RT + j) * 16 + r16) * kULine + q * 16]);
 #pragma unroll
-                    for (int i = 0; i < kTiles; ++i) p[i] = multiply<DT>(x[i], u, p[i]);
-                }
+                    for (int h = 0; h < kParts<DT>; ++h) {
 #pragma unroll
-                for (int i = 0; i < kTiles; ++i) {
-                    if constexpr (DT == FTQ_F16) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(p[i][e], f, acc[i][j][e]);
-                    } else {
-                        acc[i][j] = p[i];
+                        for (int i = 0; i < kTiles; ++i) acc[i][j] = multiply<FTQ_BF16>(x[i][h], u, acc[i][j]);
                     }
                 }
             }
@@ -1068,13 +1046,13 @@ ForwardPlan plan_forward(int64_t L, int64_t R, int64_t K, int64_t pairs, int dty
 struct BackwardPlan {
     BucketPlan bucket;
     int64_t splits, run, runs_max;
-    int64_t off_part, off_g, off_ug, off_uh, off_backs, off_pa, off_pb, bytes;
+    int64_t off_part, off_g, off_ug, off_uh, off_pa, off_pb, bytes;
 };
 
 BackwardPlan plan_backward(int64_t L, int64_t R, int64_t K, int64_t N, int64_t pairs, int dtype)
 {
     BackwardPlan p;
-    const int64_t es = size_of(dtype), rt = 16 * rank_tiles(R), pieces = dtype == FTQ_F32 ? 2 : dtype == FTQ_F16 ? 2 : 3;
+    const int64_t es = size_of(dtype), rt = 16 * rank_tiles(R), pieces = dtype == FTQ_F32 ? 2 : 3;   // (of 16 bits)
     p.bucket = make_bucket_plan(pairs, L, kTile);
     p.splits = shrink_splits(pairs, N, R, dtype);
     // runs of tiles for as many workgroups as fit the chip at once (by LDS two on a CU, one of high ranks), at most a part
@@ -1092,7 +1070,6 @@ BackwardPlan plan_backward(int64_t L, int64_t R, int64_t K, int64_t N, int64_t p
     p.off_g = take(pairs * R * 4);
     p.off_ug = take(tiles * rt * kTile * 2 * pieces);
     p.off_uh = take(tiles * rt * kTile * 2 * pieces);
-    p.off_backs = take(2 * tiles * 4);
     p.off_pa = take(2 * p.runs_max * R * K * 4);
     p.off_pb = take(2 * p.runs_max * R * N * 4);
     p.bytes = off;
@@ -1222,9 +1199,8 @@ int run_lora_backward(const LoraBackwardArgs& m, void* ws, hipStream_t s)
     }
     // the R-vectors of the outer products, and g itself
     const int64_t tiles = plan.bucket.max_tiles;
-    const PiecesArgs pg{floats(plan.off_part), m.scale, m.d_x ? floats(plan.off_g) : nullptr, m.d_a ? mem + plan.off_ug : nullptr, floats(plan.off_backs),
-                        pairs, want_g ? tiles : 0, (int32_t)m.L, (int32_t)m.R, (int32_t)plan.splits};
-    const PiecesArgs ph{m.h, m.scale, nullptr, mem + plan.off_uh, floats(plan.off_backs) + tiles, pairs, m.d_b ? tiles : 0, (int32_t)m.L,
+    const PiecesArgs pg{floats(plan.off_part), m.scale, m.d_x ? floats(plan.off_g) : nullptr, m.d_a ? mem + plan.off_ug : nullptr, pairs, want_g ? tiles : 0, (int32_t)m.L, (int32_t)m.R, (int32_t)plan.splits};
+    const PiecesArgs ph{m.h, m.scale, nullptr, mem + plan.off_uh, pairs, m.d_b ? tiles : 0, (int32_t)m.L,
                         (int32_t)m.R, 1};
     st = launch_pieces(m.dtype, rt, tab, pg, ph, s);
     if (st != FTQ_OK) return st;
@@ -1251,13 +1227,13 @@ int run_lora_backward(const LoraBackwardArgs& m, void* ws, hipStream_t s)
         if (st != FTQ_OK) return st;
     }
     if (!m.d_a && !m.d_b) return FTQ_OK;
-    const auto outer = [&](int64_t off_u, int64_t backs, const void* v, int64_t ldv, int64_t off_part, float* d, int64_t C, int64_t div, bool by_column) {
+    const auto outer = [&](int64_t off_u, const void* v, int64_t ldv, int64_t off_part, float* d, int64_t C, int64_t div, bool by_column) {
         const int64_t col_items = ceil_div(C * es, 512);
-        return OuterArgs{mem + off_u, floats(plan.off_backs) + backs, static_cast<const uint8_t*>(v), ldv * es, floats(off_part), d, C, col_items,
+        return OuterArgs{mem + off_u, static_cast<const uint8_t*>(v), ldv * es, floats(off_part), d, C, col_items,
                          d ? plan.runs_max * col_items : 0, (int32_t)div, (int32_t)m.L, (int32_t)m.R, by_column, (int32_t)plan.run};
     };
-    st = launch_outer(m.dtype, rt, tab, outer(plan.off_ug, 0, m.x, m.ldx, plan.off_pa, m.d_a, m.K, m.act_div, false),
-                      outer(plan.off_uh, tiles, m.d_out, m.ld_d, plan.off_pb, m.d_b, m.N, 1, true), s);
+    st = launch_outer(m.dtype, rt, tab, outer(plan.off_ug, m.x, m.ldx, plan.off_pa, m.d_a, m.K, m.act_div, false),
+                      outer(plan.off_uh, m.d_out, m.ld_d, plan.off_pb, m.d_b, m.N, 1, true), s);
     if (st != FTQ_OK) return st;
     return reduce(tab.tiles, plan.run, floats(plan.off_pa), floats(plan.off_pb));
 }

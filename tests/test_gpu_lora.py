@@ -269,6 +269,89 @@ def test_backward_against_differences(per_pair):
         assert abs(want - float(terms.sum())) <= 1e-5 * float(terms.abs().sum()), n
 
 
+# ranks (or pairs) in four classes of far different size; values of 16 bits hold 2^-24 beside 1 only with fewer bits, so that
+# those of a, b and x are a factor of 2^24 apart at most and fp32's h further
+FAR = (2.0 ** 12, 2.0 ** 4, 2.0 ** -4, 2.0 ** -12)
+FAR_H = (1.0, 2.0 ** -20, 2.0 ** -24, 2.0 ** -30)
+
+
+def by_class(n, factors):
+    return torch.tensor([factors[i % 4] for i in range(n)], device="cuda")
+
+
+def apart(n, m):
+    """[n, m] of ones where both indices are of one class, else zeros."""
+    return (torch.arange(n, device="cuda")[:, None] % 4 == torch.arange(m, device="cuda")[None] % 4).float()
+
+
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_results_of_ranks_of_far_different_size(dtype, path):
+    """A result owes nothing to the ranks that its own weights leave out, however large their values in h."""
+    for R in (8, 32, 64, 128):
+        c = make(2, R, 136, 264, 70, 1, dtype, "f32", none=0.1, base=False)
+        c["a"] = (c["a"].float() * by_class(R, FAR)[:, None]).to(t.DTYPES[dtype])
+        c["b"] = (c["b"].float() * apart(264, R)).to(t.DTYPES[dtype])
+        y, h = forward(c, "f32", path)
+        ro, rh, mo, mh = t.lora_forward(c["x"], c["a"], c["b"], c["ids"], c["scale"], None, False)
+        for q in range(4):
+            t.close(h[:, q::4], rh[:, q::4], mh[:, q::4], 136 + 4, f"h of class {q}")
+            t.close(y[:, q::4], ro[:, q::4], mo[:, q::4], 136 + R + 8, f"out of class {q}")
+
+
+def backward_by_class(c, h, ways, per_pair=False):
+    """Gradients compared class by class, where ways[name] is the dimension that the classes lie along."""
+    K, N, most = c["a"].shape[2], c["b"].shape[1], c["ids"].numel()
+    got = backward(c, h, per_pair)
+    ref = t.lora_backward(c["dy"], c["x"], c["a"], c["b"], c["ids"], h, c["scale"], None, per_pair)
+    terms = {"d_x": N + c["ids"].shape[1] * c["a"].shape[1] + 10, "d_a": N + most + 10, "d_b": most + 10}
+    for n, dim in ways.items():
+        for q in range(4):
+            at = [slice(None)] * ref[n][0].dim()
+            at[dim] = slice(q, None, 4)
+            at = tuple(at)
+            t.close(got[n][at], ref[n][0][at], ref[n][1][at], terms[n], f"{n} of class {q}")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("R", [8, 24, 64, 128])
+def test_gradients_of_ranks_of_far_different_size(R, dtype):
+    """A rank's gradient is a sum of its own values of g or h: however small beside the other ranks', they keep fp32's bits."""
+    c = make(2, R, 136, 264, 90, 1, dtype, "f32", none=0.1)
+    c["b"] = (c["b"].float() * by_class(R, FAR)).to(t.DTYPES[dtype])
+    c["a"] = (c["a"].float() * apart(R, 136)).to(t.DTYPES[dtype])
+    h = torch.randn(90, R, generator=torch.Generator().manual_seed(R)).cuda() * by_class(R, FAR_H)
+    backward_by_class(c, h, {"d_x": 1, "d_a": 1, "d_b": 2})
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_gradients_of_pairs_of_far_different_size(dtype):
+    """The columns that only small pairs reach, beside large pairs of the same adapter."""
+    c = make(1, 16, 136, 264, 90, 1, dtype, "f32", none=0.0)
+    c["dy"] = (c["dy"].float() * by_class(90, FAR)[:, None]).to(t.DTYPES[dtype])
+    c["x"] = (c["x"].float() * apart(90, 136)).to(t.DTYPES[dtype])
+    h = torch.randn(90, 16, generator=torch.Generator().manual_seed(1)).cuda()
+    backward_by_class(c, h, {"d_a": 2})
+    c = make(1, 16, 136, 264, 90, 1, dtype, "f32", none=0.0)
+    c["dy"] = (c["dy"].float() * apart(90, 264)).to(t.DTYPES[dtype])
+    backward_by_class(c, h * by_class(90, FAR_H)[:, None], {"d_b": 1})
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_infinity_of_one_rank_stays_in_it(dtype):
+    c = make(3, 16, 136, 264, 61, 1, dtype, "f32", none=0.1)
+    h = torch.randn(61, 16, generator=torch.Generator().manual_seed(1)).cuda() * by_class(16, (1e5, 1.0, 1e-3, 1e-6))
+    want = backward(c, h)
+    dirty, hd = {n: v.clone() for n, v in c.items()}, h.clone()
+    hd[int((c["ids"][:, 0] == 1).nonzero()[0]), 5] = float("inf")
+    dirty["b"][1, 7, 3] = float("inf")
+    got = backward(dirty, hd)
+    ranks = torch.arange(16, device="cuda")
+    assert not got["d_b"][1][:, 5].isfinite().any() and torch.equal(got["d_b"][1][:, ranks != 5], want["d_b"][1][:, ranks != 5])
+    assert not got["d_a"][1][3].isfinite().any() and torch.equal(got["d_a"][1][ranks != 3], want["d_a"][1][ranks != 3])
+    assert torch.equal(got["d_a"][[0, 2]], want["d_a"][[0, 2]]) and torch.equal(got["d_b"][[0, 2]], want["d_b"][[0, 2]])
+
+
 def test_same_bits_again():
     c = make(3, 16, 264, 136, 700, 2, "bf16", "f32")
     first, h = forward(c, "f32", ftq.PATH_AUTO)

@@ -733,6 +733,7 @@ struct OuterArgs {
     int64_t C, col_items, items;
     int32_t div, L, R, by_column;
     int32_t run;               // tiles of a workgroup
+    const float* scale;        // [L]: what an adapter's sums are multiplied by, or null (1)
 };
 
 constexpr int kBatch = 32;                             // tiles listed in LDS
@@ -764,12 +765,13 @@ __global__ __launch_bounds__(kThreads) void lora_outer_kernel(OuterTables tab, O
     __shared__ __attribute__((aligned(16))) uint8_t vs[kDeep][kTile][512];
     __shared__ __attribute__((aligned(16))) uint8_t us[kDeep][kUBytes];
     __shared__ int32_t row_lds[kBatch * kTile], id_lds[kBatch + 1];
+    __shared__ float scale_lds[kBatch];
     const bool second = (int64_t)blockIdx.x >= a0.items;
     // (field by field: a selected struct would be read from memory in the loop, and such a read waits for the copies)
-    const struct { const uint8_t *u, *v; float *part, *d; int64_t ldv, C, col_items; int32_t div, L, R, by_column, run; } m = {
+    const struct { const uint8_t *u, *v; float *part, *d; int64_t ldv, C, col_items; int32_t div, L, R, by_column, run; const float* scale; } m = {
         second ? a1.u : a0.u, second ? a1.v : a0.v, second ? a1.part : a0.part, second ? a1.d : a0.d,
         second ? a1.ldv : a0.ldv, second ? a1.C : a0.C, second ? a1.col_items : a0.col_items, second ? a1.div : a0.div, a0.L, a0.R,
-        second ? a1.by_column : a0.by_column, a0.run};
+        second ? a1.by_column : a0.by_column, a0.run, second ? a1.scale : a0.scale};
     const int64_t item = second ? blockIdx.x - a0.items : blockIdx.x;
     const int lane = threadIdx.x & 63, wave = uniform((int32_t)(threadIdx.x >> 6));
     const int r16 = lane & 15, q = lane >> 4;
@@ -789,7 +791,10 @@ __global__ __launch_bounds__(kThreads) void lora_outer_kernel(OuterTables tab, O
         const int4 d = tab.tdesc[b0 + i / kTile];
         const int s = i % kTile;
         row_lds[i] = s < d.z ? tab.sorted[d.y + s] / m.div : -1;
-        if (s == 0) id_lds[i / kTile] = d.x;
+        if (s == 0) {
+            id_lds[i / kTile] = d.x;
+            scale_lds[i / kTile] = m.scale ? m.scale[d.x] : 1.0f;
+        }
     }
     if (threadIdx.x == 0) id_lds[count] = b0 + count < t1 ? tab.tdesc[b0 + count].x : -1;
     block_barrier();
@@ -815,6 +820,7 @@ __global__ __launch_bounds__(kThreads) void lora_outer_kernel(OuterTables tab, O
         wait_step<kPer, kDeep - 2>(count - 1 - i0);
         block_barrier();                                           // all waves' copies of the tile are there, the last one has been read
         const int32_t l = uniform(id_lds[i0]), after = uniform(id_lds[i0 + 1]);
+        const float scale = scale_lds[i0];
         if (i0 + kDeep - 1 < count) copy_tile(i0 + kDeep - 1);
         if constexpr (DT == FTQ_F32) {
 #pragma unroll
@@ -873,9 +879,9 @@ __global__ __launch_bounds__(kThreads) void lora_outer_kernel(OuterTables tab, O
                 if (c < m.C && r < m.R) {
                     if (m.by_column) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) to[(c + e) * m.R + r] = acc[i][j][e];
+                        for (int e = 0; e < 4; ++e) to[(c + e) * m.R + r] = acc[i][j][e] * scale;
                     } else {
-                        *reinterpret_cast<f32x4*>(to + r * m.C + c) = acc[i][j];
+                        *reinterpret_cast<f32x4*>(to + r * m.C + c) = acc[i][j] * scale;
                     }
                 }
                 acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -1200,7 +1206,7 @@ int run_lora_backward(const LoraBackwardArgs& m, void* ws, hipStream_t s)
     // the R-vectors of the outer products, and g itself
     const int64_t tiles = plan.bucket.max_tiles;
     const PiecesArgs pg{floats(plan.off_part), m.scale, m.d_x ? floats(plan.off_g) : nullptr, m.d_a ? mem + plan.off_ug : nullptr, pairs, want_g ? tiles : 0, (int32_t)m.L, (int32_t)m.R, (int32_t)plan.splits};
-    const PiecesArgs ph{m.h, m.scale, nullptr, mem + plan.off_uh, pairs, m.d_b ? tiles : 0, (int32_t)m.L,
+    const PiecesArgs ph{m.h, nullptr, nullptr, mem + plan.off_uh, pairs, m.d_b ? tiles : 0, (int32_t)m.L,
                         (int32_t)m.R, 1};
     st = launch_pieces(m.dtype, rt, tab, pg, ph, s);
     if (st != FTQ_OK) return st;
@@ -1227,13 +1233,13 @@ int run_lora_backward(const LoraBackwardArgs& m, void* ws, hipStream_t s)
         if (st != FTQ_OK) return st;
     }
     if (!m.d_a && !m.d_b) return FTQ_OK;
-    const auto outer = [&](int64_t off_u, const void* v, int64_t ldv, int64_t off_part, float* d, int64_t C, int64_t div, bool by_column) {
+    const auto outer = [&](int64_t off_u, const void* v, int64_t ldv, int64_t off_part, float* d, int64_t C, int64_t div, bool by_column, const float* scale) {
         const int64_t col_items = ceil_div(C * es, 512);
         return OuterArgs{mem + off_u, static_cast<const uint8_t*>(v), ldv * es, floats(off_part), d, C, col_items,
-                         d ? plan.runs_max * col_items : 0, (int32_t)div, (int32_t)m.L, (int32_t)m.R, by_column, (int32_t)plan.run};
+                         d ? plan.runs_max * col_items : 0, (int32_t)div, (int32_t)m.L, (int32_t)m.R, by_column, (int32_t)plan.run, scale};
     };
-    st = launch_outer(m.dtype, rt, tab, outer(plan.off_ug, m.x, m.ldx, plan.off_pa, m.d_a, m.K, m.act_div, false),
-                      outer(plan.off_uh, m.d_out, m.ld_d, plan.off_pb, m.d_b, m.N, 1, true), s);
+    st = launch_outer(m.dtype, rt, tab, outer(plan.off_ug, m.x, m.ldx, plan.off_pa, m.d_a, m.K, m.act_div, false, nullptr),
+                      outer(plan.off_uh, m.d_out, m.ld_d, plan.off_pb, m.d_b, m.N, 1, true, m.scale), s);
     if (st != FTQ_OK) return st;
     return reduce(tab.tiles, plan.run, floats(plan.off_pa), floats(plan.off_pb));
 }

@@ -352,6 +352,18 @@ def test_infinity_of_one_rank_stays_in_it(dtype):
     assert torch.equal(got["d_a"][[0, 2]], want["d_a"][[0, 2]]) and torch.equal(got["d_b"][[0, 2]], want["d_b"][[0, 2]])
 
 
+@pytest.mark.parametrize("size", [3.4e38, 2.0 ** -100])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_r_vectors_at_the_ends_of_32_bits(dtype, size):
+    c = make(2, 8, 64, 72, 40, 1, dtype, "f32", none=0.1)
+    c["dy"] = (c["dy"].float() * 2.0 ** -12).to(t.DTYPES[dtype])
+    h = size * (0.5 + 0.5 * torch.rand(40, 8, generator=torch.Generator().manual_seed(1))).cuda()
+    got = backward(c, h)["d_b"]
+    assert got.isfinite().all()
+    ref, mag = t.lora_backward(c["dy"], c["x"], c["a"], c["b"], c["ids"], h, c["scale"], None, False)["d_b"]
+    t.close(got, ref, mag, 40 + 10, "d_b")
+
+
 def test_same_bits_again():
     c = make(3, 16, 264, 136, 700, 2, "bf16", "f32")
     first, h = forward(c, "f32", ftq.PATH_AUTO)

@@ -70,6 +70,18 @@ int launch(const char* name, void (*kernel)(KArgs...), int64_t grid, int block, 
     return FTQ_OK;
 }
 
+// More workgroups than a launch takes are several launches: go(first, count) issues those from workgroup `first` on.
+template <typename F>
+int launch_in_turn(int64_t groups, int block, F go)
+{
+    const int64_t most = (int64_t(1) << 30) / block;   // (a multiple of the chip's 8 XCDs, which workgroups go round)
+    for (int64_t first = 0; first < groups; first += most) {
+        const int st = go(first, groups - first < most ? groups - first : most);
+        if (st != FTQ_OK) return st;
+    }
+    return FTQ_OK;
+}
+
 // Number of workgroups for a grid-stride kernel: enough to fill the device
 // several times over, never more than the work needs.
 int64_t stride_grid(int64_t work_groups_needed, const DeviceLimits& lim, int per_cu = 16);

@@ -177,7 +177,7 @@ constexpr int kDepth = 4;      // pieces in LDS: one is multiplied while three a
 // rank, in 16 bits by transposing reads of four columns x 16 ranks.  The columns' places and
 // runs are permuted so that the 16 columns of such a read lie side by side and meet no bank twice.
 template <int DT, int WAVES, int RT, bool COLS>
-__global__ __launch_bounds__(64 * WAVES) void lora_shrink_kernel(ShrinkArgs m)
+__global__ __launch_bounds__(64 * WAVES) void lora_shrink_kernel(ShrinkArgs m, int64_t first_item)
 {
     constexpr int kRuns = RT * kSize<DT>;                          // 16-byte runs of a column's ranks
     constexpr int kSpread = RT == 8 ? 0 : RT == 4 ? 1 : RT == 2 ? 2 : 3;
@@ -190,7 +190,7 @@ __global__ __launch_bounds__(64 * WAVES) void lora_shrink_kernel(ShrinkArgs m)
     __shared__ u32x4 ws[kDepth][16 * RT][8];
     const int lane = threadIdx.x & 63, wave = uniform((int32_t)(threadIdx.x >> 6));
     const int r16 = lane & 15, q = lane >> 4;
-    const int64_t item = blockIdx.x, at = item / m.splits;
+    const int64_t item = first_item + blockIdx.x, at = item / m.splits;
     const int ks = (int)(item - at * m.splits), g = (int)(at % m.groups);
     int64_t slot0;
     int rows;
@@ -377,7 +377,7 @@ __device__ __forceinline__ float swap_pair(float v)
 // KST: 64-byte steps of an R-vector.  RANKS: the weights lie by rank, [R][C], also in LDS, and
 // 16-bit ones are read by transposing reads of four ranks x 16 columns.
 template <int DT, int OT, int KST, bool RANKS, int WR>
-__global__ __launch_bounds__(kThreads) void lora_expand_kernel(ExpandArgs m)
+__global__ __launch_bounds__(kThreads) void lora_expand_kernel(ExpandArgs m, int64_t first_item)
 {
     constexpr int kElems = 64 / kSize<DT>, kOwn = 16 / kSize<DT>;  // ranks of a step, and a lane's of them
     constexpr bool kWide = OT == FTQ_F32;
@@ -393,7 +393,7 @@ __global__ __launch_bounds__(kThreads) void lora_expand_kernel(ExpandArgs m)
     __shared__ __attribute__((aligned(16))) uint8_t wl[kLds ? kParts<DT> * kPlane : 16];
     const int lane = threadIdx.x & 63, wave = uniform((int32_t)(threadIdx.x >> 6)), r16 = lane & 15, q = lane >> 4;
     const bool odd = r16 & 1;
-    const int64_t item = blockIdx.x, at = item / m.col_items;
+    const int64_t item = first_item + blockIdx.x, at = item / m.col_items;
     const int64_t c_first = (item - at * m.col_items) * m.cols, c_end = min(c_first + m.cols, m.C);
     const int g = (int)(at % m.groups);
     int64_t slot0;
@@ -617,13 +617,13 @@ struct GatherArgs {
 constexpr int kXcds = 8, kGatherTokens = 4;            // tokens of a workgroup, one a wave
 
 template <int DT>
-__global__ __launch_bounds__(kThreads) void lora_gather_kernel(GatherArgs m)
+__global__ __launch_bounds__(kThreads) void lora_gather_kernel(GatherArgs m, int64_t first_item)
 {
     constexpr int kCols = 16 / kSize<DT>;
     const int lane = threadIdx.x & 63, wave = uniform((int32_t)(threadIdx.x >> 6));
     const int64_t total = m.slices * m.groups, per = (total + kXcds - 1) / kXcds;
-    const int64_t item = blockIdx.x % kXcds * per + blockIdx.x / kXcds;
-    if (item >= total || blockIdx.x / kXcds >= per) return;
+    const int64_t at = first_item + blockIdx.x, item = at % kXcds * per + at / kXcds;   // (first_item: whole rounds of the XCDs)
+    if (item >= total || at / kXcds >= per) return;
     const int64_t slice = item / m.groups, t = (item - slice * m.groups) * kGatherTokens + wave;
     const int64_t c = slice * 64 * kCols + lane * kCols;
     if (t >= m.T || c >= m.C) return;
@@ -680,12 +680,13 @@ struct PiecesArgs {
 
 // One workgroup per tile (of either set of vectors): thread h has pair h%32 and every eighth group of four ranks from h/32 on.
 template <int DT, int RT>
-__global__ __launch_bounds__(kThreads) void lora_pieces_kernel(OuterTables tab, PiecesArgs a0, PiecesArgs a1)
+__global__ __launch_bounds__(kThreads) void lora_pieces_kernel(OuterTables tab, PiecesArgs a0, PiecesArgs a1, int64_t first_item)
 {
     constexpr int kQuads = 4 * RT, kMine = (kQuads + 7) / 8;
-    const bool second = (int64_t)blockIdx.x >= a0.max_tiles;
+    const int64_t item = first_item + blockIdx.x;
+    const bool second = item >= a0.max_tiles;
     const PiecesArgs m = second ? a1 : a0;
-    const int64_t t = second ? blockIdx.x - a0.max_tiles : blockIdx.x;
+    const int64_t t = second ? item - a0.max_tiles : item;
     if (t >= tab.tiles[m.L + 1]) return;
     const int4 d = tab.tdesc[t];
     const int s = threadIdx.x % kTile, q0 = threadIdx.x / kTile;
@@ -754,7 +755,7 @@ __device__ __forceinline__ void wait_step(int left)
 }
 
 template <int DT, int RT>
-__global__ __launch_bounds__(kThreads) void lora_outer_kernel(OuterTables tab, OuterArgs a0, OuterArgs a1)
+__global__ __launch_bounds__(kThreads) void lora_outer_kernel(OuterTables tab, OuterArgs a0, OuterArgs a1, int64_t first_item)
 {
     constexpr int kCols = 512 / kSize<DT>, kTiles = kCols / 64;    // columns of a workgroup, 16-column tiles of a wave
     constexpr int kULine = kTile * kSize<DT>;                      // bytes of a rank's row of u
@@ -766,13 +767,14 @@ __global__ __launch_bounds__(kThreads) void lora_outer_kernel(OuterTables tab, O
     __shared__ __attribute__((aligned(16))) uint8_t us[kDeep][kUBytes];
     __shared__ int32_t row_lds[kBatch * kTile], id_lds[kBatch + 1];
     __shared__ float scale_lds[kBatch];
-    const bool second = (int64_t)blockIdx.x >= a0.items;
+    const int64_t at_item = first_item + blockIdx.x;
+    const bool second = at_item >= a0.items;
     // (field by field: a selected struct would be read from memory in the loop, and such a read waits for the copies)
     const struct { const uint8_t *u, *v; float *part, *d; int64_t ldv, C, col_items; int32_t div, L, R, by_column, run; const float* scale; } m = {
         second ? a1.u : a0.u, second ? a1.v : a0.v, second ? a1.part : a0.part, second ? a1.d : a0.d,
         second ? a1.ldv : a0.ldv, second ? a1.C : a0.C, second ? a1.col_items : a0.col_items, second ? a1.div : a0.div, a0.L, a0.R,
         second ? a1.by_column : a0.by_column, a0.run, second ? a1.scale : a0.scale};
-    const int64_t item = second ? blockIdx.x - a0.items : blockIdx.x;
+    const int64_t item = second ? at_item - a0.items : at_item;
     const int lane = threadIdx.x & 63, wave = uniform((int32_t)(threadIdx.x >> 6));
     const int r16 = lane & 15, q = lane >> 4;
     const int64_t chunk = item / m.col_items, col0 = (item - chunk * m.col_items) * kCols;
@@ -965,7 +967,9 @@ int by_type(int dtype, F f)
 template <int DT, int WAVES, bool COLS>
 int launch_shrink(const ShrinkArgs& m, int64_t grid, hipStream_t s)
 {
-    const auto go = [&](auto* kernel) { return launch("lora_shrink_kernel", kernel, grid, 64 * WAVES, 0, s, m); };
+    const auto go = [&](auto* kernel) {
+        return launch_in_turn(grid, 64 * WAVES, [&](int64_t first, int64_t n) { return launch("lora_shrink_kernel", kernel, n, 64 * WAVES, 0, s, m, first); });
+    };
     switch (rank_tiles(m.R)) {
         case 1: return go(lora_shrink_kernel<DT, WAVES, 1, COLS>);
         case 2: return go(lora_shrink_kernel<DT, WAVES, 2, COLS>);
@@ -994,7 +998,9 @@ int run_shrink(int dtype, ShrinkArgs m, hipStream_t s)
 template <int DT, int OT, bool RANKS, int WR>
 int launch_expand(const ExpandArgs& m, int64_t grid, hipStream_t s)
 {
-    const auto go = [&](auto* kernel) { return launch("lora_expand_kernel", kernel, grid, kThreads, 0, s, m); };
+    const auto go = [&](auto* kernel) {
+        return launch_in_turn(grid, kThreads, [&](int64_t first, int64_t n) { return launch("lora_expand_kernel", kernel, n, kThreads, 0, s, m, first); });
+    };
     const int rt = rank_tiles(m.R);
     if constexpr (DT == FTQ_F32) {
         if (rt == 1) return go(lora_expand_kernel<DT, OT, 1, RANKS, WR>);
@@ -1086,7 +1092,10 @@ int launch_pieces(int dtype, int rt, const OuterTables& tab, const PiecesArgs& a
 {
     return by_type(dtype, [&](auto dt) {
         constexpr int DT = decltype(dt)::value;
-        const auto go = [&](auto* kernel) { return launch("lora_pieces_kernel", kernel, a.max_tiles + b.max_tiles, kThreads, 0, s, tab, a, b); };
+        const auto go = [&](auto* kernel) {
+            return launch_in_turn(a.max_tiles + b.max_tiles, kThreads,
+                                  [&](int64_t first, int64_t n) { return launch("lora_pieces_kernel", kernel, n, kThreads, 0, s, tab, a, b, first); });
+        };
         if (rt == 1) return go(lora_pieces_kernel<DT, 1>);
         if (rt == 2) return go(lora_pieces_kernel<DT, 2>);
         if (rt == 4) return go(lora_pieces_kernel<DT, 4>);
@@ -1098,7 +1107,10 @@ int launch_outer(int dtype, int rt, const OuterTables& tab, const OuterArgs& a, 
 {
     return by_type(dtype, [&](auto dt) {
         constexpr int DT = decltype(dt)::value;
-        const auto go = [&](auto* kernel) { return launch("lora_outer_kernel", kernel, a.items + b.items, kThreads, 0, s, tab, a, b); };
+        const auto go = [&](auto* kernel) {
+            return launch_in_turn(a.items + b.items, kThreads,
+                                  [&](int64_t first, int64_t n) { return launch("lora_outer_kernel", kernel, n, kThreads, 0, s, tab, a, b, first); });
+        };
         if (rt == 1) return go(lora_outer_kernel<DT, 1>);
         if (rt == 2) return go(lora_outer_kernel<DT, 2>);
         if (rt == 4) return go(lora_outer_kernel<DT, 4>);
@@ -1229,7 +1241,11 @@ int run_lora_backward(const LoraBackwardArgs& m, void* ws, hipStream_t s)
         GatherArgs gather{floats(plan.off_g), static_cast<const uint8_t*>(m.a), m.ids, static_cast<const uint8_t*>(m.base), static_cast<uint8_t*>(m.d_x),
                           m.T, m.K, ceil_div(m.K * es, 1024), ceil_div(m.T, kGatherTokens), (int32_t)m.L, (int32_t)m.R, (int32_t)m.top_k};
         const int64_t grid = ceil_div(gather.slices * gather.groups, kXcds) * kXcds;
-        st = by_type(m.dtype, [&](auto dt) { return launch("lora_gather_kernel", lora_gather_kernel<decltype(dt)::value>, grid, kThreads, 0, s, gather); });
+        st = by_type(m.dtype, [&](auto dt) {
+            return launch_in_turn(grid, kThreads, [&](int64_t first, int64_t n) {
+                return launch("lora_gather_kernel", lora_gather_kernel<decltype(dt)::value>, n, kThreads, 0, s, gather, first);
+            });
+        });
         if (st != FTQ_OK) return st;
     }
     if (!m.d_a && !m.d_b) return FTQ_OK;

@@ -1,0 +1,97 @@
+"""Calls of more workgroups than one launch takes: sequences, pairs and rows up to
+the documented limits.  Most rows are zeros, so that what the others give can be told
+from a call on those alone."""
+import pytest
+import torch
+
+from quantized_moe_expert_quantize_amd import ftq
+from tests import _train as t
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def memory():
+    torch.cuda.empty_cache()
+    yield
+    torch.cuda.empty_cache()
+
+
+def spread(n, more=2000):
+    """Ascending indices below n: the first ones, the last ones and some between."""
+    g = torch.Generator().manual_seed(n)
+    at = torch.cat([torch.arange(40), torch.randint(0, n, (more,), generator=g), torch.arange(n - 40, n)])
+    return torch.unique(at).cuda()
+
+
+def nonzero_rows(v, step=1 << 26):
+    return sum(int((part != 0).any(1).sum()) for part in v.split(step))
+
+
+def adapters(L, R, K, N, pairs):
+    g = torch.Generator().manual_seed(1)
+    at = spread(pairs)
+    a, b = torch.randn(L, R, K, generator=g).half().cuda(), torch.randn(L, N, R, generator=g).half().cuda()
+    ids = torch.randint(-1, L, (len(at), 1), generator=g).to(torch.int32).cuda()
+    all_ids = (torch.arange(pairs, dtype=torch.int32, device="cuda") % L).view(pairs, 1)
+    all_ids[at] = ids
+    return g, at, a, b, ids, all_ids
+
+
+def scattered(pairs, columns, at, rows):
+    v = torch.zeros(pairs, columns, dtype=rows.dtype, device="cuda")
+    v[at] = rows
+    return v
+
+
+@pytest.mark.parametrize("path", [ftq.PATH_GEMV, ftq.PATH_GROUPED])
+def test_adapters_of_a_thousand_million_pairs(path):
+    L, R, K, N, pairs = 3, 8, 8, 8, (1 << 30) + 5000
+    print(f"[lora] pairs={pairs} path={path}", flush=True)
+    g, at, a, b, ids, all_ids = adapters(L, R, K, N, pairs)
+    few = torch.randn(len(at), K, generator=g).half().cuda()
+    x = scattered(pairs, K, at, few)
+    out = ftq.lora(x, a, b, all_ids, path=path)
+    want = ftq.lora(few, a, b, ids, path=path)
+    assert torch.equal(out[at], want) and nonzero_rows(out) == nonzero_rows(want)
+
+
+def test_gradients_of_hundreds_of_millions_of_pairs():
+    L, R, K, N, pairs = 3, 8, 8, 8, (1 << 28) + 5000
+    print(f"[lora_backward] pairs={pairs}", flush=True)
+    g, at, a, b, ids, all_ids = adapters(L, R, K, N, pairs)
+    dy, x = (torch.randn(len(at), c, generator=g).half().cuda() for c in (N, K))
+    h = torch.randn(len(at), R, generator=g).cuda()
+    d_x, d_a, d_b = ftq.lora_backward(scattered(pairs, N, at, dy), scattered(pairs, K, at, x), a, b, all_ids, scattered(pairs, R, at, h))
+    want = ftq.lora_backward(dy, x, a, b, ids, h)
+    assert torch.equal(d_x[at], want[0]) and nonzero_rows(d_x) == nonzero_rows(want[0])
+    ref = t.lora_backward(dy, x, a, b, ids, h, None, None, False)
+    t.close(d_a, *ref["d_a"], N + len(at) + 10, "d_a")
+    t.close(d_b, *ref["d_b"], len(at) + 10, "d_b")
+
+
+def test_gradients_of_rows_that_pairs_share():
+    """d_x alone, of 64 slices of columns and more than 2^20 tokens."""
+    L, R, K, N, T, k = 2, 8, 32768, 8, (1 << 20) + 300, 2
+    print(f"[lora_backward] T={T} K={K}", flush=True)
+    g = torch.Generator().manual_seed(1)
+    at = spread(T)
+    a, b = (torch.randn(L, R, K, generator=g) / 8).bfloat16().cuda(), torch.randn(L, N, R, generator=g).bfloat16().cuda()
+    ids = torch.randint(-1, L, (T, k), generator=g).to(torch.int32).cuda()
+    few_ids = ids[at].contiguous()
+    few = torch.randn(len(at), k, N, generator=g).bfloat16().cuda()
+    dy = torch.zeros(T, k, N, dtype=torch.bfloat16, device="cuda")
+    dy[at] = few
+
+    def call(dy, ids):
+        T = len(ids)
+        d_x = torch.full((T, K), float("nan"), dtype=torch.bfloat16, device="cuda")
+        need = ftq.lora_backward_workspace_bytes(L, R, K, N, T, k, torch.bfloat16)
+        ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+        st = ftq.lib().ftq_lora_backward(dy.data_ptr(), N, None, K, a.data_ptr(), b.data_ptr(), None, ids.data_ptr(), None, None, d_x.data_ptr(),
+                                         None, None, ftq.BF16, L, R, K, N, T, k, 0, ws.data_ptr(), need, None)
+        assert st == ftq.OK, ftq.last_error()
+        torch.cuda.synchronize()
+        return d_x
+    want, got = call(few, few_ids), call(dy, ids)
+    assert torch.equal(got[at], want) and nonzero_rows(got, 1 << 17) == nonzero_rows(want)

@@ -285,13 +285,13 @@ __global__ __launch_bounds__(ALONE ? kAloneThreads : kThreads) void balance_part
 constexpr int kSumThreads = 1024;
 
 __global__ __launch_bounds__(kSumThreads) void balance_sum_kernel(BalanceArgs m, int64_t chunk, const Part* __restrict__ parts,
-                                                                  const int32_t* __restrict__ part_n)
+                                                                  const int32_t* __restrict__ part_n, int64_t first)
 {
     __shared__ double p_lds[kSumThreads];
     __shared__ int32_t c_lds[kSumThreads];
     __shared__ double wave_lds[kSumThreads / 64];
     __shared__ int32_t n_lds;
-    const int64_t s = blockIdx.x;
+    const int64_t s = first + blockIdx.x;
     const int64_t begin = m.offsets ? max(m.offsets[s], 0) : 0, end = m.offsets ? min((int64_t)m.offsets[s + 1], m.T) : m.T;
     const int64_t c0 = begin / chunk, c1 = begin < end ? (end - 1) / chunk + 1 : c0;
     if (threadIdx.x == 0) n_lds = 0;
@@ -611,8 +611,10 @@ int run_balance(const BalanceArgs& m, void* ws, hipStream_t s)
         const int st = by_layout(m.dtype, m.score, m.E, PartsCall{m, p, parts, part_n, s});
         if (st != FTQ_OK || p.alone) return st;
     }
-    return launch("balance_sum_kernel", balance_sum_kernel, m.S, kSumThreads, 0, s, m, p.chunk, static_cast<const Part*>(parts),
-                  static_cast<const int32_t*>(part_n));
+    return launch_in_turn(m.S, kSumThreads, [&](int64_t first, int64_t n) {
+        return launch("balance_sum_kernel", balance_sum_kernel, n, kSumThreads, 0, s, m, p.chunk, static_cast<const Part*>(parts),
+                      static_cast<const int32_t*>(part_n), first);
+    });
 }
 
 int run_topk_backward(const TopkBackwardArgs& m, hipStream_t s)

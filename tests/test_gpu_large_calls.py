@@ -95,3 +95,25 @@ def test_gradients_of_rows_that_pairs_share():
         return d_x
     want, got = call(few, few_ids), call(dy, ids)
     assert torch.equal(got[at], want) and nonzero_rows(got, 1 << 17) == nonzero_rows(want)
+
+
+@pytest.mark.parametrize("T", [40, 3000])
+def test_millions_of_sequences(T):
+    S, E, k = (1 << 22) + 500, 3, 2
+    print(f"[balance] T={T} S={S}", flush=True)
+    g = torch.Generator().manual_seed(T)
+    logits, ids = torch.randn(T, E, generator=g), torch.randint(0, E, (T, k), generator=g).to(torch.int32)
+    cuts = torch.sort(torch.randint(0, T, (S + 1,), generator=g)).values.to(torch.int32)
+    cuts[0], cuts[-300:] = 0, T - 1                            # sequences of the last launch are empty but for one row, the last one's
+    cuts[-1] = T
+    loss, counts, tokens = ftq.moe_balance(logits.cuda(), ids.cuda(), offsets=cuts.cuda())
+    used = torch.unique(torch.searchsorted(cuts[1:].contiguous(), torch.arange(T, dtype=torch.int32), right=True))
+    few = torch.cat([cuts[used], cuts[-1:]])                   # the same rows in the sequences that hold any
+    want = ftq.moe_balance(logits.cuda(), ids.cuda(), offsets=few.cuda())
+    assert used[-1] == S - 1 and used[0] < S
+    at = used.cuda()
+    assert torch.equal(tokens[at], want[2]) and torch.equal(counts[at], want[1]) and int(tokens.sum()) == T and int(counts.sum()) == T * k
+    # sums cut into other chunks: the shares' roundings of either side, below 100 steps each
+    assert ((loss[at] - want[0]).abs() <= 2 * 2 * t.U * 100 * want[0]).all()
+    tokens[at] = 0
+    assert not tokens.any() and int((loss != 0).sum()) == len(used)

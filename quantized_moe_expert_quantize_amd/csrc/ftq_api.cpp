@@ -351,7 +351,15 @@ int check_lora_sizes(int dtype, int64_t L, int64_t R, int64_t K, int64_t N, int6
 }
 
 // A row stride of `cols` elements of `esz` bytes: at least cols, whole 16-byte units.
-bool stride_ok(int64_t ld, int64_t cols, int64_t esz) { return ld >= cols && ld <= INT64_MAX / 64 / kMaxPairs && ld * esz % 16 == 0; }
+bool stride_ok(int64_t ld, int64_t cols, int64_t esz) { return ld >= cols && ld % (16 / esz) == 0; }
+
+// Rows of these strides whose byte offsets fit 64 bits.
+int check_row_offsets(int64_t ld, int64_t rows)
+{
+    if (ld <= INT64_MAX / 64 / std::max<int64_t>(rows, 1)) return FTQ_OK;
+    set_error("%lld rows of stride %lld overflow 64-bit byte offsets", (long long)rows, (long long)ld);
+    return FTQ_ERR_UNSUPPORTED;
+}
 
 int check_lora_path(int path, int64_t L)
 {
@@ -770,6 +778,8 @@ int ftq_lora(const void* x, int64_t ldx, const void* a, const void* b, const flo
                   (long long)ld_base, (long long)ld_out);
         return FTQ_ERR_INVALID_ARG;
     }
+    st = check_row_offsets(std::max({ldx, ld_out, base ? ld_base : 0}), T * top_k);
+    if (st != FTQ_OK) return st;
     if (base && base == out && ld_base != ld_out) { set_error("out may be base only with the same row stride"); return FTQ_ERR_INVALID_ARG; }
     if (T == 0) return FTQ_OK;
     if (!x || !a || !b || !topk_ids || !out) { set_error("null pointer argument (x, a, b, topk_ids or out)"); return FTQ_ERR_INVALID_ARG; }
@@ -810,6 +820,8 @@ int ftq_lora_backward(const void* d_out, int64_t ld_d, const void* x, int64_t ld
         set_error("row strides must hold a row and be whole 16-byte units (d_out %lld, x %lld elements)", (long long)ld_d, (long long)ldx);
         return FTQ_ERR_INVALID_ARG;
     }
+    st = check_row_offsets(std::max(ld_d, d_a ? ldx : 0), T * top_k);
+    if (st != FTQ_OK) return st;
     if (T == 0 && !d_a && !d_b) return FTQ_OK;
     if (!d_x && !d_a && !d_b) { set_error("no output (d_x, d_a or d_b)"); return FTQ_ERR_INVALID_ARG; }
     if (T > 0 && (!d_out || !topk_ids || (d_a && !x) || (d_x && !a) || ((d_x || d_a) && !b) || (d_b && !h))) {

@@ -117,3 +117,50 @@ def test_millions_of_sequences(T):
     assert ((loss[at] - want[0]).abs() <= 2 * 2 * t.U * 100 * want[0]).all()
     tokens[at] = 0
     assert not tokens.any() and int((loss != 0).sum()) == len(used)
+
+
+def apart(v):
+    """The first, last and some other columns of v, which are the only ones that are not zero."""
+    v[..., spread(v.shape[-1])] = torch.randn(*v.shape[:-1], len(spread(v.shape[-1])), device="cuda").to(v.dtype)
+    return v
+
+
+def test_rows_of_more_than_2_26_elements():
+    wide, L, R, small, T = (1 << 26) + 1048, 2, 8, 64, 5
+    print(f"[lora] K, N of {wide} and {small}", flush=True)
+    ids, at = torch.tensor([[0], [1], [-1], [1], [0]], dtype=torch.int32, device="cuda"), spread(wide)
+    zeros = lambda *shape: torch.zeros(*shape, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    # wide rows: x and a
+    x, a, b = apart(zeros(T, wide)), apart(zeros(L, R, wide)), torch.randn(L, small, R, device="cuda").bfloat16()
+    h = torch.empty(T, R, device="cuda")
+    out = ftq.lora(x, a, b, ids, out_dtype=torch.float32, h=h)
+    few_x, few_a = x[:, at].contiguous(), a[:, :, at].contiguous()
+    ro, rh, mo, mh = t.lora_forward(few_x, few_a, b, ids, None, None, False)
+    t.close(h, rh, mh, len(at) + 4, "h")
+    t.close(out, ro, mo, len(at) + R + 8, "out")
+    dy = torch.randn(T, small, device="cuda").bfloat16()
+    d_x, d_a, d_b = ftq.lora_backward(dy, x, a, b, ids, h)
+    ref = t.lora_backward(dy, few_x, few_a, b, ids, h, None, None, False)
+    t.close(d_x[:, at], *ref["d_x"], small + R + 10, "d_x")
+    t.close(d_a[:, :, at], *ref["d_a"], small + T + 10, "d_a")
+    t.close(d_b, *ref["d_b"], T + 10, "d_b")
+    for v in (d_x, d_a):
+        v[..., at] = 0
+        assert not v.any()
+    del x, a, few_x, few_a, d_x, d_a
+    # wide results: b and d_out
+    x, a, b = torch.randn(T, small, device="cuda").bfloat16(), torch.randn(L, R, small, device="cuda").bfloat16(), zeros(L, wide, R)
+    b[:, at] = torch.randn(L, len(at), R, device="cuda").bfloat16()
+    out = ftq.lora(x, a, b, ids, h=h)
+    few_b, dy = b[:, at].contiguous(), apart(zeros(T, wide))
+    want = ftq.lora(x, a, torch.nn.functional.pad(few_b, (0, 0, 0, -len(at) % 8)), ids)[:, :len(at)]
+    assert torch.equal(out[:, at], want)
+    out[:, at] = 0
+    assert not out.any()
+    d_x, d_a, d_b = ftq.lora_backward(dy, x, a, b, ids, h)
+    ref = t.lora_backward(dy[:, at], x, a, few_b, ids, h, None, None, False)
+    t.close(d_x, *ref["d_x"], len(at) + R + 10, "d_x")
+    t.close(d_a, *ref["d_a"], len(at) + T + 10, "d_a")
+    t.close(d_b[:, at], *ref["d_b"], T + 10, "d_b")
+    d_b[:, at] = 0
+    assert not d_b.any()

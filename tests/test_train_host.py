@@ -139,3 +139,16 @@ def test_binding_refuses_host_tensors():
                  lambda: ftq.combine_topk_backward(x, x, torch.zeros(4, 1))):
         with pytest.raises(ValueError, match="GPU tensor"):
             call()
+
+
+def test_lora_takes_rows_of_any_length_below_2_31():
+    """Strides past 2^26 elements; refused only where offsets overflow.  (Without a workspace, which is asked for last.)"""
+    for wide in (2 ** 26 + 8, 2 ** 31 - 8):
+        for kw in (dict(K=wide, ldx=wide), dict(ldx=wide), dict(N=wide, ld_out=wide, ld_base=wide), dict(ld_out=2 ** 40, ld_base=2 ** 40)):
+            assert _call("ftq_lora", LORA, dict(kw, ws_n=0)) == ftq.ERR_WORKSPACE, kw
+        for kw in (dict(K=wide, ldx=wide), dict(ldx=wide), dict(N=wide, ld_d=wide), dict(ld_d=2 ** 40)):
+            assert _call("ftq_lora_backward", BACK, dict(kw, ws_n=0)) == ftq.ERR_WORKSPACE, kw
+    for kw in (dict(ldx=2 ** 60), dict(ld_out=2 ** 60), dict(ld_base=2 ** 60), dict(T=2 ** 30, ldx=2 ** 30)):
+        assert _call("ftq_lora", LORA, kw) == ftq.ERR_UNSUPPORTED, kw
+    for kw in (dict(ldx=2 ** 60), dict(ld_d=2 ** 60), dict(T=2 ** 30, ldx=2 ** 30)):
+        assert _call("ftq_lora_backward", BACK, kw) == ftq.ERR_UNSUPPORTED, kw

@@ -797,8 +797,8 @@ def lora(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, topk_ids: torch.Tens
          out_dtype: torch.dtype | None = None, h: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
          stream=None) -> torch.Tensor:
     """Low-rank adapters a [L, R, K], b [L, N, R] on the rows x [T or T*top_k, K] (may be strided): out [T*top_k, N] =
-    base + scale * b (a x) with the adapter that topk_ids [T, top_k] names (ids outside [0, L): base alone).  out may be
-    base itself; h (fp32 [T*top_k, R]) keeps a x for lora_backward (see ftq_lora)."""
+    base + scale * b (a x) with the adapter that topk_ids [T, top_k] names (ids outside [0, L): base alone), in base's type,
+    without one in out_dtype or else x's.  out may be base itself; h (fp32 [T*top_k, R]) keeps a x for lora_backward (see ftq_lora)."""
     dev = _device_for(x, "x")
     px, dt, ldx = _rows(x, "x", dev)
     (L, R, K, N, T, top_k), (pa, pb, ps, ids) = _adapters(x, a, b, topk_ids, per_pair, scale, dev)
@@ -806,6 +806,8 @@ def lora(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, topk_ids: torch.Tens
     pbase, dbase, ldbase = _rows(base, "base", dev) if base is not None else (None, None, 0)
     if out is None:
         out = _empty((pairs, N), base.dtype if base is not None else out_dtype or x.dtype, x.device, stream)
+    if out_dtype is not None and out_dtype != out.dtype:
+        raise ValueError(f"out is {out.dtype} (as base or the buffer given), out_dtype {out_dtype}")
     po, do, ldo = _rows(out, "out", dev)
     if out.shape != (pairs, N) or (base is not None and (base.shape != (pairs, N) or dbase != do)):
         raise ValueError(f"out and base must be {(pairs, N)} of one type")

@@ -104,6 +104,17 @@ def test_in_place_with_another_stride_is_refused():
     assert (buf[0, :8] == 66.0).all() and (buf[0, 8:] == 2.0).all()
 
 
+def test_an_out_dtype_that_base_or_out_has_not_is_refused():
+    x, a, b, ids = (torch.ones(4, 8).bfloat16().cuda(), torch.ones(1, 8, 8).bfloat16().cuda(), torch.ones(1, 8, 8).bfloat16().cuda(),
+                    torch.zeros(4, 1, dtype=torch.int32).cuda())
+    base = torch.ones(4, 8).bfloat16().cuda()
+    for kw in (dict(base=base), dict(out=base.clone()), dict(base=base, out=base)):
+        with pytest.raises(ValueError):
+            ftq.lora(x, a, b, ids, out_dtype=torch.float32, **kw)
+        assert ftq.lora(x, a, b, ids, out_dtype=torch.bfloat16, **kw).dtype == torch.bfloat16
+    assert ftq.lora(x, a, b, ids, out_dtype=torch.float32).dtype == torch.float32 and ftq.lora(x, a, b, ids).dtype == torch.bfloat16
+
+
 @pytest.mark.parametrize("path", PATHS)
 def test_rows_depend_on_their_own_inputs_alone(path):
     """NaN and infinities of one adapter or row stay with the pairs that use them; a pair alone has the same bits."""

@@ -811,8 +811,6 @@ def lora(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, topk_ids: torch.Tens
     po, do, ldo = _rows(out, "out", dev)
     if out.shape != (pairs, N) or (base is not None and (base.shape != (pairs, N) or dbase != do)):
         raise ValueError(f"out and base must be {(pairs, N)} of one type")
-    if base is not None and pbase == po and pairs <= 1:   # one row has no stride of its own
-        ldbase = ldo = max(ldbase, ldo)
     if workspace is None:
         need = lora_workspace_bytes(L, R, K, N, T, top_k, x.dtype, path)
         workspace = _empty(need, torch.uint8, x.device, stream) if need else None

@@ -74,9 +74,9 @@ def _route(ids_d, E, need, split):
     return ws.cpu().numpy()
 
 
-# (E, T, top_k, routing, masked): one chunk, ragged chunks, the 8-chunk limit
-# of the one-workgroup bucketing, one pair over it, Zipf routing, many experts
-# (up to the 2048-bucket limit and past it)
+# (E, T, top_k, routing, masked): one chunk, ragged chunks, 8192 pairs and some
+# more, batches that take the three kernels anyway, Zipf routing, many experts
+# (up to the 2048-bucket limit of the one-workgroup bucketing and past it)
 CASES = [
     (8, 100, 2, "uniform", False),
     (128, 64, 8, "uniform", False),
@@ -87,6 +87,21 @@ CASES = [
     (1024, 700, 4, "uniform", False),
     (2047, 1024, 4, "uniform", True),
     (4000, 300, 8, "uniform", True),
+]
+
+
+# The one-workgroup bucketing takes up to 12288 pairs, in chunks of 64, 128, ..
+# 1024 pairs, as short as 16 waves and 12288 counts (buckets x chunks) allow:
+# the edges of each chunk length, the last batch it takes and the first it does
+# not, the most counts (1024 buckets x 12 chunks) and the buckets for which no
+# chunk is long enough (2048 take 6 chunks, 6144 pairs; 1117 take 11, 11264).
+SMALL = [
+    (128, 1, 1, "uniform", False), (128, 63, 1, "uniform", True), (128, 1023, 1, "uniform", False), (128, 1025, 1, "uniform", True),
+    (128, 1536, 1, "zipf", False), (128, 2048, 1, "uniform", False), (128, 2049, 1, "uniform", True), (8, 4096, 1, "uniform", False),
+    (8, 4097, 1, "zipf", True), (8, 8193, 1, "uniform", False), (128, 1536, 8, "uniform", True), (128, 12287, 1, "uniform", True),
+    (128, 12288, 1, "zipf", False), (128, 12289, 1, "uniform", True), (1023, 1536, 8, "uniform", True), (1023, 12288, 1, "zipf", False),
+    (2047, 768, 8, "uniform", True), (2047, 6145, 1, "uniform", False), (2047, 1536, 8, "uniform", True), (1116, 11264, 1, "uniform", True),
+    (1116, 11265, 1, "uniform", True),
 ]
 
 
@@ -116,3 +131,8 @@ def test_one_workgroup_route_equals_three_kernels_and_host(case):
     assert np.array_equal(i32(lay["sorted"], T * k), order)
     assert len(desc) <= lay["max_tiles"]
     assert np.array_equal(i32(lay["tdesc"], 4 * len(desc)).reshape(-1, 4), desc)
+
+
+@pytest.mark.parametrize("case", SMALL, ids=lambda c: "E{}T{}k{}{}{}".format(c[0], c[1], c[2], c[3], "m" if c[4] else ""))
+def test_limits_of_the_one_workgroup_route(case):
+    test_one_workgroup_route_equals_three_kernels_and_host(case)

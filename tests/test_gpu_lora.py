@@ -200,6 +200,29 @@ def test_backward_of_many_rows(dtype):
     check_backward(c)
 
 
+@pytest.mark.parametrize("dtype,R", [("bf16", 8), ("f16", 16), ("f32", 8), ("bf16", 128), ("f16", 64)])
+def test_backward_of_long_runs(dtype, R):
+    """Runs of more than 32 tiles of 32 pairs, whose rows are listed 32 tiles at a time, with data in all of them: an adapter that ends inside a
+    list, one that ends with it, one over several lists and runs, one pair, none."""
+    K = N = 2048
+    counts = [20 * 32 + 5, 11 * 32, 500 * 32 + 7, 0, 1, 32 * 32, 44000]
+    T, L, g = sum(counts), len(counts), torch.Generator().manual_seed(R)
+    item = 512 // (4 if dtype == "f32" else 2)
+    assert (T // 32) * (K // item + N // item) > 33 * 512      # the workgroups that share the tiles: longer than 32 each
+    dt = t.DTYPES[dtype]
+    ids = torch.repeat_interleave(torch.arange(L), torch.tensor(counts))[torch.randperm(T, generator=g)].to(torch.int32).cuda()
+    torch.manual_seed(R)
+    x, dy, h = torch.randn(T, K, device="cuda").to(dt), torch.randn(T, N, device="cuda").to(dt), torch.randn(T, R, device="cuda")
+    a, b, scale = (torch.randn(L, R, K, device="cuda") / 45).to(dt), (torch.randn(L, N, R, device="cuda") / 45).to(dt), torch.rand(L, device="cuda") + 0.5
+    _, d_a, d_b = ftq.lora_backward(dy, x, a, b, ids.view(T, 1), h, scale=scale)
+    for l, n in enumerate(counts):
+        p = (ids == l).nonzero()[:, 0]
+        xl, dl, hl, s = x[p].double(), dy[p].double(), h[p].double(), float(scale[l])
+        gl, ml = s * (dl @ b[l].double()), s * (dl.abs() @ b[l].double().abs())
+        t.close(d_a[l], gl.t().contiguous() @ xl, ml.t().contiguous() @ xl.abs(), N + n + 10, f"d_a of {n} pairs")
+        t.close(d_b[l], s * (dl.t().contiguous() @ hl), s * (dl.abs().t().contiguous() @ hl.abs()), n + 10, f"d_b of {n} pairs")
+
+
 @pytest.mark.parametrize("per_pair", [False, True])
 def test_backward_base_strides_and_parts(per_pair):
     k = 3

@@ -948,6 +948,14 @@ TileList in_order(int64_t pairs)
     return TileList{nullptr, nullptr, nullptr, 1, rows, ceil_div(pairs, rows)};
 }
 
+// The tables' plan; a tile holds a pair at least (ten pairs of 4095 adapters: ten tiles, not a partly filled one of each adapter).
+BucketPlan plan_tables(int64_t pairs, int64_t L, int64_t tile)
+{
+    BucketPlan p = make_bucket_plan(pairs, L, tile);
+    p.max_tiles = std::min(p.max_tiles, pairs);
+    return p;
+}
+
 TileList from_tables(const BucketPlan& plan, const uint8_t* mem, int64_t L, int64_t span)
 {
     return TileList{reinterpret_cast<const int32_t*>(mem + plan.off_sorted), reinterpret_cast<const int4*>(mem + plan.off_tdesc),
@@ -1048,7 +1056,7 @@ struct ForwardPlan {
 ForwardPlan plan_forward(int64_t L, int64_t R, int64_t K, int64_t pairs, int dtype, int path)
 {
     ForwardPlan p;
-    if (path == FTQ_PATH_GROUPED) p.bucket = make_bucket_plan(pairs, L, table_tile(pairs, L));
+    if (path == FTQ_PATH_GROUPED) p.bucket = plan_tables(pairs, L, table_tile(pairs, L));
     p.splits = shrink_splits(pairs, K, R, dtype);
     p.off_part = p.bucket.bytes;
     p.bytes = p.off_part + align256(p.splits * pairs * R * 4);
@@ -1065,7 +1073,7 @@ BackwardPlan plan_backward(int64_t L, int64_t R, int64_t K, int64_t N, int64_t p
 {
     BackwardPlan p;
     const int64_t es = size_of(dtype), rt = 16 * rank_tiles(R), pieces = dtype == FTQ_F32 ? 2 : 3;   // (of 16 bits)
-    p.bucket = make_bucket_plan(pairs, L, kTile);
+    p.bucket = plan_tables(pairs, L, kTile);
     p.splits = shrink_splits(pairs, N, R, dtype);
     // runs of tiles for as many workgroups as fit the chip at once (by LDS two on a CU, one of high ranks), at most a part
     // for every four tiles

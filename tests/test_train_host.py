@@ -152,3 +152,11 @@ def test_lora_takes_rows_of_any_length_below_2_31():
         assert _call("ftq_lora", LORA, kw) == ftq.ERR_UNSUPPORTED, kw
     for kw in (dict(ldx=2 ** 60), dict(ld_d=2 ** 60), dict(T=2 ** 30, ldx=2 ** 30)):
         assert _call("ftq_lora_backward", BACK, kw) == ftq.ERR_UNSUPPORTED, kw
+
+
+def test_lora_backward_workspace_of_few_pairs():
+    """Room for the tiles that there can be: pieces of at most ten tiles of 32 pairs (both sets, 6 bytes a value of 128 ranks, 24 KiB each), g and its
+    parts (10 KiB), parts of the sums of at most three runs (6 x 64 KiB), and the tables of 4096 buckets (counts, offsets, first
+    tiles, descriptors of 16 bytes)."""
+    need = ftq.lora_backward_workspace_bytes(4095, 128, 64, 64, 10, 1, torch.bfloat16)
+    assert need <= 2 * 10 * 128 * 32 * 6 + 2 * 10 * 128 * 4 + 2 * 6 * 128 * 64 * 4 + 4096 * (3 * 4 + 16) + 12 * 256

@@ -540,7 +540,8 @@ int ftq_moe_fp8_routed(const void* w, const float* w_scale, const void* a, const
  *            empty, and rows before the first and behind the last belong to none.
  *   counts   int32 [S][E], tokens int32 [S] (n_s), loss fp32 [S], written.
  *   workspace: ftq_moe_balance_workspace_bytes(T, E, top_k, S) bytes, 256-byte aligned.
- * Counts are exact; probabilities are fp32 and summed in fp32 over at most T/512
+ * Counts are exact; probabilities are fp32 (their exponentials within |x| + 2 units of 2^-24 for logits x below the
+ * row's largest, those of ftq_moe_topk's gates within 21 at any distance) and summed in fp32 over at most T/512
  * (or 1024) rows and then in fp64, in a fixed order: the same call gives the same bits.
  * A row without a finite logit has p = 0; one that holds a NaN (for softmax also +inf) makes
  * its sequence's loss NaN.  T == 0 writes zeros.  Limits: E <= 1024, top_k <= 64
@@ -565,7 +566,7 @@ int ftq_moe_balance(const void* logits, int dtype, int64_t ld, const int32_t* to
  * one expert.  Experts whose logit is -inf have gradient 0.  A row whose logits hold a NaN
  * has NaN from the balance loss, and nothing from gates if its ids name no expert.
  * Renormalised gates have their gradient relative to the largest chosen logit, so that
- * choices far below the row's largest keep theirs.  d_logits must not overlap the inputs.  At least one of d_gates
+ * choices far below the row's largest keep theirs.  Exponentials are as exact as ftq_moe_balance's.  d_logits must not overlap the inputs.  At least one of d_gates
  * and d_loss; other limits as ftq_moe_balance.  T == 0: no-op.
  */
 int ftq_moe_topk_backward(const void* logits, int dtype, int64_t ld, const int32_t* topk_ids, const float* d_gates,
@@ -605,9 +606,13 @@ int ftq_moe_combine_topk_backward(const float* d_out, const float* y, const floa
  *   h        fp32 [T*top_k][R] or NULL: written, for ftq_lora_backward.
  *   workspace: ftq_lora_workspace_bytes(...) bytes, 256-byte aligned (NULL if 0).
  *   path     FTQ_PATH_GEMV takes the pairs in their order: best when rows of an
- *            adapter lie together, as a request's do, or are few.  FTQ_PATH_GROUPED
- *            sorts them by adapter first.  FTQ_PATH_AUTO: ftq_lora_select_path,
- *            in order for top_k == 1 or few pairs, else sorted.
+ *            adapter lie together, as a long prompt's do, or are few.  A tile of 64 pairs (16 of up to 256)
+ *            is gone through once for each adapter in it.  FTQ_PATH_GROUPED sorts
+ *            the pairs by adapter first.  FTQ_PATH_AUTO: ftq_lora_select_path,
+ *            in order for top_k == 1, up to 256 pairs or L > 4095, else sorted: it goes by sizes and does not see the
+ *            ids, so that for top_k == 1 it assumes rows that lie together.  Ask for FTQ_PATH_GROUPED where more than 256 rows
+ *            mix adapters or change them every few dozen rows (512 rows of 64 adapters, 4096 x 4096, rank 16, bf16:
+ *            288 us in order, 20 sorted).
  * Products are exact to fp32's 24 bits and sums fp32 (h too), in all types; out is rounded once.  A row's bits depend neither on
  * other rows nor on the path, but for h's sums the number of parts they are split into goes by the sizes.  NaN and infinities of an
  * adapter or a row reach only the pairs that use them; what an infinity is a factor of is infinite or NaN.

@@ -1138,6 +1138,9 @@ int64_t lora_backward_workspace(int64_t L, int64_t R, int64_t K, int64_t N, int6
     return T == 0 ? 0 : plan_backward(L, R, K, N, T * top_k, dtype).bytes;
 }
 
+// In order where a tile holds few adapters: rows of requests (top_k 1), by what a call can know, or few pairs.  In order /
+// sorted, us, rank 16, 4096 x 4096, bf16: 8192 rows of 8 adapters, each one's together, 49 / 59, at random 181 / 60; 512 of
+// 64 together 92 / 19, at random 288 / 20; 256 of 8 together 16 / 21, at random 20 / 21.
 int lora_select_path(int64_t T, int64_t top_k) { return top_k == 1 || T * top_k <= 256 ? FTQ_PATH_GEMV : FTQ_PATH_GROUPED; }
 
 int run_lora(const LoraArgs& m, void* ws, int path, hipStream_t s)

@@ -540,9 +540,9 @@ int ftq_moe_fp8_routed(const void* w, const float* w_scale, const void* a, const
  *            empty, and rows before the first and behind the last belong to none.
  *   counts   int32 [S][E], tokens int32 [S] (n_s), loss fp32 [S], written.
  *   workspace: ftq_moe_balance_workspace_bytes(T, E, top_k, S) bytes, 256-byte aligned.
- * Counts are exact; probabilities are fp32 (their exponentials within |x| + 2 units of 2^-24 for logits x below the
- * row's largest, those of ftq_moe_topk's gates within 21 at any distance) and summed in fp32 over at most T/512
- * (or 1024) rows and then in fp64, in a fixed order: the same call gives the same bits.
+ * Counts are exact; probabilities are fp32 (an exponential e^-x within 1.25 x + 2 units of 2^-24, so that what is far
+ * below a row's largest is less exact than a gate of ftq_moe_topk) and summed in fp32 over at most T/512 (or 1024) rows
+ * and then in fp64, in a fixed order: the same call gives the same bits.
  * A row without a finite logit has p = 0; one that holds a NaN (for softmax also +inf) makes
  * its sequence's loss NaN.  T == 0 writes zeros.  Limits: E <= 1024, top_k <= 64
  * (FTQ_ERR_UNSUPPORTED above), S >= 1, T*top_k < 2^31, S < 2^31.

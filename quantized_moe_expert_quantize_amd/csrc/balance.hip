@@ -68,7 +68,7 @@ __device__ __forceinline__ void load_row(const void* logits, int64_t at, int sub
     }
 }
 
-// e^x for x <= 0: within |x| + 2 units of 2^-24 of its size (the rounding of the base-2 exponent), so that what is
+// e^x for x <= 0: within 1.25 |x| + 2 units of 2^-24 of its size (the base-2 exponent's and its factor's rounding), so that what is
 // far off in its own size is small beside the row's largest.  -inf gives 0, a NaN itself.
 __device__ __forceinline__ float exp_neg(float x) { return __builtin_amdgcn_exp2f(x * 1.4426950408889634f); }
 

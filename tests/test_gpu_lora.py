@@ -408,6 +408,16 @@ def test_same_bits_again():
         assert all(torch.equal(v, grads[n]) for n, v in backward(c, h).items())
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("L,T,k", [(4095, 300, 8), (4095, 7, 1), (2048, 2000, 2)])
+def test_as_many_adapters_as_a_sort_takes(L, T, k, dtype):
+    c = make(L, 8, 64, 72, T, k, dtype, "f32", per_pair=k > 1)
+    c["ids"][0, 0], c["ids"][-1, 0], c["ids"][T // 2, 0] = L - 1, 2 ** 31 - 1, -2 ** 31
+    a, b = (check_forward(c, "f32", p, k > 1) for p in PATHS)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    check_backward(c, k > 1)
+
+
 def test_offsets_past_32_bits():
     """Rows of x and out, and adapters, whose byte and element offsets pass 2^31 and 2^32."""
     L, R, K, N, T = 2, 8, 65536, 8, 33000                      # x: 2.16e9 elements

@@ -60,6 +60,19 @@ def test_loss_of_one_sequence(T, E, k, dtype, score):
 
 
 @pytest.mark.parametrize("score", [ftq.SCORE_SOFTMAX, ftq.SCORE_SIGMOID])
+@pytest.mark.parametrize("T,E,k", [(20, 1024, 64), (32, 1023, 8), (1024, 32, 64), (1025, 32, 64), (300, 28, 64)])
+def test_layouts_of_the_most_lds(T, E, k, score):
+    """Loss by one workgroup over rows of up to 1024 experts, gradients of 128 rows at a time with 64 choices each."""
+    g, logits, _ = _inputs(T, E, 1, "f32", seed=T + E)
+    ids = torch.randint(-1, E + 1, (T, k), generator=g).to(torch.int32)
+    offsets = _cuts(g, T, 4)
+    d_gates, d_loss = torch.randn(T, k, generator=g), torch.randn(4, generator=g)
+    _check_loss(logits, ids, score)
+    _check_loss(logits, ids, score, offsets)
+    _check_grad(logits, ids, score, True, 1.0, d_gates, d_loss, offsets)
+
+
+@pytest.mark.parametrize("score", [ftq.SCORE_SOFTMAX, ftq.SCORE_SIGMOID])
 @pytest.mark.parametrize("T,S,before,behind,padded", [(500, 1, 3, 70, 0.0), (700, 5, 0, 0, 0.2), (1000, 40, 5, 130, 0.1), (130, 300, 0, 0, 0.5), (64, 2, 0, 0, 1.0)])
 def test_loss_of_packed_sequences(T, S, before, behind, padded, score):
     g, logits, ids = _inputs(T, 64, 4, "f32", seed=S)
